@@ -459,6 +459,216 @@ int selscan_ssd_step(float* state, const void* x, const void* delta, const float
                      const selscan_ssd_dims_t* dims, void* stream);
 
 /*
+ * selscan_linattn_fwd — linear attention with a decay for each head: a state
+ * layer like the SSD layer, with one constant decay per head and the heads'
+ * own queries and keys.
+ *
+ * Defined by: the linear recurrence h_t = A h_{t-1} + B x_t, y_t = C h_t of
+ * "State Space Models and Mamba" (multigrid.ai), section "It is a linear
+ * recurrence", with A a scalar per head, B_t = k_t, C_t = scale q_t and
+ * x_t = v_t; and, over a chunk, the matrix form of the state space duality
+ * ("State Space Models Explained: How Mamba Works and How It Compares to
+ * Transformers" (mernstackdev.com), section "From S4 to Mamba"), whose decay
+ * mask is here lambda^(t-s). Per batch entry b and head h, with S the
+ * dk x dv state, lambda = exp(log_decay[h]), j = h / (heads / kv_heads), and
+ * len = lengths[b] (or L):
+ *   S_0 = h0[b,h] (or 0);  for t < len:
+ *   S = lambda S + k[b,t,j,:]^T v[b,t,j,:]
+ *   y[b,t,h,:] = scale * q[b,t,h,:] S
+ *   y[b,t,h,:] = 0 for len <= t < L;   last_state[b,h] = S after token len-1
+ *
+ * Arguments (device pointers):
+ *   q          : [B, L, H, dk] of dtype (token-major, as a projection writes it)
+ *   k, v       : [B, L, Hkv, dk], [B, L, Hkv, dv] of dtype; head h reads kv
+ *                head h / (H / Hkv)
+ *   log_decay  : [H] fp32, the natural logarithm of each head's decay per
+ *                token (0: nothing is forgotten; -inf: only the token itself)
+ *   y          : [B, L, H, dv] of dtype (output)
+ *   last_state : [B, H, dk, dv] fp32 output or NULL
+ * dims: H a multiple of Hkv; dk, dv multiples of 8 from 8 to 256 (else
+ * SELSCAN_ERR_DSTATE); L < 2^27; H * max(dk, dv) <= 2^20; B * H <= 2^20
+ * (2^21 for selscan_linattn_step).
+ * The state is held in fp32. bfloat16 calls round only operands of the matrix
+ * products, each kept as two (outputs) or three (states) bfloat16 terms, so
+ * that y is rounded once and the state keeps fp32 accuracy. Tokens behind an
+ * entry's length are not read. Outputs must not overlap inputs.
+ * Deterministic: the same inputs and launch choices give the same bits.
+ */
+typedef struct {
+    int64_t batch;
+    int64_t seqlen;
+    int64_t heads;
+    int64_t kv_heads;
+    int64_t dk;
+    int64_t dv;
+    int32_t dtype;
+} selscan_linattn_dims_t;
+
+/*
+ * Options of selscan_linattn_fwd (NULL: all defaults). Zero-initialise, then
+ * set what is wanted.
+ *   h0        : [B, H, dk, dv] fp32, the state entering token 0 (NULL: zeros).
+ *               It may be last_state itself; it must not overlap y.
+ *   lengths   : [B] int32, tokens of each entry (NULL: all have L); a value
+ *               below 0 counts as 0, above L as L. Must not overlap an output.
+ *   scale     : multiplies q; 0 means 1 / sqrt(dk). Finite.
+ *   segments  : runs of tokens walked in parallel (1 = one walk per head;
+ *               > 1 = the runs' own end states, their carries, then the
+ *               outputs); 0 = automatic. At most 65536; the run length is
+ *               rounded up to whole chunks. Results agree to rounding.
+ *   workspace : caller-owned device memory of workspace_bytes bytes, 256-byte
+ *               aligned, at least selscan_linattn_fwd_workspace_size(); NULL
+ *               means the library takes and returns its own on the stream.
+ *               It must not overlap any input or output.
+ */
+typedef struct {
+    const float* h0;
+    const int32_t* lengths;
+    float scale;
+    int32_t segments;
+    void* workspace;
+    uint64_t workspace_bytes;
+} selscan_linattn_opts_t;
+
+int selscan_linattn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                        void* y, float* last_state, const selscan_linattn_dims_t* dims,
+                        const selscan_linattn_opts_t* opts, void* stream);
+
+/* Bytes of workspace selscan_linattn_fwd needs (only opts->segments matters;
+ * opts may be NULL). Host only. */
+int selscan_linattn_fwd_workspace_size(const selscan_linattn_dims_t* dims,
+                                       const selscan_linattn_opts_t* opts, uint64_t* bytes);
+
+/*
+ * selscan_linattn_step — one token of the layer, the state updated in place:
+ * the recurrence of selscan_linattn_fwd for a single token ("State Space
+ * Models and Mamba" (multigrid.ai), section "Why a linear recurrence can be
+ * trained in parallel"). Per (b, h):
+ *   state[b,h] = exp(log_decay[h]) state[b,h] + k[b,j,:]^T v[b,j,:]
+ *   y[b,h,:]   = scale * q[b,h,:] state[b,h]
+ * state [B, H, dk, dv] fp32; q, y [B, H, dk], [B, H, dv]; k, v [B, Hkv, dk],
+ * [B, Hkv, dv] of dtype. dims->seqlen is ignored. scale 0 means 1 / sqrt(dk).
+ * fp32 arithmetic. y and state must not overlap any input or each other.
+ */
+int selscan_linattn_step(float* state, const void* q, const void* k, const void* v,
+                         const float* log_decay, void* y, const selscan_linattn_dims_t* dims,
+                         float scale, void* stream);
+
+/*
+ * selscan_linattn_bwd — gradients of selscan_linattn_fwd for an output
+ * gradient dy (and, with dlast_state, for the last state).
+ *
+ * Defined by: the chain rule through the recurrence. With M_t the gradient of
+ * S after token t (M = dlast_state, or 0, after the last one):
+ *   M_t = lambda M_{t+1} + scale q_t^T dy_t     (M_{len-1} = dlast_state + ...)
+ *   dq_t = scale S_t dy_t;  dk_t = M_t v_t;  dv_t = M_t^T k_t;  dh0 = lambda M_0
+ *   dlog_decay[h] = sum over b, t of scale q_t T_t dy_t, plus <dlast_state, T_len-1>,
+ *     T_t = lambda (T_{t-1} + S_{t-1}) the derivative of S_t by log_decay
+ * dk and dv of a kv head are the sums over the heads that read it. dq is thus
+ * the same walk as the forward's with (dy, v, k) in place of (q, k, v), and
+ * dk, dv are walks against time with (v, dy, q) and (k, q, dy): the states
+ * are recomputed, never stored ("Mamba: Linear-Time Sequence Modeling with
+ * Selective State Spaces" (azimuth.plus), hardware-aware algorithm).
+ *
+ * Arguments: inputs as selscan_linattn_fwd; dy [B, L, H, dv] of dtype;
+ * outputs dq [B, L, H, dk], dk [B, L, Hkv, dk], dv [B, L, Hkv, dv] of dtype
+ * (zero behind an entry's length), dlog_decay [H] fp32 or NULL (not wanted).
+ * Options: h0, lengths, scale as the forward's; dlast_state [B, H, dk, dv]
+ * fp32 (NULL: zeros); dh0 [B, H, dk, dv] fp32 output or NULL; segments and
+ * workspace as the forward's (selscan_linattn_bwd_workspace_size()).
+ * Outputs must not overlap inputs or each other. Deterministic.
+ */
+typedef struct {
+    const float* h0;
+    const int32_t* lengths;
+    const float* dlast_state;
+    float* dh0;
+    float scale;
+    int32_t segments;
+    void* workspace;
+    uint64_t workspace_bytes;
+} selscan_linattn_bwd_opts_t;
+
+int selscan_linattn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                        const void* dy, void* dq, void* dk, void* dv, float* dlog_decay,
+                        const selscan_linattn_dims_t* dims, const selscan_linattn_bwd_opts_t* opts,
+                        void* stream);
+
+/* Bytes of workspace selscan_linattn_bwd needs (only opts->segments and
+ * whether dlog_decay is wanted matter; opts may be NULL). Host only. */
+int selscan_linattn_bwd_workspace_size(const selscan_linattn_dims_t* dims,
+                                       const selscan_linattn_bwd_opts_t* opts, int32_t want_dlog_decay,
+                                       uint64_t* bytes);
+
+/*
+ * selscan_groupnorm — group norm with an activation, channels last: what
+ * stands behind the heads of a state layer, whose outputs are normalised head
+ * by head (groups = heads, spatial = 1: every token by itself) and multiplied
+ * by the block's SiLU gate branch ("State Space Models and Mamba"
+ * (multigrid.ai), section "What a Mamba block actually contains"); with
+ * spatial > 1 the usual norm of a feature map over its positions.
+ * For every n and group g, over its S positions and C / G channels:
+ *   mean = average of x,   rstd = 1 / sqrt(average of (x - mean)^2 + eps)
+ *   u[n,s,c] = (x[n,s,c] - mean[n,g]) * rstd[n,g] * weight[c] + bias[c]
+ *   y = u (SELSCAN_ACT_NONE), silu(u) (SELSCAN_ACT_SILU) or
+ *       u * silu(z[n,s,c]) (SELSCAN_ACT_GATE)
+ *
+ * Arguments (device pointers):
+ *   x, z, y      : [N, S, C] of dtype (C contiguous); z with SELSCAN_ACT_GATE,
+ *                  else NULL
+ *   weight, bias : [C] fp32 or NULL (1 and 0)
+ *   mean, rstd   : [N, G] fp32 outputs or NULL (both or neither)
+ * dims: C a multiple of G (> 0); eps >= 0 and finite. Statistics in fp32,
+ * the variance from differences to the mean. y must not overlap any input.
+ * workspace as in selscan_fwd_opts_t (selscan_groupnorm_workspace_size();
+ * opts may be NULL). Deterministic.
+ */
+#define SELSCAN_ACT_NONE 0
+#define SELSCAN_ACT_SILU 1
+#define SELSCAN_ACT_GATE 2
+typedef struct {
+    int64_t batch;    /* N */
+    int64_t spatial;  /* S */
+    int64_t channels; /* C */
+    int64_t groups;   /* G */
+    int32_t dtype;
+    int32_t act;
+    float eps;        /* ignored by selscan_groupnorm_bwd */
+} selscan_groupnorm_dims_t;
+
+typedef struct {
+    void* workspace;
+    uint64_t workspace_bytes;
+} selscan_groupnorm_opts_t;
+
+int selscan_groupnorm(const void* x, const float* weight, const float* bias, const void* z,
+                      void* y, float* mean, float* rstd, const selscan_groupnorm_dims_t* dims,
+                      const selscan_groupnorm_opts_t* opts, void* stream);
+
+/*
+ * selscan_groupnorm_bwd — gradients of selscan_groupnorm for an output
+ * gradient dy, from the mean and rstd [N, G] that the forward gave: the chain
+ * rule through its definition. With xh = (x - mean) rstd, du = dy act'(u)
+ * (dy silu(z) with the gate) and e = du * weight:
+ *   dx = rstd (e - average(e) - xh average(e xh))      (averages over the group)
+ *   dweight[c] = sum over n, s of du xh;  dbias[c] = sum of du
+ *   dz = dy u silu'(z)                                  (with the gate)
+ * dx, dz [N, S, C] of dtype; dweight, dbias [C] fp32 or NULL (not wanted).
+ * Outputs must not overlap inputs or each other. Sums in a fixed order:
+ * deterministic.
+ */
+int selscan_groupnorm_bwd(const void* x, const float* weight, const float* bias, const void* z,
+                          const void* dy, const float* mean, const float* rstd, void* dx,
+                          float* dweight, float* dbias, void* dz,
+                          const selscan_groupnorm_dims_t* dims,
+                          const selscan_groupnorm_opts_t* opts, void* stream);
+
+/* Bytes of workspace selscan_groupnorm (backward 0) or selscan_groupnorm_bwd
+ * (backward 1) needs. Host only. */
+int selscan_groupnorm_workspace_size(const selscan_groupnorm_dims_t* dims, int32_t backward,
+                                     uint64_t* bytes);
+
+/*
  * selscan_conv1d — the short causal convolution in front of the scan: a
  * depthwise conv1d of width SELSCAN_CONV_WIDTH (4), then SiLU.
  *

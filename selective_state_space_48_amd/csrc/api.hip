@@ -1,6 +1,7 @@
 // libselscan C ABI: argument checks, launch planning, workspace, launches.
 // Every check runs before the first HIP call, so argument errors are
 // reported without touching the device (and are testable without a GPU).
+#include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
 
@@ -15,6 +16,7 @@ using namespace selscan;
 
 namespace selscan {
 hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
+hipError_t launch_fill(float* p, float v, int64_t n, hipStream_t st);
 hipError_t launch_copy_f32(float* dst, const float* src, int64_t n, hipStream_t st);
 }
 
@@ -391,6 +393,115 @@ void bwd_segments(const selscan_dims_t* dims, int32_t requested, int32_t* segmen
 
 }  // namespace
 
+namespace {
+
+// Sizes of a linear-attention call, in elements.
+struct LinattnSizes {
+    int64_t q, k, v, y;  // y: also dy
+    int64_t state;       // batch * heads * dk * dv
+};
+
+int check_linattn_dims(const selscan_linattn_dims_t* d, bool step, LinattnSizes* z) {
+    if (!d) return SELSCAN_ERR_NULL;
+    if (d->batch < 0 || (!step && d->seqlen < 0) || d->heads < 0 || d->kv_heads < 0 || d->dk < 0 || d->dv < 0)
+        return SELSCAN_ERR_DIMS;
+    if (d->dtype != SELSCAN_F32 && d->dtype != SELSCAN_BF16) return SELSCAN_ERR_DTYPE;
+    if (d->dk < 8 || d->dk > 256 || d->dk % 8 || d->dv < 8 || d->dv > 256 || d->dv % 8) return SELSCAN_ERR_DSTATE;
+    if (d->heads > 0 && (d->kv_heads < 1 || d->heads % d->kv_heads)) return SELSCAN_ERR_DIMS;
+    const int64_t L = step ? 1 : d->seqlen;
+    if (L >= (int64_t(1) << 27)) return SELSCAN_ERR_DIMS;
+    // Offsets inside a chunk of tokens are 32-bit.
+    const int64_t wide = d->dk > d->dv ? d->dk : d->dv;
+    if (d->heads > (int64_t(1) << 20) || d->heads * wide > (int64_t(1) << 20)) return SELSCAN_ERR_DIMS;
+    int64_t bl, bh, t;
+    if (!mul_ok(d->batch, L, &bl) || !mul_ok(bl, d->heads * wide, &t) || !mul_ok(t, 4, &t) ||
+        !mul_ok(d->batch, d->heads, &bh) || bh > (int64_t(1) << 21) || !mul_ok(bh, d->dk * d->dv * 4, &t))
+        return SELSCAN_ERR_DIMS;
+    z->q = bl * d->heads * d->dk;
+    z->k = bl * d->kv_heads * d->dk;
+    z->v = bl * d->kv_heads * d->dv;
+    z->y = bl * d->heads * d->dv;
+    z->state = bh * d->dk * d->dv;
+    return SELSCAN_OK;
+}
+
+bool finite_f32(float v) { return v - v == 0.0f; }
+
+LinattnShape linattn_shape(const selscan_linattn_dims_t& d) {
+    return {d.batch, d.seqlen, d.heads, d.kv_heads, d.dk, d.dv,
+            d.dtype == SELSCAN_BF16 ? DType::BF16 : DType::F32};
+}
+float linattn_scale(float scale, int64_t dk) { return scale != 0.0f ? scale : float(1.0 / sqrt(double(dk))); }
+
+// Argument checks of the calls that run walks: segments, grid size.
+int linattn_make_plan(const selscan_linattn_dims_t& d, int32_t segments, bool backward, LinattnPlan* p) {
+    if (segments < 0 || segments > 65536) return SELSCAN_ERR_CONFIG;
+    *p = linattn_plan(linattn_shape(d), segments, backward);
+    // up to three walks of up to 4 column tiles per (entry, head, run), of 256
+    // threads: a grid has fewer than 2^32 threads
+    if (int64_t(p->segments) * d.batch * d.heads * 12 >= (int64_t(1) << 24)) return SELSCAN_ERR_DIMS;
+    return SELSCAN_OK;
+}
+
+// dst = src (zeros without one), in pieces: a grid has fewer than 2^32 threads.
+hipError_t pass_state(float* dst, const float* src, int64_t n, hipStream_t st) {
+    const int64_t piece = int64_t(1) << 30;
+    hipError_t e = hipSuccess;
+    for (int64_t i = 0; dst && i < n && e == hipSuccess; i += piece) {
+        const int64_t m = n - i < piece ? n - i : piece;
+        e = src ? launch_copy_f32(dst + i, src + i, m, st) : launch_fill_zero(dst + i, m, st);
+    }
+    return e;
+}
+
+// The caller's workspace, or one taken on the stream.
+struct Workspace {
+    void* p = nullptr;
+    bool own = false;
+    int take(void* given, size_t bytes, hipStream_t st) {
+        p = given;
+        if (p || !bytes) return SELSCAN_OK;
+        if (hipMallocAsync(&p, bytes, st) != hipSuccess || !p) {
+            (void)hipGetLastError();
+            return SELSCAN_ERR_ALLOC;
+        }
+        own = true;
+        return SELSCAN_OK;
+    }
+    void give_back(hipStream_t st) {
+        if (own) (void)hipFreeAsync(p, st);
+    }
+};
+
+template <size_t NI, size_t NO>
+bool any_alias(const Span (&ins)[NI], const Span (&outs)[NO]) {
+    for (size_t i = 0; i < NO; ++i) {
+        for (const Span& s : ins)
+            if (overlaps(s, outs[i])) return true;
+        for (size_t j = i + 1; j < NO; ++j)
+            if (overlaps(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+int check_groupnorm_dims(const selscan_groupnorm_dims_t* d, GroupnormShape* s) {
+    if (!d) return SELSCAN_ERR_NULL;
+    if (d->batch < 0 || d->spatial < 0 || d->channels < 0 || d->groups < 0) return SELSCAN_ERR_DIMS;
+    if (d->dtype != SELSCAN_F32 && d->dtype != SELSCAN_BF16) return SELSCAN_ERR_DTYPE;
+    if (d->act < SELSCAN_ACT_NONE || d->act > SELSCAN_ACT_GATE) return SELSCAN_ERR_CONFIG;
+    if (d->channels > 0 && (d->groups < 1 || d->channels % d->groups)) return SELSCAN_ERR_DIMS;
+    int64_t ns, n, t;
+    if (d->channels > (int64_t(1) << 24) || d->spatial >= (int64_t(1) << 31) ||
+        !mul_ok(d->batch, d->spatial, &ns) || ns > (int64_t(1) << 40) || !mul_ok(ns, d->channels, &n) ||
+        !mul_ok(n, 4, &t) || !mul_ok(d->batch, d->groups, &t) || t > INT32_MAX)
+        return SELSCAN_ERR_DIMS;
+    *s = GroupnormShape{d->batch, d->spatial, d->channels, d->groups,
+                        d->dtype == SELSCAN_BF16 ? DType::BF16 : DType::F32, d->act, d->eps};
+    return SELSCAN_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 int selscan_fwd(const void* x, const void* delta, const float* A, const void* B, const void* C,
@@ -700,6 +811,246 @@ int selscan_ssd_step(float* state, const void* x, const void* delta, const float
     SsdStepTensors tt{state, x, delta, A, B, C, D, dt_bias, y};
     const hipError_t e = launch_ssd_step(tt, dims->batch, dims->heads, dims->dstate,
                                          static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
+}
+
+int selscan_linattn_fwd_workspace_size(const selscan_linattn_dims_t* dims,
+                                       const selscan_linattn_opts_t* opts, uint64_t* bytes) {
+    if (!bytes) return SELSCAN_ERR_NULL;
+    LinattnSizes z;
+    int rc = check_linattn_dims(dims, false, &z);
+    if (rc != SELSCAN_OK) return rc;
+    LinattnPlan p;
+    rc = linattn_make_plan(*dims, opts ? opts->segments : 0, false, &p);
+    if (rc != SELSCAN_OK) return rc;
+    *bytes = z.y > 0 ? linattn_fwd_workspace_bytes(linattn_shape(*dims), p) : 0;
+    return SELSCAN_OK;
+}
+
+int selscan_linattn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                        void* y, float* last_state, const selscan_linattn_dims_t* dims,
+                        const selscan_linattn_opts_t* opts, void* stream) {
+    LinattnSizes z;
+    int rc = check_linattn_dims(dims, false, &z);
+    if (rc != SELSCAN_OK) return rc;
+    const selscan_linattn_opts_t o = opts ? *opts : selscan_linattn_opts_t{};
+    if (!finite_f32(o.scale)) return SELSCAN_ERR_CONFIG;
+    LinattnPlan plan;
+    rc = linattn_make_plan(*dims, o.segments, false, &plan);
+    if (rc != SELSCAN_OK) return rc;
+    // A tensor with no elements may come with a null pointer (torch gives one).
+    if (z.y > 0 && (!q || !k || !v || !y)) return SELSCAN_ERR_NULL;
+    if (dims->heads > 0 && !log_decay) return SELSCAN_ERR_NULL;
+    for (const void* p : {q, k, v, (const void*)log_decay, (const void*)y, (const void*)last_state,
+                          (const void*)o.h0, (const void*)o.lengths})
+        if (!aligned16(p)) return SELSCAN_ERR_ALIGN;
+    if (o.workspace && (reinterpret_cast<uintptr_t>(o.workspace) & 255u)) return SELSCAN_ERR_CONFIG;
+    const int64_t es = dims->dtype == SELSCAN_BF16 ? 2 : 4;
+    const size_t ws_bytes = z.y > 0 ? linattn_fwd_workspace_bytes(linattn_shape(*dims), plan) : 0;
+    if (o.workspace && o.workspace_bytes < ws_bytes) return SELSCAN_ERR_CONFIG;
+    const Span oy = span(y, z.y * es), os = span(last_state, z.state * 4), ih = span(o.h0, z.state * 4),
+               w = span(o.workspace, int64_t(ws_bytes));
+    const Span ins[] = {span(q, z.q * es), span(k, z.k * es), span(v, z.v * es),
+                        span(log_decay, dims->heads * 4), span(o.lengths, dims->batch * 4)};
+    const Span outs[] = {oy, os, w};
+    if (any_alias(ins, outs) || overlaps(ih, oy) || overlaps(ih, w)) return SELSCAN_ERR_ALIAS;
+    // h0 may be last_state itself (read before it is written)
+    if (overlaps(ih, os) && static_cast<const void*>(o.h0) != static_cast<const void*>(last_state))
+        return SELSCAN_ERR_ALIAS;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (z.state == 0) return SELSCAN_OK;
+    if (dims->seqlen == 0) {
+        return pass_state(last_state, o.h0, z.state, st) == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
+    }
+    LinattnTensors t{};
+    t.q = q; t.k = k; t.v = v; t.log_decay = log_decay;
+    t.lengths = o.lengths; t.h0 = o.h0; t.scale = linattn_scale(o.scale, dims->dk);
+    t.y = y; t.last_state = last_state;
+    Workspace ws;
+    rc = ws.take(o.workspace, ws_bytes, st);
+    if (rc != SELSCAN_OK) return rc;
+    const hipError_t e = launch_linattn_fwd(t, linattn_shape(*dims), plan, ws.p, st);
+    ws.give_back(st);
+    return e == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
+}
+
+int selscan_linattn_step(float* state, const void* q, const void* k, const void* v,
+                         const float* log_decay, void* y, const selscan_linattn_dims_t* dims,
+                         float scale, void* stream) {
+    LinattnSizes z;
+    const int rc = check_linattn_dims(dims, true, &z);
+    if (rc != SELSCAN_OK) return rc;
+    if (!finite_f32(scale)) return SELSCAN_ERR_CONFIG;
+    if (z.state > 0 && (!state || !q || !k || !v || !y)) return SELSCAN_ERR_NULL;
+    if (dims->heads > 0 && !log_decay) return SELSCAN_ERR_NULL;
+    for (const void* p : {(const void*)state, q, k, v, (const void*)log_decay, (const void*)y})
+        if (!aligned16(p)) return SELSCAN_ERR_ALIGN;
+    const int64_t es = dims->dtype == SELSCAN_BF16 ? 2 : 4;
+    const Span ins[] = {span(q, z.q * es), span(k, z.k * es), span(v, z.v * es),
+                        span(log_decay, dims->heads * 4)};
+    const Span outs[] = {span(state, z.state * 4), span(y, z.y * es)};
+    if (any_alias(ins, outs)) return SELSCAN_ERR_ALIAS;
+    if (z.state == 0) return SELSCAN_OK;
+    const hipError_t e = launch_linattn_step(state, q, k, v, log_decay, y, linattn_shape(*dims),
+                                             linattn_scale(scale, dims->dk), static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
+}
+
+int selscan_linattn_bwd_workspace_size(const selscan_linattn_dims_t* dims,
+                                       const selscan_linattn_bwd_opts_t* opts, int32_t want_dlog_decay,
+                                       uint64_t* bytes) {
+    if (!bytes) return SELSCAN_ERR_NULL;
+    LinattnSizes z;
+    int rc = check_linattn_dims(dims, false, &z);
+    if (rc != SELSCAN_OK) return rc;
+    LinattnPlan p;
+    rc = linattn_make_plan(*dims, opts ? opts->segments : 0, true, &p);
+    if (rc != SELSCAN_OK) return rc;
+    *bytes = z.y > 0 ? linattn_bwd_workspace_bytes(linattn_shape(*dims), p, want_dlog_decay != 0) : 0;
+    return SELSCAN_OK;
+}
+
+int selscan_linattn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                        const void* dy, void* dq, void* dk, void* dv, float* dlog_decay,
+                        const selscan_linattn_dims_t* dims, const selscan_linattn_bwd_opts_t* opts,
+                        void* stream) {
+    LinattnSizes z;
+    int rc = check_linattn_dims(dims, false, &z);
+    if (rc != SELSCAN_OK) return rc;
+    const selscan_linattn_bwd_opts_t o = opts ? *opts : selscan_linattn_bwd_opts_t{};
+    if (!finite_f32(o.scale)) return SELSCAN_ERR_CONFIG;
+    LinattnPlan plan;
+    rc = linattn_make_plan(*dims, o.segments, true, &plan);
+    if (rc != SELSCAN_OK) return rc;
+    if (z.y > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv)) return SELSCAN_ERR_NULL;
+    if (dims->heads > 0 && !log_decay) return SELSCAN_ERR_NULL;
+    for (const void* p : {q, k, v, (const void*)log_decay, dy, (const void*)dq, (const void*)dk, (const void*)dv,
+                          (const void*)dlog_decay, (const void*)o.h0, (const void*)o.lengths,
+                          (const void*)o.dlast_state, (const void*)o.dh0})
+        if (!aligned16(p)) return SELSCAN_ERR_ALIGN;
+    if (o.workspace && (reinterpret_cast<uintptr_t>(o.workspace) & 255u)) return SELSCAN_ERR_CONFIG;
+    const int64_t es = dims->dtype == SELSCAN_BF16 ? 2 : 4;
+    const size_t ws_bytes =
+        z.y > 0 ? linattn_bwd_workspace_bytes(linattn_shape(*dims), plan, dlog_decay != nullptr) : 0;
+    if (o.workspace && o.workspace_bytes < ws_bytes) return SELSCAN_ERR_CONFIG;
+    const Span ins[] = {span(q, z.q * es), span(k, z.k * es), span(v, z.v * es), span(dy, z.y * es),
+                        span(log_decay, dims->heads * 4), span(o.lengths, dims->batch * 4),
+                        span(o.h0, z.state * 4), span(o.dlast_state, z.state * 4)};
+    const Span outs[] = {span(dq, z.q * es), span(dk, z.k * es), span(dv, z.v * es),
+                         span(dlog_decay, dims->heads * 4), span(o.dh0, z.state * 4),
+                         span(o.workspace, int64_t(ws_bytes))};
+    if (any_alias(ins, outs)) return SELSCAN_ERR_ALIAS;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (z.state == 0 || dims->seqlen == 0) {  // no terms
+        if (dlog_decay && launch_fill_zero(dlog_decay, dims->heads, st) != hipSuccess) return SELSCAN_ERR_LAUNCH;
+        // the last state is h0 itself: its gradient passes straight through
+        return pass_state(o.dh0, o.dlast_state, z.state, st) == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
+    }
+    LinattnTensors t{};
+    t.q = q; t.k = k; t.v = v; t.log_decay = log_decay;
+    t.lengths = o.lengths; t.h0 = o.h0; t.scale = linattn_scale(o.scale, dims->dk);
+    t.dy = dy; t.dlast = o.dlast_state;
+    t.dq = dq; t.dk = dk; t.dv = dv; t.dlog_decay = dlog_decay; t.dh0 = o.dh0;
+    Workspace ws;
+    rc = ws.take(o.workspace, ws_bytes, st);
+    if (rc != SELSCAN_OK) return rc;
+    const hipError_t e = launch_linattn_bwd(t, linattn_shape(*dims), plan, ws.p, st);
+    ws.give_back(st);
+    return e == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
+}
+
+int selscan_groupnorm_workspace_size(const selscan_groupnorm_dims_t* dims, int32_t backward,
+                                     uint64_t* bytes) {
+    if (!bytes) return SELSCAN_ERR_NULL;
+    GroupnormShape s;
+    const int rc = check_groupnorm_dims(dims, &s);
+    if (rc != SELSCAN_OK) return rc;
+    *bytes = s.N * s.S * s.C > 0 ? groupnorm_workspace_bytes(s, backward != 0) : 0;
+    return SELSCAN_OK;
+}
+
+int selscan_groupnorm(const void* x, const float* weight, const float* bias, const void* z,
+                      void* y, float* mean, float* rstd, const selscan_groupnorm_dims_t* dims,
+                      const selscan_groupnorm_opts_t* opts, void* stream) {
+    GroupnormShape s;
+    int rc = check_groupnorm_dims(dims, &s);
+    if (rc != SELSCAN_OK) return rc;
+    if (!(s.eps >= 0.0f) || !finite_f32(s.eps)) return SELSCAN_ERR_CONFIG;
+    if ((z != nullptr) != (s.act == SELSCAN_ACT_GATE) && s.N * s.S * s.C > 0) return SELSCAN_ERR_NULL;
+    if ((mean != nullptr) != (rstd != nullptr)) return SELSCAN_ERR_NULL;
+    const int64_t n = s.N * s.S * s.C;
+    if (n > 0 && (!x || !y)) return SELSCAN_ERR_NULL;
+    const selscan_groupnorm_opts_t o = opts ? *opts : selscan_groupnorm_opts_t{};
+    for (const void* p : {x, (const void*)weight, (const void*)bias, z, (const void*)y, (const void*)mean,
+                          (const void*)rstd})
+        if (!aligned16(p)) return SELSCAN_ERR_ALIGN;
+    if (o.workspace && (reinterpret_cast<uintptr_t>(o.workspace) & 255u)) return SELSCAN_ERR_CONFIG;
+    const size_t ws_bytes = n > 0 ? groupnorm_workspace_bytes(s, false) : 0;
+    if (o.workspace && o.workspace_bytes < ws_bytes) return SELSCAN_ERR_CONFIG;
+    const int64_t es = s.dtype == DType::BF16 ? 2 : 4;
+    const Span ins[] = {span(x, n * es), span(weight, s.C * 4), span(bias, s.C * 4), span(z, n * es)};
+    const Span outs[] = {span(y, n * es), span(mean, s.N * s.G * 4), span(rstd, s.N * s.G * 4),
+                         span(o.workspace, int64_t(ws_bytes))};
+    if (any_alias(ins, outs)) return SELSCAN_ERR_ALIAS;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (n == 0) {  // no positions: the mean and the variance of nothing count as 0
+        if (mean && s.N * s.G > 0) {
+            if (launch_fill_zero(mean, s.N * s.G, st) != hipSuccess ||
+                launch_fill(rstd, 1.0f / sqrtf(s.eps), s.N * s.G, st) != hipSuccess)
+                return SELSCAN_ERR_LAUNCH;
+        }
+        return SELSCAN_OK;
+    }
+    GroupnormTensors t{};
+    t.x = x; t.weight = weight; t.bias = bias; t.z = z; t.y = y; t.mean = mean; t.rstd = rstd;
+    Workspace ws;
+    rc = ws.take(o.workspace, ws_bytes, st);
+    if (rc != SELSCAN_OK) return rc;
+    const hipError_t e = launch_groupnorm(t, s, ws.p, st);
+    ws.give_back(st);
+    return e == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
+}
+
+int selscan_groupnorm_bwd(const void* x, const float* weight, const float* bias, const void* z,
+                          const void* dy, const float* mean, const float* rstd, void* dx,
+                          float* dweight, float* dbias, void* dz,
+                          const selscan_groupnorm_dims_t* dims,
+                          const selscan_groupnorm_opts_t* opts, void* stream) {
+    GroupnormShape s;
+    int rc = check_groupnorm_dims(dims, &s);
+    if (rc != SELSCAN_OK) return rc;
+    const int64_t n = s.N * s.S * s.C;
+    const bool gate = s.act == SELSCAN_ACT_GATE;
+    if (n > 0 && (!x || !dy || !mean || !rstd || !dx)) return SELSCAN_ERR_NULL;
+    if (n > 0 && ((z != nullptr) != gate || (dz != nullptr) != gate)) return SELSCAN_ERR_NULL;
+    const selscan_groupnorm_opts_t o = opts ? *opts : selscan_groupnorm_opts_t{};
+    for (const void* p : {x, (const void*)weight, (const void*)bias, z, dy, (const void*)mean, (const void*)rstd,
+                          (const void*)dx, (const void*)dweight, (const void*)dbias, (const void*)dz})
+        if (!aligned16(p)) return SELSCAN_ERR_ALIGN;
+    if (o.workspace && (reinterpret_cast<uintptr_t>(o.workspace) & 255u)) return SELSCAN_ERR_CONFIG;
+    const size_t ws_bytes = n > 0 ? groupnorm_workspace_bytes(s, true) : 0;
+    if (o.workspace && o.workspace_bytes < ws_bytes) return SELSCAN_ERR_CONFIG;
+    const int64_t es = s.dtype == DType::BF16 ? 2 : 4;
+    const Span ins[] = {span(x, n * es), span(weight, s.C * 4), span(bias, s.C * 4), span(z, n * es),
+                        span(dy, n * es), span(mean, s.N * s.G * 4), span(rstd, s.N * s.G * 4)};
+    const Span outs[] = {span(dx, n * es), span(dweight, s.C * 4), span(dbias, s.C * 4), span(dz, n * es),
+                         span(o.workspace, int64_t(ws_bytes))};
+    if (any_alias(ins, outs)) return SELSCAN_ERR_ALIAS;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (n == 0) {  // no terms
+        if (dweight && launch_fill_zero(dweight, s.C, st) != hipSuccess) return SELSCAN_ERR_LAUNCH;
+        if (dbias && launch_fill_zero(dbias, s.C, st) != hipSuccess) return SELSCAN_ERR_LAUNCH;
+        return SELSCAN_OK;
+    }
+    GroupnormTensors t{};
+    t.x = x; t.weight = weight; t.bias = bias; t.z = z;
+    t.mean = const_cast<float*>(mean); t.rstd = const_cast<float*>(rstd);
+    t.dy = dy; t.dx = dx; t.dweight = dweight; t.dbias = dbias; t.dz = dz;
+    Workspace ws;
+    rc = ws.take(o.workspace, ws_bytes, st);
+    if (rc != SELSCAN_OK) return rc;
+    const hipError_t e = launch_groupnorm_bwd(t, s, ws.p, st);
+    ws.give_back(st);
     return e == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNCH;
 }
 

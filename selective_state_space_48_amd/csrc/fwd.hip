@@ -1448,6 +1448,11 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float* __restrict__ p, i
     if (i < n) p[i] = 0.0f;
 }
 
+__global__ __launch_bounds__(256) void fill_kernel(float* __restrict__ p, float v, int64_t n) {
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) p[i] = v;
+}
+
 __global__ __launch_bounds__(256) void copy_f32_kernel(float* __restrict__ dst,
                                                       const float* __restrict__ src, int64_t n) {
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -1457,6 +1462,12 @@ __global__ __launch_bounds__(256) void copy_f32_kernel(float* __restrict__ dst,
 }  // namespace
 
 // A fill kernel rather than a memset, so that the call stays capturable.
+hipError_t launch_fill(float* p, float v, int64_t n, hipStream_t st) {
+    if (n <= 0) return hipSuccess;
+    hipLaunchKernelGGL(fill_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st, p, v, n);
+    return hipGetLastError();
+}
+
 hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st) {
     if (n <= 0) return hipSuccess;
     hipLaunchKernelGGL(fill_zero_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st, p, n);

@@ -177,6 +177,95 @@ struct SsdStepTensors {
 hipError_t launch_ssd_step(const SsdStepTensors& t, int64_t batch, int64_t heads, int64_t dstate,
                            hipStream_t stream);
 
+// Linear attention with a decay for each head. A walk is the layer's
+// recurrence over one role of tensors, in one direction of time: with a, b of
+// width K and c, o of width P per token and head, S the K x P state,
+//   forward:  S = lambda S + b_t^T c_t;  o_t = scale a_t S       (rev false)
+//   backward: S = S + scale b_t^T c_t;   o_t = a_t S;  S = lambda S   (rev true)
+// over an entry's tokens in order (rev: from its last one on). The layer's
+// output, dq, dk and dv are the walks (q, k, v), (dy, v, k), (v, dy, q) and
+// (k, q, dy), the last two reversed.
+struct LinattnWalk {
+    const void* a;   // [batch, L, ha, K]
+    const void* b;   // [batch, L, hb, K]
+    const void* c;   // [batch, L, hc, P]
+    void* o;         // [batch, L, heads, P] (fp32 if o_f32), zero behind an entry's length
+    const float* s0; // entering state: element (n, p) of (b, h) at (b*heads + h)*K*P + n*sn + p*sp; null: 0
+    float* s1;       // leaving state, the same strides; null: not wanted
+    int32_t ha, hb, hc, K, P;
+    int32_t sn, sp;
+    bool rev, o_f32;
+};
+struct LinattnShape {
+    int64_t batch, L, heads, kv_heads, dk, dv;
+    DType dtype;
+};
+// Runs of tokens walked in parallel: `segments` runs of seg_len tokens (a
+// multiple of the chunk when segments > 1).
+struct LinattnPlan {
+    int32_t segments;
+    int64_t seg_len;
+};
+LinattnPlan linattn_plan(const LinattnShape& s, int32_t requested, bool backward);
+size_t linattn_fwd_workspace_bytes(const LinattnShape& s, const LinattnPlan& p);
+size_t linattn_bwd_workspace_bytes(const LinattnShape& s, const LinattnPlan& p, bool slope);
+
+struct LinattnTensors {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* log_decay;
+    const int32_t* lengths;  // [batch] or null
+    const float* h0;         // null: zeros
+    float scale;
+    // forward
+    void* y;
+    float* last_state;
+    // backward
+    const void* dy;
+    const float* dlast;  // null: zeros
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dlog_decay;  // null: not wanted
+    float* dh0;         // null: not wanted
+};
+hipError_t launch_linattn_fwd(const LinattnTensors& t, const LinattnShape& s, const LinattnPlan& p,
+                              void* workspace, hipStream_t stream);
+hipError_t launch_linattn_bwd(const LinattnTensors& t, const LinattnShape& s, const LinattnPlan& p,
+                              void* workspace, hipStream_t stream);
+// One token: state [batch, heads, dk, dv] fp32 in place; y [batch, heads, dv].
+hipError_t launch_linattn_step(float* state, const void* q, const void* k, const void* v,
+                               const float* log_decay, void* y, const LinattnShape& s, float scale,
+                               hipStream_t stream);
+
+// Group norm with an activation, channels last: x, z, y [N, S, C].
+struct GroupnormShape {
+    int64_t N, S, C, G;
+    DType dtype;
+    int32_t act;  // SELSCAN_ACT_*
+    float eps;
+};
+struct GroupnormTensors {
+    const void* x;
+    const float* weight;
+    const float* bias;
+    const void* z;
+    void* y;
+    float* mean;  // outputs of the forward (null: not wanted), inputs of the backward
+    float* rstd;
+    const void* dy;
+    void* dx;
+    float* dweight;
+    float* dbias;
+    void* dz;
+};
+size_t groupnorm_workspace_bytes(const GroupnormShape& s, bool backward);
+hipError_t launch_groupnorm(const GroupnormTensors& t, const GroupnormShape& s, void* workspace,
+                            hipStream_t stream);
+hipError_t launch_groupnorm_bwd(const GroupnormTensors& t, const GroupnormShape& s, void* workspace,
+                                hipStream_t stream);
+
 // Causal depthwise conv (width 4) + SiLU. x/out: [rows, L]; w: [dim, 4];
 // bias: [dim] or null; x_prev/x_last: [rows, 3] fp32 or null.
 struct ConvTensors {

@@ -11,6 +11,7 @@ x, delta, z, B, C (and y) share one dtype: float32 or bfloat16.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -59,6 +60,34 @@ class SsdDims(ctypes.Structure):
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
+class LinattnDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class LinattnOpts(ctypes.Structure):
+    _fields_ = [("h0", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("segments", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class LinattnBwdOpts(ctypes.Structure):
+    _fields_ = [("h0", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("dlast_state", ctypes.c_void_p),
+                ("dh0", ctypes.c_void_p), ("scale", ctypes.c_float), ("segments", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class GroupnormDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("spatial", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class GroupnormOpts(ctypes.Structure):
+    _fields_ = [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+
+
 class SelscanError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"libselscan error {code}: {msg}")
@@ -103,6 +132,21 @@ def _load() -> ctypes.CDLL:
     lib.selscan_ssd_fwd_ex.restype = ctypes.c_int
     lib.selscan_ssd_step.argtypes = [fp, vp, vp, fp, vp, vp, fp, fp, vp, ctypes.POINTER(SsdDims), vp]
     lib.selscan_ssd_step.restype = ctypes.c_int
+    u64_p = ctypes.POINTER(ctypes.c_uint64)
+    la_p, gn_p, gno_p = (ctypes.POINTER(t) for t in (LinattnDims, GroupnormDims, GroupnormOpts))
+    la_o, la_bo = ctypes.POINTER(LinattnOpts), ctypes.POINTER(LinattnBwdOpts)
+    lib.selscan_linattn_fwd.argtypes = [vp, vp, vp, fp, vp, fp, la_p, la_o, vp]
+    lib.selscan_linattn_fwd_workspace_size.argtypes = [la_p, la_o, u64_p]
+    lib.selscan_linattn_step.argtypes = [fp, vp, vp, vp, fp, vp, la_p, ctypes.c_float, vp]
+    lib.selscan_linattn_bwd.argtypes = [vp, vp, vp, fp, vp, vp, vp, vp, fp, la_p, la_bo, vp]
+    lib.selscan_linattn_bwd_workspace_size.argtypes = [la_p, la_bo, i32, u64_p]
+    lib.selscan_groupnorm.argtypes = [vp, fp, fp, vp, vp, fp, fp, gn_p, gno_p, vp]
+    lib.selscan_groupnorm_bwd.argtypes = [vp, fp, fp, vp, vp, fp, fp, vp, fp, fp, vp, gn_p, gno_p, vp]
+    lib.selscan_groupnorm_workspace_size.argtypes = [gn_p, i32, u64_p]
+    for f in (lib.selscan_linattn_fwd, lib.selscan_linattn_fwd_workspace_size, lib.selscan_linattn_step,
+              lib.selscan_linattn_bwd, lib.selscan_linattn_bwd_workspace_size, lib.selscan_groupnorm,
+              lib.selscan_groupnorm_bwd, lib.selscan_groupnorm_workspace_size):
+        f.restype = ctypes.c_int
     lib.selscan_conv1d.argtypes = [vp, fp, fp, fp, vp, fp, dims_p, vp]
     lib.selscan_conv1d.restype = ctypes.c_int
     lib.selscan_conv1d_step.argtypes = [fp, vp, fp, fp, vp, dims_p, vp]
@@ -481,6 +525,260 @@ def ssd_step(state: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A: torch
     _check(lib.selscan_ssd_step(_ptr(state), _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
                                 _ptr(D), _ptr(dt_bias), _ptr(y), ctypes.byref(dims), _stream(dev)))
     return y
+
+
+def _device(dev: torch.device):
+    """The device the call launches on, made current where it is not."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {dev}")
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device) -> Optional[torch.Tensor]:
+    """The caller's workspace, checked, or one of ``need`` bytes from torch's allocator (None for 0)."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    _req(workspace, "workspace", torch.uint8, None, dev)
+    return workspace
+
+
+def _scale(scale: Optional[float]) -> float:
+    """The C calls' scale: 0 stands for 1 / sqrt(dk)."""
+    if scale is None:
+        return 0.0
+    if scale == 0:
+        raise ValueError("scale must not be 0 (None: 1 / sqrt(dk))")
+    return float(scale)
+
+
+def _linattn_dims(q, k, v, L, dtype) -> "LinattnDims":
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return LinattnDims(q.shape[0], L, q.shape[-2], k.shape[-2], q.shape[-1], v.shape[-1], _DTYPES[dtype])
+
+
+def linattn_workspace_size(batch: int, L: int, heads: int, kv_heads: int, dk: int, dv: int, dtype: torch.dtype, *,
+                           segments: int = 0) -> int:
+    """Bytes of device workspace a ``linattn_fwd`` call of this shape needs."""
+    dims = LinattnDims(batch, L, heads, kv_heads, dk, dv, _DTYPES[dtype])
+    opts = LinattnOpts(None, None, 0.0, int(segments), None, 0)
+    out = ctypes.c_uint64(0)
+    _check(lib.selscan_linattn_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(out)))
+    return int(out.value)
+
+
+def linattn_bwd_workspace_size(batch: int, L: int, heads: int, kv_heads: int, dk: int, dv: int, dtype: torch.dtype,
+                               *, segments: int = 0, want_dlog_decay: bool = True) -> int:
+    """Bytes of device workspace a ``linattn_bwd`` call of this shape needs."""
+    dims = LinattnDims(batch, L, heads, kv_heads, dk, dv, _DTYPES[dtype])
+    opts = LinattnBwdOpts(None, None, None, None, 0.0, int(segments), None, 0)
+    out = ctypes.c_uint64(0)
+    _check(lib.selscan_linattn_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), int(want_dlog_decay),
+                                                  ctypes.byref(out)))
+    return int(out.value)
+
+
+def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
+                scale: Optional[float] = None, h0: Optional[torch.Tensor] = None,
+                lengths: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                last_state: Optional[torch.Tensor] = None, return_last_state: bool = True, segments: int = 0,
+                workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head (selscan_linattn_fwd). Returns (y, last_state).
+
+    ``q`` [batch, L, heads, dk]; ``k``, ``v`` [batch, L, kv_heads, dk / dv]
+    (heads a multiple of kv_heads; float32 or bfloat16); ``log_decay`` [heads]
+    fp32, the logarithm of each head's decay per token; y [batch, L, heads, dv],
+    last_state [batch, heads, dk, dv] fp32. ``h0`` (same shape) is the state
+    entering token 0 (it may be ``last_state`` itself); ``lengths`` [batch]
+    int32 the tokens of each entry (y is 0 behind them); ``scale`` multiplies q
+    (None: 1 / sqrt(dk)). ``segments`` and ``workspace`` as for ``fwd``
+    (``linattn_workspace_size``).
+    """
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [batch, L, heads, width]")
+    batch, L, H, dk = q.shape
+    Hk, dv = k.shape[2], v.shape[3]
+    dev, dt = q.device, q.dtype
+    dims = _linattn_dims(q, k, v, L, dt)
+    _req(q, "q", dt, None, dev)
+    _req(k, "k", dt, (batch, L, Hk, dk), dev)
+    _req(v, "v", dt, (batch, L, Hk, dv), dev)
+    _req(log_decay, "log_decay", torch.float32, (H,), dev)
+    _req(h0, "h0", torch.float32, (batch, H, dk, dv), dev)
+    _req(lengths, "lengths", torch.int32, (batch,), dev)
+    with _device(dev):
+        if y is None:
+            y = torch.empty((batch, L, H, dv), dtype=dt, device=dev)
+        _req(y, "y", dt, (batch, L, H, dv), dev)
+        if last_state is None and return_last_state:
+            last_state = torch.empty((batch, H, dk, dv), dtype=torch.float32, device=dev)
+        _req(last_state, "last_state", torch.float32, (batch, H, dk, dv), dev)
+        opts = LinattnOpts(_ptr(h0), _ptr(lengths), _scale(scale), int(segments), None, 0)
+        need = ctypes.c_uint64(0)
+        _check(lib.selscan_linattn_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(need)))
+        workspace = _scratch(workspace, int(need.value), dev)
+        if workspace is not None:
+            opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _check(lib.selscan_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(y), _ptr(last_state),
+                                       ctypes.byref(dims), ctypes.byref(opts), _stream(dev)))
+    return y, last_state
+
+
+def linattn_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
+                 scale: Optional[float] = None, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the layer (selscan_linattn_step): updates ``state`` [batch,
+    heads, dk, dv] fp32 in place and returns y [batch, heads, dv]. ``q`` [batch,
+    heads, dk]; ``k``, ``v`` [batch, kv_heads, dk / dv]; ``log_decay`` [heads]
+    fp32; ``scale`` as for ``linattn_fwd``."""
+    if state.dim() != 4 or q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("state must be [batch, heads, dk, dv] and q, k, v [batch, heads, width]")
+    batch, H, dk, dv = state.shape
+    dev, dt, Hk = state.device, q.dtype, k.shape[1]
+    _req(state, "state", torch.float32, (batch, H, dk, dv), dev)
+    _req(q, "q", dt, (batch, H, dk), dev)
+    _req(k, "k", dt, (batch, Hk, dk), dev)
+    _req(v, "v", dt, (batch, Hk, dv), dev)
+    _req(log_decay, "log_decay", torch.float32, (H,), dev)
+    dims = _linattn_dims(q, k, v, 1, dt)
+    with _device(dev):
+        if y is None:
+            y = torch.empty((batch, H, dv), dtype=dt, device=dev)
+        _req(y, "y", dt, (batch, H, dv), dev)
+        _check(lib.selscan_linattn_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(y),
+                                        ctypes.byref(dims), _scale(scale), _stream(dev)))
+    return y
+
+
+def linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *, dy: torch.Tensor,
+                scale: Optional[float] = None, h0: Optional[torch.Tensor] = None,
+                lengths: Optional[torch.Tensor] = None, dlast_state: Optional[torch.Tensor] = None,
+                want_dlog_decay: bool = True, want_dh0: bool = False, segments: int = 0,
+                workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``linattn_fwd`` (selscan_linattn_bwd) for ``dy`` [batch, L,
+    heads, dv] and, when given, ``dlast_state`` (the gradient into last_state).
+
+    Returns a dict with dq, dk, dv (like q, k, v; 0 behind an entry's length),
+    dlog_decay [heads] fp32 and dh0 [batch, heads, dk, dv] fp32 when wanted.
+    ``workspace``: at least ``linattn_bwd_workspace_size(...)`` bytes.
+    """
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [batch, L, heads, width]")
+    batch, L, H, dk = q.shape
+    Hk, dv = k.shape[2], v.shape[3]
+    dev, dt = q.device, q.dtype
+    dims = _linattn_dims(q, k, v, L, dt)
+    state = (batch, H, dk, dv)
+    for t, name, tt, shape in ((q, "q", dt, None), (k, "k", dt, (batch, L, Hk, dk)), (v, "v", dt, (batch, L, Hk, dv)),
+                               (dy, "dy", dt, (batch, L, H, dv)), (log_decay, "log_decay", torch.float32, (H,)),
+                               (h0, "h0", torch.float32, state), (dlast_state, "dlast_state", torch.float32, state),
+                               (lengths, "lengths", torch.int32, (batch,))):
+        _req(t, name, tt, shape, dev)
+    with _device(dev):
+        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
+        if want_dlog_decay:
+            out["dlog_decay"] = torch.empty_like(log_decay)
+        if want_dh0:
+            out["dh0"] = torch.empty(state, dtype=torch.float32, device=dev)
+        opts = LinattnBwdOpts(_ptr(h0), _ptr(lengths), _ptr(dlast_state), _ptr(out.get("dh0")), _scale(scale),
+                              int(segments), None, 0)
+        need = ctypes.c_uint64(0)
+        _check(lib.selscan_linattn_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), int(want_dlog_decay),
+                                                      ctypes.byref(need)))
+        workspace = _scratch(workspace, int(need.value), dev)
+        if workspace is not None:
+            opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _check(lib.selscan_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(dy), _ptr(out["dq"]),
+                                       _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out.get("dlog_decay")),
+                                       ctypes.byref(dims), ctypes.byref(opts), _stream(dev)))
+    return out
+
+
+ACTS = {"none": 0, "silu": 1, "gate": 2}
+
+
+def _groupnorm_dims(x: torch.Tensor, groups: int, act: str, eps: float) -> "GroupnormDims":
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [rows, channels] or [batch, spatial, channels]")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    spatial = x.shape[1] if x.dim() == 3 else 1
+    return GroupnormDims(x.shape[0], spatial, x.shape[-1], int(groups), _DTYPES[x.dtype], ACTS[act], float(eps))
+
+
+def _groupnorm_workspace(dims, backward: bool, workspace, dev) -> Tuple[Optional[torch.Tensor], "GroupnormOpts"]:
+    need = ctypes.c_uint64(0)
+    _check(lib.selscan_groupnorm_workspace_size(ctypes.byref(dims), int(backward), ctypes.byref(need)))
+    workspace = _scratch(workspace, int(need.value), dev)
+    return workspace, GroupnormOpts(None, 0) if workspace is None else GroupnormOpts(workspace.data_ptr(),
+                                                                                     workspace.numel())
+
+
+def groupnorm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+              bias: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None, *, act: str = "none",
+              eps: float = 1e-5, y: Optional[torch.Tensor] = None, return_stats: bool = True,
+              workspace: Optional[torch.Tensor] = None
+              ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Group norm with an activation, channels last (selscan_groupnorm). Returns (y, mean, rstd).
+
+    ``x`` [rows, channels] (each row by itself) or [batch, spatial, channels]
+    (over all positions of an entry), float32 or bfloat16; ``weight``, ``bias``
+    [channels] fp32. ``act``: "none", "silu" (of the normed value) or "gate"
+    (times silu(z), ``z`` like x). mean and rstd [rows, groups] fp32 are what
+    ``groupnorm_bwd`` needs (None with ``return_stats=False``).
+    """
+    dims = _groupnorm_dims(x, groups, act, eps)
+    dev, dt, C = x.device, x.dtype, x.shape[-1]
+    _req(x, "x", dt, None, dev)
+    _req(weight, "weight", torch.float32, (C,), dev)
+    _req(bias, "bias", torch.float32, (C,), dev)
+    if (z is None) != (act != "gate"):
+        raise ValueError('z belongs to act="gate", and to it alone')
+    _req(z, "z", dt, x.shape, dev)
+    with _device(dev):
+        if y is None:
+            y = torch.empty_like(x)
+        _req(y, "y", dt, x.shape, dev)
+        mean = rstd = None
+        if return_stats:
+            mean, rstd = (torch.empty((x.shape[0], int(groups)), dtype=torch.float32, device=dev) for _ in range(2))
+        workspace, opts = _groupnorm_workspace(dims, False, workspace, dev)
+        _check(lib.selscan_groupnorm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ptr(y), _ptr(mean), _ptr(rstd),
+                                     ctypes.byref(dims), ctypes.byref(opts), _stream(dev)))
+    return y, mean, rstd
+
+
+def groupnorm_bwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None, *, act: str = "none",
+                  dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, want_dweight: bool = True,
+                  want_dbias: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``groupnorm`` (selscan_groupnorm_bwd) for ``dy``, from the
+    ``mean`` and ``rstd`` that it returned: a dict with dx (like x), dweight and
+    dbias [channels] fp32 when wanted, and dz (like z) with the gate."""
+    dims = _groupnorm_dims(x, groups, act, 0.0)
+    dev, dt, C = x.device, x.dtype, x.shape[-1]
+    stats = (x.shape[0], int(groups))
+    if (z is None) != (act != "gate"):
+        raise ValueError('z belongs to act="gate", and to it alone')
+    for t, name, tt, shape in ((x, "x", dt, None), (weight, "weight", torch.float32, (C,)),
+                               (bias, "bias", torch.float32, (C,)), (z, "z", dt, x.shape), (dy, "dy", dt, x.shape),
+                               (mean, "mean", torch.float32, stats), (rstd, "rstd", torch.float32, stats)):
+        _req(t, name, tt, shape, dev)
+    with _device(dev):
+        out = {"dx": torch.empty_like(x)}
+        if want_dweight:
+            out["dweight"] = torch.empty((C,), dtype=torch.float32, device=dev)
+        if want_dbias:
+            out["dbias"] = torch.empty((C,), dtype=torch.float32, device=dev)
+        if z is not None:
+            out["dz"] = torch.empty_like(z)
+        workspace, opts = _groupnorm_workspace(dims, True, workspace, dev)
+        _check(lib.selscan_groupnorm_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ptr(dy), _ptr(mean),
+                                         _ptr(rstd), _ptr(out["dx"]), _ptr(out.get("dweight")),
+                                         _ptr(out.get("dbias")), _ptr(out.get("dz")), ctypes.byref(dims),
+                                         ctypes.byref(opts), _stream(dev)))
+    return out
 
 
 CONV_WIDTH = 4

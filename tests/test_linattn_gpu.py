@@ -1,0 +1,386 @@
+"""Linear attention with a decay for each head on the GPU against its 64-bit
+definition: prompts, single tokens and gradients over head layouts, widths,
+lengths, decays and runs; padding, streams, graphs, offsets past 2^31.
+Tolerances: tests/linattn_util.py."""
+import numpy as np
+import pytest
+import torch
+
+from linattn_util import DT, bwd_ref, close, fwd_ref, host, make, relative
+from oracle import linattn as ref
+from selective_state_space_48_amd import selscan
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [
+    # (batch, L, heads, kv_heads, dk, dv)
+    (1, 1, 1, 1, 8, 8),
+    (2, 31, 2, 2, 32, 32),
+    (1, 32, 3, 1, 16, 40),
+    (2, 63, 3, 3, 64, 64),
+    (1, 64, 2, 1, 64, 128),
+    (2, 65, 4, 2, 128, 64),
+    (1, 130, 2, 2, 72, 104),
+    (1, 257, 2, 2, 128, 128),
+    (1, 97, 2, 1, 256, 256),
+    (1, 40, 2, 2, 256, 8),
+    (1, 70, 1, 1, 8, 248),
+]
+DTYPES = ["f32", "bf16"]
+
+
+def case(msg):
+    print(f"[case] {msg}", flush=True)
+
+
+def fwd(p, **kw):
+    y, s = selscan.linattn_fwd(p["q"], p["k"], p["v"], p["log_decay"], h0=p["h0"], lengths=p["lengths"], **kw)
+    torch.cuda.synchronize()
+    return y, s
+
+
+def bwd(p, **kw):
+    r = selscan.linattn_bwd(p["q"], p["k"], p["v"], p["log_decay"], dy=p["dy"], h0=p["h0"], lengths=p["lengths"],
+                            dlast_state=p["dlast"], want_dh0=True, **kw)
+    torch.cuda.synchronize()
+    return r
+
+
+def sizes(p):
+    return p["q"].shape[1], p["q"].shape[3], p["v"].shape[3]
+
+
+def check_fwd(p, what, scale=None, **kw):
+    y, s = fwd(p, scale=scale, **kw)
+    ry, rs, ya, sa = fwd_ref(p, scale)
+    c = relative(p["q"].dtype, *sizes(p))
+    close(y, ry, ya, y.dtype, c, what + " y")
+    # the state keeps fp32 accuracy for both types of input
+    close(s, rs, sa, s.dtype, relative(torch.float32, *sizes(p)), what + " state")
+
+
+def check_bwd(p, what, scale=None, **kw):
+    r = bwd(p, scale=scale, **kw)
+    want, size = bwd_ref(p, scale)
+    L, dk, dv = sizes(p)
+    c = relative(p["q"].dtype, L, dk, dv)
+    for name in want:
+        cc = relative(torch.float32, L, dk, dv) if name == "dh0" else c
+        if name == "dlog_decay":  # summed over every token, key and value: as many more additions
+            cc = c + (L + p["q"].shape[0] * 8) * 2.0 ** -24
+        close(r[name], want[name], size[name], r[name].dtype, cc, f"{what} {name}")
+
+
+def ragged(B, L):
+    return [L, 0, 1, L // 2][:B] if B > 1 else [max(1, L - 3)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_prompt(shape, dtype):
+    for h0, lengths in ((False, None), (True, ragged(shape[0], shape[1]))):
+        case(f"prompt {shape} {dtype} h0={h0} lengths={lengths}")
+        check_fwd(make(*shape, DT[dtype], seed=1, h0=h0, lengths=lengths), f"{shape} {dtype} {lengths}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_gradients(shape, dtype):
+    for h0, lengths in ((False, None), (True, ragged(shape[0], shape[1]))):
+        case(f"gradients {shape} {dtype} h0={h0} lengths={lengths}")
+        check_bwd(make(*shape, DT[dtype], seed=2, h0=h0, lengths=lengths, grads=True), f"{shape} {dtype} {lengths}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segments", [1, 2, 3, 7, 64])
+def test_runs_of_tokens(segments, dtype):
+    """The sequence cut into runs; entries that end before, inside and at the ends of runs."""
+    p = make(4, 300, 4, 2, 64, 96, DT[dtype], seed=3, h0=True, lengths=[300, 129, 64, 0], grads=True)
+    case(f"segments {segments} {dtype}")
+    check_fwd(p, f"segments {segments} {dtype}", segments=segments)
+    check_bwd(p, f"segments {segments} {dtype}", segments=segments)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_long_automatic(dtype):
+    """Few heads and many tokens: the automatic plan cuts the sequence."""
+    p = make(1, 1500, 2, 1, 32, 64, DT[dtype], seed=4, h0=True, grads=True)
+    case(f"long {dtype}")
+    check_fwd(p, f"long {dtype}")
+    check_bwd(p, f"long {dtype}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decays(dtype):
+    """Heads that forget nothing, everything, nearly everything, and one that grows."""
+    decay = torch.tensor([0.0, float("-inf"), -40.0, -0.7, 0.02])
+    p = make(2, 150, 5, 5, 32, 32, DT[dtype], seed=5, h0=True, grads=True, lengths=[150, 70], decay=decay)
+    for segments in (1, 2):
+        case(f"decays {dtype} segments={segments}")
+        check_fwd(p, f"decays {dtype} {segments}", segments=segments)
+        check_bwd(p, f"decays {dtype} {segments}", segments=segments)
+
+
+@pytest.mark.parametrize("scale", [1.0, -0.3])
+def test_scale(scale):
+    p = make(1, 75, 2, 2, 48, 64, torch.bfloat16, seed=6, h0=True, grads=True)
+    case(f"scale {scale}")
+    check_fwd(p, f"scale {scale}", scale=scale)
+    check_bwd(p, f"scale {scale}", scale=scale)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1, 1, 1, 8, 8), (3, 4, 2, 64, 64), (2, 6, 6, 128, 128), (5, 2, 1, 256, 200),
+                                   (1, 3, 3, 72, 104), (300, 2, 2, 64, 128)])
+def test_token(shape, dtype):
+    B, H, Hk, dk, dv = shape
+    p = make(B, 1, H, Hk, dk, dv, DT[dtype], seed=7, h0=True)
+    case(f"token {shape} {dtype}")
+    state = p["h0"].clone()
+    y = selscan.linattn_step(state, p["q"][:, 0], p["k"][:, 0], p["v"][:, 0], p["log_decay"])
+    torch.cuda.synchronize()
+    ry, rs, ya, sa = fwd_ref(p)
+    c = relative(torch.float32, 1, dk, dv)
+    close(y, ry[:, 0], ya[:, 0], y.dtype, c, f"token {shape} {dtype} y")
+    close(state, rs, sa, state.dtype, c, f"token {shape} {dtype} state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prompt_then_tokens(dtype):
+    """A prompt, then single tokens from its state: the whole sequence's outputs."""
+    B, L, T, H, Hk, dk, dv = 2, 67, 5, 4, 2, 64, 64
+    p = make(B, L + T, H, Hk, dk, dv, DT[dtype], seed=8)
+    case(f"prompt then tokens {dtype}")
+    cut = lambda a, b: {n: p[n][:, a:b].contiguous() for n in "qkv"}  # noqa: E731
+    a = cut(0, L)
+    y, state = selscan.linattn_fwd(a["q"], a["k"], a["v"], p["log_decay"])
+    ys = [y]
+    for t in range(L, L + T):
+        a = cut(t, t + 1)
+        ys.append(selscan.linattn_step(state, a["q"][:, 0], a["k"][:, 0], a["v"][:, 0], p["log_decay"])[:, None])
+    torch.cuda.synchronize()
+    ry, rs, ya, sa = fwd_ref(p)
+    close(torch.cat(ys, 1), ry, ya, DT[dtype], relative(DT[dtype], L + T, dk, dv), f"prompt then tokens {dtype}")
+    close(state, rs, sa, torch.float32, relative(torch.float32, L + T, dk, dv), f"prompt then tokens {dtype} state")
+
+
+def test_split_in_place():
+    """A sequence in two calls, the state passed on in its own buffer (h0 is last_state)."""
+    p = make(2, 150, 3, 3, 64, 64, torch.bfloat16, seed=9)
+    case("split, state in place")
+    state = torch.zeros(2, 3, 64, 64, device="cuda")
+    ys = []
+    for a, b in ((0, 77), (77, 150)):
+        x = {n: p[n][:, a:b].contiguous() for n in "qkv"}
+        ys.append(selscan.linattn_fwd(x["q"], x["k"], x["v"], p["log_decay"], h0=state, last_state=state)[0])
+    torch.cuda.synchronize()
+    ry, rs, ya, sa = fwd_ref(p)
+    close(torch.cat(ys, 1), ry, ya, torch.bfloat16, relative(torch.bfloat16, 150, 64, 64), "split y")
+    close(state, rs, sa, torch.float32, relative(torch.float32, 150, 64, 64), "split state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segments", [1, 3])
+def test_padding_is_not_read(dtype, segments):
+    """NaN and infinities behind an entry's length, and in another entry and head, reach nothing else."""
+    p = make(3, 140, 4, 2, 64, 64, DT[dtype], seed=10, h0=True, lengths=[140, 70, 0], grads=True)
+    for n in ("q", "k", "v", "dy"):
+        p[n][1, 70:] = float("nan")
+        p[n][2] = float("inf")
+    case(f"NaN behind the lengths {dtype} segments={segments}")
+    clean = {k: None if t is None else t.clone() for k, t in p.items()}
+    for n in ("q", "k", "v", "dy"):
+        clean[n][1, 70:] = 0
+        clean[n][2] = 0
+    for a, b in zip(fwd(p, segments=segments), fwd(clean, segments=segments)):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+    r, c = bwd(p, segments=segments), bwd(clean, segments=segments)
+    for n in r:
+        assert torch.equal(r[n], c[n]) and torch.isfinite(r[n]).all(), n
+    y, _ = fwd(p, segments=segments)
+    assert (y[1, 70:] == 0).all() and (y[2] == 0).all()
+    case("NaN in one head")
+    clean["k"][0, 5, 0] = float("nan")  # read by heads 0 and 1 of entry 0 alone
+    y, s = fwd(clean, segments=segments)
+    assert torch.isnan(y[0, 5:, :2]).all() and torch.isfinite(y[0, :5]).all()
+    assert torch.isfinite(y[0, :, 2:]).all() and torch.isfinite(y[1:]).all() and torch.isfinite(s[1:]).all()
+
+
+def test_lengths_out_of_range_are_clamped():
+    p = make(3, 50, 2, 2, 32, 32, torch.float32, seed=11, grads=True)
+    case("lengths -5, 50, 99")
+    p["lengths"] = torch.tensor([-5, 50, 99], dtype=torch.int32, device="cuda")
+    q = dict(p, lengths=torch.tensor([0, 50, 50], dtype=torch.int32, device="cuda"))
+    for a, b in zip(fwd(p), fwd(q)):
+        assert torch.equal(a, b)
+    r, c = bwd(p), bwd(q)
+    assert all(torch.equal(r[n], c[n]) for n in r)
+
+
+def test_empty():
+    case("no tokens, no entries, no heads")
+    p = make(2, 0, 3, 3, 32, 16, torch.bfloat16, h0=True, grads=True)
+    y, s = fwd(p)
+    assert y.shape == (2, 0, 3, 16) and torch.equal(s, p["h0"])
+    r = bwd(p)
+    assert (r["dlog_decay"] == 0).all() and torch.equal(r["dh0"], p["dlast"])
+    p["h0"] = p["dlast"] = None
+    assert (fwd(p)[1] == 0).all() and (bwd(p)["dh0"] == 0).all()
+    p = make(0, 5, 3, 3, 32, 16, torch.bfloat16, grads=True)
+    assert fwd(p)[0].shape == (0, 5, 3, 16)
+    assert (bwd(p)["dlog_decay"] == 0).all()
+    state = torch.empty(0, 3, 32, 16, device="cuda")
+    e = torch.empty(0, 3, 32, device="cuda"), torch.empty(0, 3, 16, device="cuda")
+    assert selscan.linattn_step(state, e[0], e[0], e[1], p["log_decay"]).shape == (0, 3, 16)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_deterministic_and_workspace(dtype):
+    p = make(2, 260, 4, 2, 64, 64, DT[dtype], seed=12, h0=True, grads=True)
+    case(f"determinism, the caller's workspace {dtype}")
+    a, b = fwd(p, segments=2), bwd(p, segments=2)
+    shape = (2, 260, 4, 2, 64, 64, DT[dtype])
+    nf, nb = selscan.linattn_workspace_size(*shape, segments=2), selscan.linattn_bwd_workspace_size(*shape, segments=2)
+    wf, wb = (torch.full((n + 64,), 0xFF, dtype=torch.uint8, device="cuda") for n in (nf, nb))
+    c, d = fwd(p, segments=2, workspace=wf[:nf]), bwd(p, segments=2, workspace=wb[:nb])
+    assert (wf[nf:] == 0xFF).all() and (wb[nb:] == 0xFF).all()
+    assert all(torch.equal(x, y) for x, y in zip(a, c)) and all(torch.equal(b[n], d[n]) for n in b)
+
+
+def test_optional_outputs():
+    p = make(2, 80, 4, 2, 32, 64, torch.bfloat16, seed=13, h0=True, grads=True)
+    case("without last_state, dlog_decay, dh0")
+    y, s = fwd(p, return_last_state=False)
+    assert s is None and torch.equal(y, fwd(p)[0])
+    r = selscan.linattn_bwd(p["q"], p["k"], p["v"], p["log_decay"], dy=p["dy"], h0=p["h0"], dlast_state=p["dlast"],
+                            want_dlog_decay=False)
+    c = bwd(p)
+    assert sorted(r) == ["dk", "dq", "dv"] and all(torch.equal(r[n], c[n]) for n in r)
+
+
+def test_gradients_against_differences():
+    """The kernels' gradients along a direction against central differences of the 64-bit forward."""
+    p = make(2, 90, 4, 2, 32, 48, torch.float32, seed=14, h0=True, lengths=[90, 41], grads=True)
+    case("gradients against differences")
+    r = {k: t.double().cpu().numpy() for k, t in bwd(p).items()}
+    h = host(p)
+    rng = np.random.default_rng(15)
+
+    def loss(b):
+        y, s = ref.linattn(b["q"], b["k"], b["v"], b["log_decay"], None, b["h0"], b["lengths"])
+        return (y * h["dy"]).sum() + (s * h["dlast"]).sum()
+
+    size = bwd_ref(p)[1]
+    for name, x in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dlog_decay", "log_decay"), ("dh0", "h0")):
+        d = rng.standard_normal(h[x].shape)
+        e = 1e-6
+        diff = (loss(dict(h, **{x: h[x] + e * d})) - loss(dict(h, **{x: h[x] - e * d}))) / (2 * e)
+        room = relative(torch.float32, 90, 32, 48) * (size[name] * np.abs(d)).sum() + 1e-7 * abs(diff) + 1e-4
+        assert abs(diff - (r[name] * d).sum()) <= room, (name, diff, (r[name] * d).sum(), room)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_graph(dtype):
+    """Prompt, token and gradients captured into one graph each and replayed among eager work."""
+    p = make(2, 200, 4, 2, 64, 64, DT[dtype], seed=16, h0=True, grads=True, lengths=[200, 90])
+    case(f"graph {dtype}")
+    new = make(2, 200, 4, 2, 64, 64, DT[dtype], seed=17, h0=True, grads=True)
+    names = ("q", "k", "v", "dy", "h0")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        fwd(p, segments=2), bwd(p, segments=2)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    state = p["h0"].clone()
+    tok = [p[n][:, 3].contiguous() for n in "qkv"]
+    for f in (lambda: fwd_(p), lambda: bwd_(p), lambda: {"y": selscan.linattn_step(state, *tok, p["log_decay"])}):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for turn in range(4):
+        src = new if turn % 2 else p
+        vals = {n: (new if turn % 2 else make(2, 200, 4, 2, 64, 64, DT[dtype], seed=18 + turn, h0=True, grads=True))[n]
+                for n in names}
+        for n in names:
+            p[n].copy_(vals[n])
+        for t, n in zip(tok, "qkv"):
+            t.copy_(p[n][:, 3])
+        state.copy_(p["h0"])
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        got = [{k: t.clone() for k, t in o.items()} for o in outs] + [{"state": state.clone()}]
+        st = p["h0"].clone()
+        want = [fwd_(p), bwd_(p), {"y": selscan.linattn_step(st, *tok, p["log_decay"])}, {"state": st}]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for k in b:
+                assert torch.equal(a[k], b[k]), f"replay {turn} {k}"
+        del src
+
+
+def fwd_(p):
+    y, s = selscan.linattn_fwd(p["q"], p["k"], p["v"], p["log_decay"], h0=p["h0"], lengths=p["lengths"], segments=2)
+    return {"y": y, "s": s}
+
+
+def bwd_(p):
+    return selscan.linattn_bwd(p["q"], p["k"], p["v"], p["log_decay"], dy=p["dy"], h0=p["h0"], lengths=p["lengths"],
+                               dlast_state=p["dlast"], want_dh0=True, segments=2)
+
+
+def test_side_stream_and_two_calls_at_once():
+    p = make(2, 300, 8, 8, 64, 64, torch.bfloat16, seed=20, h0=True, grads=True)
+    o = make(2, 300, 8, 8, 64, 64, torch.bfloat16, seed=21, h0=True, grads=True)
+    case("two streams")
+    want = [fwd_(p), bwd_(p), fwd_(o), bwd_(o)]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(2):
+        with torch.cuda.stream(s1):
+            a = [fwd_(p), bwd_(p)]
+        with torch.cuda.stream(s2):
+            b = [fwd_(o), bwd_(o)]
+        got.append(a + b)
+    torch.cuda.synchronize()
+    for g in got:
+        for x, y in zip(g, want):
+            assert all(torch.equal(x[k], y[k]) for k in y)
+
+
+def test_offsets_past_2_31():
+    """More than 2^31 elements in every tensor: the last entry, against a call on it alone."""
+    B, L, H, d = 9, 65536, 32, 128
+    case(f"offsets past 2^31: b{B} L{L} H{H} d{d}")
+    g = torch.Generator(device="cuda").manual_seed(22)
+    q, k, v, dy = (torch.empty((B, L, H, d), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+                   for _ in range(4))
+    assert q.numel() > 2 ** 31
+    dec = torch.full((H,), -0.01, device="cuda")
+    y, s = selscan.linattn_fwd(q, k, v, dec, segments=8)
+    r = selscan.linattn_bwd(q, k, v, dec, dy=dy, segments=8, want_dlog_decay=False, want_dh0=True)
+    torch.cuda.synchronize()
+    one = [t[B - 1:].contiguous() for t in (q, k, v, dy)]
+    y1, s1 = selscan.linattn_fwd(*one[:3], dec, segments=8)
+    r1 = selscan.linattn_bwd(*one[:3], dec, dy=one[3], segments=8, want_dlog_decay=False, want_dh0=True)
+    torch.cuda.synchronize()
+    assert torch.equal(y[B - 1:], y1) and torch.equal(s[B - 1:], s1)
+    for n in r:
+        assert torch.equal(r[n][B - 1:], r1[n]), n
+
+
+def test_token_offsets_past_2_31():
+    B, H, d = 4200, 32, 128
+    case(f"state offsets past 2^31: b{B} H{H} d{d}")
+    g = torch.Generator(device="cuda").manual_seed(23)
+    state = torch.empty((B, H, d, d), device="cuda").normal_(generator=g)
+    assert state.numel() > 2 ** 31
+    q, k, v = (torch.empty((B, H, d), dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(3))
+    dec = torch.full((H,), -0.01, device="cuda")
+    s1, one = state[B - 1:].clone(), [t[B - 1:].contiguous() for t in (q, k, v)]
+    y = selscan.linattn_step(state, q, k, v, dec)
+    y1 = selscan.linattn_step(s1, *one, dec)
+    torch.cuda.synchronize()
+    assert torch.equal(y[B - 1:], y1) and torch.equal(state[B - 1:], s1)
