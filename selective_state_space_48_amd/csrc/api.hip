@@ -484,7 +484,7 @@ bool any_alias(const Span (&ins)[NI], const Span (&outs)[NO]) {
     return false;
 }
 
-int check_groupnorm_dims(const selscan_groupnorm_dims_t* d, GroupnormShape* s) {
+int check_groupnorm_dims(const selscan_groupnorm_dims_t* d, bool backward, GroupnormShape* s) {
     if (!d) return SELSCAN_ERR_NULL;
     if (d->batch < 0 || d->spatial < 0 || d->channels < 0 || d->groups < 0) return SELSCAN_ERR_DIMS;
     if (d->dtype != SELSCAN_F32 && d->dtype != SELSCAN_BF16) return SELSCAN_ERR_DTYPE;
@@ -497,6 +497,7 @@ int check_groupnorm_dims(const selscan_groupnorm_dims_t* d, GroupnormShape* s) {
         return SELSCAN_ERR_DIMS;
     *s = GroupnormShape{d->batch, d->spatial, d->channels, d->groups,
                         d->dtype == SELSCAN_BF16 ? DType::BF16 : DType::F32, d->act, d->eps};
+    if (!groupnorm_fits(*s, backward)) return SELSCAN_ERR_DIMS;
     return SELSCAN_OK;
 }
 
@@ -963,7 +964,7 @@ int selscan_groupnorm_workspace_size(const selscan_groupnorm_dims_t* dims, int32
                                      uint64_t* bytes) {
     if (!bytes) return SELSCAN_ERR_NULL;
     GroupnormShape s;
-    const int rc = check_groupnorm_dims(dims, &s);
+    const int rc = check_groupnorm_dims(dims, backward != 0, &s);
     if (rc != SELSCAN_OK) return rc;
     *bytes = s.N * s.S * s.C > 0 ? groupnorm_workspace_bytes(s, backward != 0) : 0;
     return SELSCAN_OK;
@@ -973,7 +974,7 @@ int selscan_groupnorm(const void* x, const float* weight, const float* bias, con
                       void* y, float* mean, float* rstd, const selscan_groupnorm_dims_t* dims,
                       const selscan_groupnorm_opts_t* opts, void* stream) {
     GroupnormShape s;
-    int rc = check_groupnorm_dims(dims, &s);
+    int rc = check_groupnorm_dims(dims, false, &s);
     if (rc != SELSCAN_OK) return rc;
     if (!(s.eps >= 0.0f) || !finite_f32(s.eps)) return SELSCAN_ERR_CONFIG;
     if ((z != nullptr) != (s.act == SELSCAN_ACT_GATE) && s.N * s.S * s.C > 0) return SELSCAN_ERR_NULL;
@@ -1017,7 +1018,7 @@ int selscan_groupnorm_bwd(const void* x, const float* weight, const float* bias,
                           const selscan_groupnorm_dims_t* dims,
                           const selscan_groupnorm_opts_t* opts, void* stream) {
     GroupnormShape s;
-    int rc = check_groupnorm_dims(dims, &s);
+    int rc = check_groupnorm_dims(dims, true, &s);
     if (rc != SELSCAN_OK) return rc;
     const int64_t n = s.N * s.S * s.C;
     const bool gate = s.act == SELSCAN_ACT_GATE;

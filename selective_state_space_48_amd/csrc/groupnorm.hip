@@ -1,4 +1,15 @@
-// Group norm with an activation, channels last, and its gradients.
+// Group norm with an activation, channels last, and its gradients. Bound by
+// memory: x (and z) is read once and y written once where an instance (the
+// S x D values of one n and group, D = C / G) fits the registers of a
+// workgroup; else statistics are formed by slabs of rows first and the slabs
+// read again. Three kernels, by the shape of an instance:
+//   rows  (S = 1, D up to 64 or 256 vectors): a power of two of lanes per
+//         instance, sums by shuffles, weights kept in registers over many rows;
+//   block (a row of the group fits a workgroup's threads): one workgroup per
+//         instance or slab, its values in registers;
+//   plain (wider groups): one workgroup per instance, several passes.
+// Statistics in fp32 by differences: the mean first, then the squares about it
+// (slabs: their own means, joined by n_i (mean_i - mean)^2).
 #include "../../include/selscan.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -20,189 +31,650 @@ struct GnArgs {
     int64_t N, S, C, G;
     int32_t act;
     float eps;
+    // work split
+    int32_t D, lanes;   // channels of a group; vectors of a row of it
+    int32_t sub, gb;    // rows kernel: lanes of an instance, groups of a workgroup
+    int64_t per;        // rows kernel: rows of a workgroup; block kernel: rows of a slab
+    int32_t slabs;
+    float* stats;       // per instance and slab: (mean, M2), backward (sum e, sum e xh)
+    float* part;        // partial column sums: [part][2][C] of du xh and du; null: not wanted
 };
 
-// Sum over the 256 threads of a workgroup, in a fixed order; every thread gets it.
+// ---- vectors of V values -----------------------------------------------------
+
+template <typename T, int V> struct Vec {
+    float v[V];
+};
+template <int B> struct Raw;
+template <> struct Raw<2> { using type = uint16_t; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<16> { using type = uint4; };
+
+template <typename T, int V> using raw_t = typename Raw<int(sizeof(T)) * V>::type;
+template <typename T, int V>
+__device__ __forceinline__ raw_t<T, V> load_raw(const void* p, int64_t i) {
+    return *reinterpret_cast<const raw_t<T, V>*>(static_cast<const T*>(p) + i);
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const raw_t<T, V>& r, float (&f)[V]) {
+    struct A { T t[V]; };
+    const A a = __builtin_bit_cast(A, r);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f32(a.t[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&f)[V]) {
+    struct A { T t[V]; } a;
+#pragma unroll
+    for (int j = 0; j < V; ++j) a.t[j] = from_f32<T>(f[j]);
+    *reinterpret_cast<raw_t<T, V>*>(static_cast<T*>(p) + i) = __builtin_bit_cast(raw_t<T, V>, a);
+}
+template <int V>
+__device__ __forceinline__ void load_affine(const float* p, int64_t c, float dflt, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = p ? p[c + i] : dflt;
+}
+
+// ---- the functions -------------------------------------------------------------
+
+__device__ __forceinline__ float activate(float u, int act, float z) {
+    return act == SELSCAN_ACT_SILU ? silu(u) : act == SELSCAN_ACT_GATE ? u * silu(z) : u;
+}
+// du and (gate) dz of one value.
+__device__ __forceinline__ float grad_u(int act, float u, float dy, float z, float* dz) {
+    if (act == SELSCAN_ACT_SILU) return dy * silu_grad(u);
+    if (act == SELSCAN_ACT_GATE) {
+        *dz = dy * u * silu_grad(z);
+        return dy * silu(z);
+    }
+    return dy;
+}
+
+// Sum over the workgroup's threads, in a fixed order; every thread gets it.
 __device__ __forceinline__ float block_sum(float v, float* red) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, waves = (blockDim.x + 63) / 64;
 #pragma unroll
     for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
     __syncthreads();
     if (tid % 64 == 0) red[tid / 64] = v;
     __syncthreads();
-    return red[0] + red[1] + red[2] + red[3];
+    float s = red[0];
+    for (int i = 1; i < waves; ++i) s += red[i];
+    return s;
 }
 
-__device__ __forceinline__ float activate(float u, int act, float z) {
-    return act == SELSCAN_ACT_SILU ? silu(u) : act == SELSCAN_ACT_GATE ? u * silu(z) : u;
+// ---- rows: S = 1 ----------------------------------------------------------------
+//
+// `sub` lanes (a power of two) hold an instance, KV vectors each; a workgroup
+// covers gb groups and 256 / sub / gb rows at once, and goes down `per` rows
+// with its columns fixed, the next row's loads in flight.
+template <typename T, int V, int KV, bool BWD>
+__global__ __launch_bounds__(256) void rows_kernel(GnArgs a) {
+    __shared__ float cols[BWD ? 256 * KV * V : 1];
+    const int tid = threadIdx.x, j = tid / a.sub, l = tid % a.sub, step = 256 / a.sub / a.gb;
+    const int gi = j % a.gb, ri = j / a.gb;
+    const int64_t g = int64_t(blockIdx.x) * a.gb + gi;
+    const bool live = g < a.G && ri < step;
+    const int64_t r0 = int64_t(blockIdx.y) * a.per, r1 = r0 + a.per < a.N ? r0 + a.per : a.N;
+    const bool gate = a.act == SELSCAN_ACT_GATE;
+    float w[KV][V], b[KV][V], sw[KV][V], sb[KV][V];
+    bool in[KV];
+#pragma unroll
+    for (int k = 0; k < KV; ++k) {
+        in[k] = live && l + a.sub * k < a.lanes;
+        const int64_t c = g * a.D + int64_t(l + a.sub * k) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            w[k][i] = in[k] && a.weight ? a.weight[c + i] : 1.0f;
+            b[k][i] = in[k] && a.bias ? a.bias[c + i] : 0.0f;
+            sw[k][i] = sb[k][i] = 0.0f;
+        }
+    }
+    raw_t<T, V> nx[KV], nz[KV], ny[KV];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < KV; ++k) {
+            if (!in[k] || r >= r1) continue;
+            const int64_t at = r * a.C + g * a.D + int64_t(l + a.sub * k) * V;
+            nx[k] = load_raw<T, V>(a.x, at);
+            if (gate) nz[k] = load_raw<T, V>(a.z, at);
+            if (BWD) ny[k] = load_raw<T, V>(a.dy, at);
+        }
+    };
+    auto sum = [&](float v) {
+        for (int m = a.sub / 2; m; m >>= 1) v += __shfl_xor(v, m, 64);
+        return v;
+    };
+    if (live) {
+        const float inv = 1.0f / float(a.D);
+        fetch(r0 + ri);
+        for (int64_t r = r0 + ri; r < r1; r += step) {
+            float x[KV][V], z[KV][V], dy[KV][V];
+#pragma unroll
+            for (int k = 0; k < KV; ++k) {
+                unpack<T, V>(nx[k], x[k]);
+                if (gate) unpack<T, V>(nz[k], z[k]);
+                if (BWD) unpack<T, V>(ny[k], dy[k]);
+            }
+            fetch(r + step);
+            float mean, rstd;
+            if (!BWD) {
+                float s = 0.0f;
+#pragma unroll
+                for (int k = 0; k < KV; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s += in[k] ? x[k][i] : 0.0f;
+                mean = sum(s) * inv;
+                s = 0.0f;
+#pragma unroll
+                for (int k = 0; k < KV; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float d = in[k] ? x[k][i] - mean : 0.0f;
+                        s = fmaf(d, d, s);
+                    }
+                rstd = 1.0f / sqrtf(sum(s) * inv + a.eps);
+                if (a.mean && l == 0) {
+                    a.mean[r * a.G + g] = mean;
+                    a.rstd[r * a.G + g] = rstd;
+                }
+            } else {
+                mean = a.mean[r * a.G + g];
+                rstd = a.rstd[r * a.G + g];
+            }
+            const int64_t at = r * a.C + g * a.D + int64_t(l) * V;
+            if (!BWD) {
+#pragma unroll
+                for (int k = 0; k < KV; ++k) {
+                    float y[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        y[i] = activate(fmaf((x[k][i] - mean) * rstd, w[k][i], b[k][i]), a.act, gate ? z[k][i] : 0.0f);
+                    if (in[k]) store_vec<T, V>(a.y, at + int64_t(a.sub) * k * V, y);
+                }
+            } else {
+                float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+                for (int k = 0; k < KV; ++k) {
+                    float dz[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float xh = (x[k][i] - mean) * rstd;
+                        const float du = grad_u(a.act, fmaf(xh, w[k][i], b[k][i]), dy[k][i], gate ? z[k][i] : 0.0f, &dz[i]);
+                        const float e = in[k] ? du * w[k][i] : 0.0f;
+                        sw[k][i] = fmaf(du, xh, sw[k][i]);
+                        sb[k][i] += du;
+                        s1 += e;
+                        s2 = in[k] ? fmaf(e, xh, s2) : s2;
+                        x[k][i] = xh;
+                        dy[k][i] = e;
+                    }
+                    if (gate && in[k]) store_vec<T, V>(a.dz, at + int64_t(a.sub) * k * V, dz);
+                }
+                const float m1 = sum(s1) * inv, m2 = sum(s2) * inv;
+#pragma unroll
+                for (int k = 0; k < KV; ++k) {
+                    float dx[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) dx[i] = rstd * (dy[k][i] - m1 - x[k][i] * m2);
+                    if (in[k]) store_vec<T, V>(a.dx, at + int64_t(a.sub) * k * V, dx);
+                }
+            }
+        }
+    }
+    if (BWD && a.part) {  // the workgroup's column sums: its `step` rows at a time joined in order
+        const int width = a.gb * a.D;
+        float* out = a.part + int64_t(blockIdx.y) * 2 * a.C + int64_t(blockIdx.x) * width;
+        const int64_t have = a.C - int64_t(blockIdx.x) * width;
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < KV; ++k)
+                if (in[k])
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        cols[ri * width + gi * a.D + (l + a.sub * k) * V + i] = which ? sb[k][i] : sw[k][i];
+            __syncthreads();
+            for (int c = tid; c < width && c < have; c += 256) {
+                float s = cols[c];
+                for (int r = 1; r < step; ++r) s += cols[r * width + c];
+                out[which * a.C + c] = s;
+            }
+        }
+    }
 }
 
-// One workgroup per (n, group), over its S x D values three times.
-template <typename T>
-__global__ __launch_bounds__(256) void gn_kernel(GnArgs a) {
-    __shared__ float red[4];
-    for (int64_t i0 = blockIdx.x; i0 < a.N * a.G; i0 += gridDim.x) {
-        const int64_t n = i0 / a.G, g = i0 % a.G, D = a.C / a.G, cnt = a.S * D;
-        const T* x = static_cast<const T*>(a.x) + n * a.S * a.C + g * D;
-        const T* z = static_cast<const T*>(a.z) + n * a.S * a.C + g * D;
-        T* y = static_cast<T*>(a.y) + n * a.S * a.C + g * D;
+// ---- block: an instance or a slab of its rows per workgroup ----------------------
+//
+// Thread (r, v) takes vector v of rows r, r + rs, ... of the slab, K of them in
+// registers; threads past the last whole row idle.
+enum { kFused = 0, kStats = 1, kApply = 2 };
+constexpr int kFwdK = 8, kBwdK = 4;
+
+template <typename T, int V, bool BWD, int MODE>
+__global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
+    constexpr int K = BWD ? kBwdK : kFwdK;
+    __shared__ float red[16];
+    __shared__ float cols[BWD && MODE != kApply ? 1024 * V : 1];
+    const int tid = threadIdx.x, rs = int(blockDim.x) / a.lanes, r0 = tid / a.lanes, v = tid % a.lanes;
+    const int64_t inst = blockIdx.x / a.slabs, slab = blockIdx.x % a.slabs;
+    const int64_t n = inst / a.G, g = inst % a.G;
+    const int64_t s0 = slab * a.per, s1 = s0 + a.per < a.S ? s0 + a.per : a.S;
+    const bool gate = a.act == SELSCAN_ACT_GATE, live = r0 < rs;
+    const int64_t c = g * a.D + int64_t(v) * V;
+    const int64_t base = n * a.S * a.C + c;
+    raw_t<T, V> x[K], z[K], dy[K];
+    bool in[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t s = s0 + r0 + int64_t(rs) * k;
+        in[k] = live && s < s1;
+        if (!in[k]) continue;
+        x[k] = load_raw<T, V>(a.x, base + s * a.C);
+        if ((BWD || MODE != kStats) && gate) z[k] = load_raw<T, V>(a.z, base + s * a.C);
+        if (BWD) dy[k] = load_raw<T, V>(a.dy, base + s * a.C);
+    }
+    auto values = [&](const raw_t<T, V>& r, float (&f)[V]) { unpack<T, V>(r, f); };
+    const float cnt = float(s1 - s0) * float(a.D), all = float(a.S) * float(a.D);
+    float w[V], b[V];
+    if (BWD || MODE != kStats) {
+        load_affine<V>(live ? a.weight : nullptr, c, 1.0f, w);
+        load_affine<V>(live ? a.bias : nullptr, c, 0.0f, b);
+    }
+    if (!BWD) {
+        float mean, var;
+        if (MODE != kApply) {
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float f[V];
+                if (!in[k]) continue;
+                values(x[k], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s += f[i];
+            }
+            mean = block_sum(s, red) / cnt;
+            s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float f[V];
+                if (!in[k]) continue;
+                values(x[k], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s = fmaf(f[i] - mean, f[i] - mean, s);
+            }
+            var = block_sum(s, red);
+            if (MODE == kStats) {
+                if (tid == 0) {
+                    a.stats[2 * int64_t(blockIdx.x)] = mean;
+                    a.stats[2 * int64_t(blockIdx.x) + 1] = var;
+                }
+                return;
+            }
+        } else {
+            const float* st = a.stats + 2 * inst * a.slabs;
+            auto rows = [&](int i) { return float(i + 1 < a.slabs ? a.per : a.S - int64_t(i) * a.per) * float(a.D); };
+            float s = 0.0f;
+            for (int i = tid; i < a.slabs; i += blockDim.x) s = fmaf(st[2 * i], rows(i), s);
+            mean = block_sum(s, red) / all;
+            s = 0.0f;
+            for (int i = tid; i < a.slabs; i += blockDim.x) {
+                const float d = st[2 * i] - mean;
+                s += fmaf(d * d, rows(i), st[2 * i + 1]);
+            }
+            var = block_sum(s, red);
+        }
+        const float rstd = 1.0f / sqrtf(var / all + a.eps);
+        if (a.mean && slab == 0 && tid == 0) {
+            a.mean[inst] = mean;
+            a.rstd[inst] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (!in[k]) continue;
+            float f[V], zz[V], y[V];
+            values(x[k], f);
+            if (gate) values(z[k], zz);
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] = activate(fmaf((f[i] - mean) * rstd, w[i], b[i]), a.act, gate ? zz[i] : 0.0f);
+            store_vec<T, V>(a.y, base + (s0 + r0 + int64_t(rs) * k) * a.C, y);
+        }
+    } else {
+        const float mean = a.mean[inst], rstd = a.rstd[inst];
+        // xh, du and dz of vector k
+        auto grads = [&](int k, float (&xh)[V], float (&du)[V], float (&dz)[V]) {
+            float f[V], zz[V], gy[V];
+            values(x[k], f);
+            values(dy[k], gy);
+            if (gate) values(z[k], zz);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                xh[i] = (f[i] - mean) * rstd;
+                du[i] = grad_u(a.act, fmaf(xh[i], w[i], b[i]), gy[i], gate ? zz[i] : 0.0f, &dz[i]);
+            }
+        };
+        float m1, m2;
+        if (MODE != kApply) {
+            float s1_ = 0.0f, s2_ = 0.0f, sw[V], sb[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) sw[i] = sb[i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!in[k]) continue;
+                float xh[V], du[V], dz[V];
+                grads(k, xh, du, dz);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    sw[i] = fmaf(du[i], xh[i], sw[i]);
+                    sb[i] += du[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s1_ = fmaf(sb[i], w[i], s1_);
+                s2_ = fmaf(sw[i], w[i], s2_);
+            }
+            m1 = block_sum(s1_, red);
+            m2 = block_sum(s2_, red);
+            if (a.part) {  // this slab's column sums, its rows joined in order
+                float* out = a.part + (n * a.slabs + slab) * 2 * a.C + g * a.D;
+                for (int which = 0; which < 2; ++which) {
+                    __syncthreads();
+                    if (live)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) cols[(r0 * a.lanes + v) * V + i] = which ? sb[i] : sw[i];
+                    __syncthreads();
+                    for (int i = tid; i < a.D; i += blockDim.x) {
+                        float s = cols[i];
+                        for (int r = 1; r < rs; ++r) s += cols[r * a.D + i];
+                        out[which * a.C + i] = s;
+                    }
+                }
+            }
+            if (MODE == kStats) {
+                if (tid == 0) {
+                    a.stats[2 * int64_t(blockIdx.x)] = m1;
+                    a.stats[2 * int64_t(blockIdx.x) + 1] = m2;
+                }
+                return;
+            }
+        } else {
+            const float* st = a.stats + 2 * inst * a.slabs;
+            float p1 = 0.0f, p2 = 0.0f;
+            for (int i = tid; i < a.slabs; i += blockDim.x) {
+                p1 += st[2 * i];
+                p2 += st[2 * i + 1];
+            }
+            m1 = block_sum(p1, red);
+            m2 = block_sum(p2, red);
+        }
+        m1 /= all;
+        m2 /= all;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (!in[k]) continue;
+            float xh[V], du[V], dz[V], dx[V];
+            grads(k, xh, du, dz);
+#pragma unroll
+            for (int i = 0; i < V; ++i) dx[i] = rstd * (du[i] * w[i] - m1 - xh[i] * m2);
+            const int64_t at = base + (s0 + r0 + int64_t(rs) * k) * a.C;
+            store_vec<T, V>(a.dx, at, dx);
+            if (gate) store_vec<T, V>(a.dz, at, dz);
+        }
+    }
+}
+
+// ---- plain: groups wider than a workgroup's vectors -------------------------------
+
+template <typename T, bool BWD>
+__global__ __launch_bounds__(1024) void plain_kernel(GnArgs a) {
+    __shared__ float red[16];
+    const int64_t n = blockIdx.x / a.G, g = blockIdx.x % a.G, cnt = a.S * a.D;
+    const int64_t base = n * a.S * a.C + g * a.D;
+    const T* x = static_cast<const T*>(a.x) + base;
+    const T* z = static_cast<const T*>(a.z) + base;
+    const bool gate = a.act == SELSCAN_ACT_GATE;
+    auto each = [&](auto f) {
+        for (int64_t i = threadIdx.x; i < cnt; i += blockDim.x) f(i / a.D * a.C + i % a.D, g * a.D + i % a.D);
+    };
+    if (!BWD) {
+        T* y = static_cast<T*>(a.y) + base;
         float s = 0.0f;
-        for (int64_t i = threadIdx.x; i < cnt; i += 256) s += to_f32(x[i / D * a.C + i % D]);
+        each([&](int64_t i, int64_t) { s += to_f32(x[i]); });
         const float mean = block_sum(s, red) / float(cnt);
         s = 0.0f;
-        for (int64_t i = threadIdx.x; i < cnt; i += 256) {
-            const float d = to_f32(x[i / D * a.C + i % D]) - mean;
+        each([&](int64_t i, int64_t) {
+            const float d = to_f32(x[i]) - mean;
             s = fmaf(d, d, s);
-        }
+        });
         const float rstd = 1.0f / sqrtf(block_sum(s, red) / float(cnt) + a.eps);
-        for (int64_t i = threadIdx.x; i < cnt; i += 256) {
-            const int64_t at = i / D * a.C + i % D, c = g * D + i % D;
-            const float u = fmaf((to_f32(x[at]) - mean) * rstd, a.weight ? a.weight[c] : 1.0f, a.bias ? a.bias[c] : 0.0f);
-            y[at] = from_f32<T>(activate(u, a.act, a.act == SELSCAN_ACT_GATE ? to_f32(z[at]) : 0.0f));
-        }
+        each([&](int64_t i, int64_t c) {
+            const float u = fmaf((to_f32(x[i]) - mean) * rstd, a.weight ? a.weight[c] : 1.0f, a.bias ? a.bias[c] : 0.0f);
+            y[i] = from_f32<T>(activate(u, a.act, gate ? to_f32(z[i]) : 0.0f));
+        });
         if (a.mean && threadIdx.x == 0) {
-            a.mean[i0] = mean;
-            a.rstd[i0] = rstd;
+            a.mean[blockIdx.x] = mean;
+            a.rstd[blockIdx.x] = rstd;
         }
-    }
-}
-
-// du and (gate) dz of one value.
-struct Grad {
-    float xh, du, dz;
-};
-__device__ __forceinline__ Grad grad_of(const GnArgs& a, float x, float dy, float z, float mean, float rstd, float w,
-                                        float b) {
-    Grad r;
-    r.xh = (x - mean) * rstd;
-    r.dz = 0.0f;
-    const float u = fmaf(r.xh, w, b);
-    if (a.act == SELSCAN_ACT_SILU) {
-        r.du = dy * silu_grad(u);
-    } else if (a.act == SELSCAN_ACT_GATE) {
-        r.du = dy * silu(z);
-        r.dz = dy * u * silu_grad(z);
     } else {
-        r.du = dy;
-    }
-    return r;
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void gn_bwd_kernel(GnArgs a) {
-    __shared__ float red[4];
-    for (int64_t i0 = blockIdx.x; i0 < a.N * a.G; i0 += gridDim.x) {
-        const int64_t n = i0 / a.G, g = i0 % a.G, D = a.C / a.G, cnt = a.S * D;
-        const int64_t base = n * a.S * a.C + g * D;
-        const T* x = static_cast<const T*>(a.x) + base;
-        const T* z = static_cast<const T*>(a.z) + base;
         const T* dy = static_cast<const T*>(a.dy) + base;
         T* dx = static_cast<T*>(a.dx) + base;
         T* dz = static_cast<T*>(a.dz) + base;
-        const float mean = a.mean[i0], rstd = a.rstd[i0];
-        const bool gate = a.act == SELSCAN_ACT_GATE;
+        const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
         float s1 = 0.0f, s2 = 0.0f;
-        auto at = [&](int64_t i) { return i / D * a.C + i % D; };
-        auto get = [&](int64_t i, float* w) {
-            const int64_t c = g * D + i % D, j = at(i);
-            *w = a.weight ? a.weight[c] : 1.0f;
-            return grad_of(a, to_f32(x[j]), to_f32(dy[j]), gate ? to_f32(z[j]) : 0.0f, mean, rstd, *w,
-                           a.bias ? a.bias[c] : 0.0f);
+        auto grad = [&](int64_t i, int64_t c, float* xh, float* d) {
+            const float w = a.weight ? a.weight[c] : 1.0f;
+            *xh = (to_f32(x[i]) - mean) * rstd;
+            return w * grad_u(a.act, fmaf(*xh, w, a.bias ? a.bias[c] : 0.0f), to_f32(dy[i]), gate ? to_f32(z[i]) : 0.0f, d);
         };
-        for (int64_t i = threadIdx.x; i < cnt; i += 256) {
-            float w;
-            const Grad r = get(i, &w);
-            s1 += r.du * w;
-            s2 = fmaf(r.du * w, r.xh, s2);
-        }
+        each([&](int64_t i, int64_t c) {
+            float xh, d;
+            const float e = grad(i, c, &xh, &d);
+            s1 += e;
+            s2 = fmaf(e, xh, s2);
+        });
         const float m1 = block_sum(s1, red) / float(cnt), m2 = block_sum(s2, red) / float(cnt);
-        for (int64_t i = threadIdx.x; i < cnt; i += 256) {
-            float w;
-            const Grad r = get(i, &w);
-            if (gate) dz[at(i)] = from_f32<T>(r.dz);
-            dx[at(i)] = from_f32<T>(rstd * (r.du * w - m1 - r.xh * m2));
-        }
+        each([&](int64_t i, int64_t c) {
+            float xh, d;
+            const float e = grad(i, c, &xh, &d);
+            dx[i] = from_f32<T>(rstd * (e - m1 - xh * m2));
+            if (gate) dz[i] = from_f32<T>(d);
+        });
     }
 }
 
-constexpr int kParts = 256;  // runs of rows whose column sums are formed apart
-
-// part[k][0..1][c]: the sums of du xh and du over run k's rows (n, s).
+// Its column sums: part[k][0..1][c] over run k's rows (n, s).
 template <typename T>
-__global__ __launch_bounds__(256) void gn_cols_kernel(GnArgs a, int64_t rows, int64_t per, float* part) {
-    const int64_t c = int64_t(blockIdx.y) * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void plain_cols_kernel(GnArgs a) {
+    const int64_t c = int64_t(blockIdx.y) * 256 + threadIdx.x, rows = a.N * a.S;
     if (c >= a.C) return;
-    const int64_t g = c / (a.C / a.G), r0 = int64_t(blockIdx.x) * per, r1 = min(r0 + per, rows);
+    const int64_t g = c / a.D, r0 = int64_t(blockIdx.x) * a.per, r1 = r0 + a.per < rows ? r0 + a.per : rows;
     const float w = a.weight ? a.weight[c] : 1.0f, b = a.bias ? a.bias[c] : 0.0f;
     float sw = 0.0f, sb = 0.0f;
     for (int64_t r = r0; r < r1; ++r) {
         const int64_t n = r / a.S, j = r * a.C + c;
-        const Grad v = grad_of(a, to_f32(static_cast<const T*>(a.x)[j]), to_f32(static_cast<const T*>(a.dy)[j]),
-                               a.act == SELSCAN_ACT_GATE ? to_f32(static_cast<const T*>(a.z)[j]) : 0.0f,
-                               a.mean[n * a.G + g], a.rstd[n * a.G + g], w, b);
-        sw = fmaf(v.du, v.xh, sw);
-        sb += v.du;
+        const float xh = (to_f32(static_cast<const T*>(a.x)[j]) - a.mean[n * a.G + g]) * a.rstd[n * a.G + g];
+        float dz;
+        const float du = grad_u(a.act, fmaf(xh, w, b), to_f32(static_cast<const T*>(a.dy)[j]),
+                                a.act == SELSCAN_ACT_GATE ? to_f32(static_cast<const T*>(a.z)[j]) : 0.0f, &dz);
+        sw = fmaf(du, xh, sw);
+        sb += du;
     }
-    part[(int64_t(blockIdx.x) * 2 + 0) * a.C + c] = sw;
-    part[(int64_t(blockIdx.x) * 2 + 1) * a.C + c] = sb;
+    a.part[(int64_t(blockIdx.x) * 2 + 0) * a.C + c] = sw;
+    a.part[(int64_t(blockIdx.x) * 2 + 1) * a.C + c] = sb;
 }
 
-__global__ __launch_bounds__(256) void gn_cols_sum_kernel(const float* part, int parts, int64_t C, float* dweight,
-                                                          float* dbias) {
-    const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (c >= C) return;
-    float sw = 0.0f, sb = 0.0f;
-    for (int k = 0; k < parts; ++k) {
-        sw += part[(int64_t(k) * 2 + 0) * C + c];
-        sb += part[(int64_t(k) * 2 + 1) * C + c];
+// dweight (y 0) and dbias (y 1): the partial sums of 16 interleaved rows of
+// parts, joined in order; 64 columns per workgroup.
+__global__ __launch_bounds__(1024) void cols_sum_kernel(const float* __restrict__ part, int parts, int64_t C,
+                                                        float* __restrict__ dweight, float* __restrict__ dbias) {
+    __shared__ float red[16][64];
+    const int col = threadIdx.x % 64, r = threadIdx.x / 64;
+    const int64_t c = int64_t(blockIdx.x) * 64 + col;
+    float* out = blockIdx.y ? dbias : dweight;
+    if (!out) return;
+    float s = 0.0f;
+    if (c < C) {
+#pragma unroll 4
+        for (int k = r; k < parts; k += 16) s += part[(int64_t(k) * 2 + blockIdx.y) * C + c];
     }
-    if (dweight) dweight[c] = sw;
-    if (dbias) dbias[c] = sb;
+    red[r][col] = s;
+    __syncthreads();
+    if (r == 0 && c < C) {
+#pragma unroll
+        for (int k = 1; k < 16; ++k) s += red[k][col];
+        out[c] = s;
+    }
 }
 
-GnArgs args_of(const GroupnormTensors& t, const GroupnormShape& s) {
-    return {t.x, t.weight, t.bias, t.z, t.y, t.mean, t.rstd, t.dy, t.dx, t.dz, s.N, s.S, s.C, s.G, s.act, s.eps};
+// ---- the split of a call -----------------------------------------------------------
+
+struct Plan {
+    enum Kind { kRows, kBlock, kPlain } kind;
+    int V, KV;
+    int sub, gb;
+    int64_t per;
+    int slabs, threads;
+    int64_t parts;  // backward: partial column sums
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+Plan plan_of(const GroupnormShape& s, bool bwd) {
+    Plan p{};
+    const int64_t D = s.C / s.G;
+    // the widest vector (16 bytes at most) that divides a group: rows are then aligned to it too
+    const int full = s.dtype == DType::BF16 ? 8 : 4;
+    p.V = full;
+    while (D % p.V) p.V /= 2;
+    const int64_t lanes = D / p.V;
+    p.KV = 1;
+    if (s.S == 1 && (lanes <= 64 || (lanes <= 256 && p.V == full))) {
+        p.kind = Plan::kRows;
+        if (lanes > 64) p.KV = 4;
+        p.sub = 1;
+        while (p.sub * p.KV < lanes) p.sub *= 2;
+        const int n = 256 / p.sub;
+        p.gb = int(s.G < n ? s.G : n);
+        const int step = n / p.gb;
+        // about 8 workgroups a CU; the backward's partial sums are written per
+        // workgroup, so it takes half as many
+        const int64_t blocks = ceil_div(s.G, p.gb), want = ceil_div(bwd ? 1024 : 2048, blocks);
+        p.per = ceil_div(ceil_div(s.N, want), step) * step;
+        p.slabs = 1;
+        p.parts = ceil_div(s.N, p.per);
+    } else if (lanes <= 1024) {
+        p.kind = Plan::kBlock;
+        const int K = bwd ? kBwdK : kFwdK;
+        // threads for two vectors each, whole waves, at least one row
+        int64_t t = ceil_div(s.S * lanes, 2);
+        t = t < lanes ? lanes : t;
+        t = t > 1024 ? 1024 : t;
+        p.threads = int(ceil_div(t, 64) * 64);
+        const int64_t rs = p.threads / lanes;
+        p.per = rs * K;
+        p.slabs = int(ceil_div(s.S, p.per));
+        p.parts = s.N * p.slabs;
+    } else {
+        p.kind = Plan::kPlain;
+        p.threads = 1024;
+        p.slabs = 1;
+        p.per = ceil_div(s.N * s.S, 256);
+        p.parts = ceil_div(s.N * s.S, p.per);
+    }
+    return p;
 }
-int64_t rows_per_part(const GroupnormShape& s) { return (s.N * s.S + kParts - 1) / kParts; }
-int parts_of(const GroupnormShape& s) {
-    const int64_t per = rows_per_part(s);
-    return int((s.N * s.S + per - 1) / per);
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+size_t stats_bytes(const GroupnormShape& s, const Plan& p) {
+    return p.slabs > 1 ? up256(size_t(s.N * s.G) * p.slabs * 2 * sizeof(float)) : 0;
+}
+
+GnArgs args_of(const GroupnormTensors& t, const GroupnormShape& s, const Plan& p) {
+    GnArgs a{};
+    a.x = t.x; a.weight = t.weight; a.bias = t.bias; a.z = t.z; a.y = t.y;
+    a.mean = t.mean; a.rstd = t.rstd; a.dy = t.dy; a.dx = t.dx; a.dz = t.dz;
+    a.N = s.N; a.S = s.S; a.C = s.C; a.G = s.G; a.act = s.act; a.eps = s.eps;
+    a.D = int32_t(s.C / s.G);
+    a.lanes = a.D / p.V;
+    a.sub = p.sub; a.gb = p.gb; a.per = p.per; a.slabs = p.slabs;
+    return a;
+}
+
+template <typename T, int V, bool BWD>
+void launch_v(const GnArgs& a, const Plan& p, hipStream_t st) {
+    if (p.kind == Plan::kRows) {
+        const dim3 grid(unsigned(ceil_div(a.G, a.gb)), unsigned(ceil_div(a.N, a.per)));
+        if constexpr (V * sizeof(T) == 16) {
+            if (p.KV == 4) {
+                hipLaunchKernelGGL((rows_kernel<T, V, 4, BWD>), grid, dim3(256), 0, st, a);
+                return;
+            }
+        }
+        hipLaunchKernelGGL((rows_kernel<T, V, 1, BWD>), grid, dim3(256), 0, st, a);
+        return;
+    }
+    const dim3 grid(unsigned(a.N * a.G * a.slabs)), block(unsigned(p.threads));
+    if (a.slabs == 1) {
+        hipLaunchKernelGGL((block_kernel<T, V, BWD, kFused>), grid, block, 0, st, a);
+    } else {
+        hipLaunchKernelGGL((block_kernel<T, V, BWD, kStats>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((block_kernel<T, V, BWD, kApply>), grid, block, 0, st, a);
+    }
+}
+
+template <typename T, bool BWD>
+void launch(const GnArgs& a, const Plan& p, hipStream_t st) {
+    if (p.kind == Plan::kPlain) {
+        hipLaunchKernelGGL((plain_kernel<T, BWD>), dim3(unsigned(a.N * a.G)), dim3(unsigned(p.threads)), 0, st, a);
+        if (BWD && a.part)
+            hipLaunchKernelGGL((plain_cols_kernel<T>), dim3(unsigned(p.parts), unsigned(ceil_div(a.C, 256))), dim3(256),
+                               0, st, a);
+        return;
+    }
+    if (p.V == 1) launch_v<T, 1, BWD>(a, p, st);
+    else if (p.V == 2) launch_v<T, 2, BWD>(a, p, st);
+    else if (p.V == 4) launch_v<T, 4, BWD>(a, p, st);
+    else if constexpr (sizeof(T) == 2) launch_v<T, 8, BWD>(a, p, st);
 }
 
 }  // namespace
 
-size_t groupnorm_workspace_bytes(const GroupnormShape& s, bool backward) {
-    return backward ? size_t(parts_of(s)) * 2 * s.C * sizeof(float) : 0;
+// A grid has fewer than 2^32 threads; slabs and partial sums are counted in 32 bits.
+bool groupnorm_fits(const GroupnormShape& s, bool backward) {
+    if (s.N * s.S * s.C == 0) return true;
+    const Plan p = plan_of(s, backward);
+    if (p.kind == Plan::kRows) return true;
+    return p.parts <= INT32_MAX && s.N * s.G * p.slabs * p.threads < (int64_t(1) << 32);
 }
 
-hipError_t launch_groupnorm(const GroupnormTensors& t, const GroupnormShape& s, void*, hipStream_t stream) {
-    // a grid has fewer than 2^32 threads
-    const dim3 grid(unsigned(s.N * s.G < (1 << 20) ? s.N * s.G : (1 << 20))), block(256);
-    const GnArgs a = args_of(t, s);
-    if (s.dtype == DType::BF16) hipLaunchKernelGGL((gn_kernel<bf16_bits>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((gn_kernel<float>), grid, block, 0, stream, a);
+size_t groupnorm_workspace_bytes(const GroupnormShape& s, bool backward) {
+    const Plan p = plan_of(s, backward);
+    return stats_bytes(s, p) + (backward ? size_t(p.parts) * 2 * s.C * sizeof(float) : 0);
+}
+
+hipError_t launch_groupnorm(const GroupnormTensors& t, const GroupnormShape& s, void* workspace, hipStream_t stream) {
+    const Plan p = plan_of(s, false);
+    GnArgs a = args_of(t, s, p);
+    a.stats = static_cast<float*>(workspace);
+    if (s.dtype == DType::BF16) launch<bf16_bits, false>(a, p, stream);
+    else launch<float, false>(a, p, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_groupnorm_bwd(const GroupnormTensors& t, const GroupnormShape& s, void* workspace,
                                 hipStream_t stream) {
-    // a grid has fewer than 2^32 threads
-    const dim3 grid(unsigned(s.N * s.G < (1 << 20) ? s.N * s.G : (1 << 20))), block(256);
-    const GnArgs a = args_of(t, s);
-    float* part = static_cast<float*>(workspace);
-    const int parts = parts_of(s);
-    const unsigned cb = unsigned((s.C + 255) / 256);
-    if (s.dtype == DType::BF16) {
-        hipLaunchKernelGGL((gn_bwd_kernel<bf16_bits>), grid, block, 0, stream, a);
-        hipLaunchKernelGGL((gn_cols_kernel<bf16_bits>), dim3(unsigned(parts), cb), block, 0, stream, a, s.N * s.S,
-                           rows_per_part(s), part);
-    } else {
-        hipLaunchKernelGGL((gn_bwd_kernel<float>), grid, block, 0, stream, a);
-        hipLaunchKernelGGL((gn_cols_kernel<float>), dim3(unsigned(parts), cb), block, 0, stream, a, s.N * s.S,
-                           rows_per_part(s), part);
-    }
-    if (t.dweight || t.dbias)
-        hipLaunchKernelGGL(gn_cols_sum_kernel, dim3(cb), block, 0, stream, part, parts, s.C, t.dweight, t.dbias);
+    const Plan p = plan_of(s, true);
+    GnArgs a = args_of(t, s, p);
+    a.stats = static_cast<float*>(workspace);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(s, p));
+    a.part = t.dweight || t.dbias ? part : nullptr;
+    if (s.dtype == DType::BF16) launch<bf16_bits, true>(a, p, stream);
+    else launch<float, true>(a, p, stream);
+    if (a.part)
+        hipLaunchKernelGGL(cols_sum_kernel, dim3(unsigned(ceil_div(s.C, 64)), 2), dim3(1024), 0, stream, part,
+                           int(p.parts), s.C, t.dweight, t.dbias);
     return hipGetLastError();
 }
 

@@ -260,6 +260,8 @@ struct GroupnormTensors {
     float* dbias;
     void* dz;
 };
+// Whether the call's grids and work splits stay within their index ranges.
+bool groupnorm_fits(const GroupnormShape& s, bool backward);
 size_t groupnorm_workspace_bytes(const GroupnormShape& s, bool backward);
 hipError_t launch_groupnorm(const GroupnormTensors& t, const GroupnormShape& s, void* workspace,
                             hipStream_t stream);
