@@ -177,7 +177,7 @@ def _check(code: int) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _req(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=None):
@@ -189,14 +189,21 @@ def _req(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=No
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
+# The current stream's handle without a Stream object around it (0.1 instead of
+# 2 us a call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def workspace_size(batch: int, L: int, dim: int, dtype: torch.dtype, N: int = 16, *,
@@ -527,11 +534,14 @@ def ssd_step(state: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A: torch
     return y
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _device(dev: torch.device):
     """The device the call launches on, made current where it is not."""
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {dev}")
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _HERE
 
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device) -> Optional[torch.Tensor]:
