@@ -41,17 +41,33 @@ template <> struct Ops<bf16_bits> {
     static __device__ __forceinline__ f32x4 mfma(const Frag& a, const Frag& b, const f32x4& c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
-    template <int N> static __device__ __forceinline__ void split(const float (&v)[E], Frag (&t)[N]) {
+    // v in N bf16 terms: the upper halves of v and of what is left (a mask, a
+    // subtraction and half a byte permutation each; the rounding conversion
+    // takes twice as long). ROUND: the second term rounded instead. Two terms are
+    // then off by 2^-16 of v at most; three hold all of its 24 bits either way.
+    template <int N, bool ROUND> static __device__ __forceinline__ void split(const float (&v)[E], Frag (&t)[N]) {
         float r[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) r[e] = v[e];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
+        for (int k = 0; k < N; ++k) {
+            uint32_t p[E / 2];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                t[k][e] = (__bf16)r[e];
-                if (k + 1 < N) r[e] -= (float)t[k][e];
+            for (int e = 0; e < E; e += 2) {
+                p[e / 2] = k == 1 && ROUND ? pack_bf16x2(r[e], r[e + 1]) : upper_halves(r[e], r[e + 1]);
+                if (k + 1 < N) {
+                    r[e] -= bf16_lo(p[e / 2]);
+                    r[e + 1] -= bf16_hi(p[e / 2]);
+                }
             }
+            struct A { uint32_t w[E / 2]; } a;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) a.w[e] = p[e];
+            t[k] = __builtin_bit_cast(Frag, a);
+        }
+    }
+    static __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
+        return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
     }
     static __device__ __forceinline__ float value(const Frag& f, int e) { return (float)f[e]; }
 };
@@ -65,7 +81,7 @@ template <> struct Ops<float> {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
-    template <int N> static __device__ __forceinline__ void split(const float (&v)[E], Frag (&t)[N]) {
+    template <int N, bool ROUND> static __device__ __forceinline__ void split(const float (&v)[E], Frag (&t)[N]) {
 #pragma unroll
         for (int e = 0; e < E; ++e) t[0][e] = v[e];
     }
@@ -169,7 +185,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // A run of a walk, chunk by chunk. KD: the width of a and b rounded up (64,
-// 128, 256); PT: state columns of the workgroup, 16 per wave.
+// 128, 256); PT: state columns of the workgroup.
 // STATE: only the run's end state, into run_state. SLOPE: with the outputs,
 // their derivative by log_decay, summed against `factor`.
 //
@@ -178,23 +194,40 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 //   o_i  = scale sum_j P_ij c_j + (scale or 1) lambda^(i + e0) a_i H
 //   H'   = lambda^n H + (1 or scale) sum_j lambda^(n-1-j+e1) b_j^T c_j
 // (e0, e1) = (1, 0) forwards, (0, 1) backwards, n tokens in the chunk.
-template <typename T, int Q, int KD, int PT, bool STATE, bool SLOPE, int WPE>
-__global__ __launch_bounds__(PT * 4, WPE) void walk_kernel(WalkArgs g) {
+//
+// Two kinds of waves. PT / 16 compute waves hold 16 state columns each and
+// form outputs and state; 4 supply waves load, stage the next chunk in the
+// other half of LDS and form its scores. Two barriers a chunk:
+//   outputs of chunk c   beside  staging chunk c + 1, loading c + 2
+//   state over chunk c   beside  scores of chunk c + 1
+constexpr int kSupply = 4;
+
+template <typename T, int Q, int KD, int PT, bool STATE, bool SLOPE>
+__global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) void walk_kernel(WalkArgs g) {
     using O = Ops<T>;
     using Frag = typename O::Frag;
-    constexpr int E = O::E, KB = O::KB, V = 16 / int(sizeof(T));
-    constexpr int NW = PT / 16, NTH = 64 * NW;  // waves, threads
-    constexpr int KT = KD / 16;           // 16-row tiles of the state
-    constexpr int TT = Q / 16;            // 16-token tiles of a chunk
-    constexpr int QB = Q / KB;            // operands along a chunk's tokens
+    constexpr int E = O::E, KB = O::KB, V = 16 / int(sizeof(T)), ES = int(sizeof(T));
+    constexpr int NW = PT / 16, NTH = 64 * (NW + kSupply);  // compute waves; all threads
+    constexpr int NS = kSupply * 64;       // supply threads
+    constexpr int KT = KD / 16;            // 16-row tiles of the state
+    constexpr int TT = Q / 16;             // 16-token tiles of a chunk
+    constexpr int QB = Q / KB;             // operands along a chunk's tokens
     constexpr bool BF = sizeof(T) == 2;
-    constexpr int NA = Q * KD / V / NTH;  // 16-byte pieces of a or b per thread
-    constexpr int NC = Q * PT / V / NTH;
-    __shared__ alignas(16) T As[STATE ? 16 : Q * Tile<T, KD>::kStride];
-    __shared__ alignas(16) T Bs[Q * Tile<T, KD>::kStride];
-    __shared__ alignas(16) T Cs[Q * Tile<T, PT>::kStride];
-    constexpr int NPS = O::TP * (SLOPE ? 2 : 1);
+    constexpr int NA = Q * KD / V / NS;    // 16-byte pieces of a or b per supply thread
+    constexpr int NC = Q * PT / V / NS;
+    constexpr int SA = Q * Tile<T, KD>::kStride, SC = Q * Tile<T, PT>::kStride;
+    // terms of the states in the outputs and of the scores; the slope is an fp32
+    // result, so its operands (the entering states, its own scores) take three
+    constexpr int TS = SLOPE && BF ? 3 : O::TS, TP = O::TP, TD = BF ? 3 : 1;
+    constexpr int NPS = TP + (SLOPE ? TD : 0);
+    constexpr bool VIA = BF && !SLOPE;  // outputs through LDS (SLOPE: no room left)
+    __shared__ alignas(16) T As2[STATE ? 1 : 2][STATE ? 16 : SA];  // chunks c (even, odd)
+    __shared__ alignas(16) T Bs2[2][SA];
+    __shared__ alignas(16) T Cs2[2][SC];
     __shared__ alignas(16) T Ps[STATE ? 1 : NPS][STATE ? 16 : Q * Tile<T, Q>::kStride];
+    // bf16 outputs go through LDS: stored in whole rows by the supply waves
+    constexpr int SO = PT + 8;
+    __shared__ alignas(16) T Os[STATE || !VIA ? 16 : Q * SO];
     __shared__ float red[NW];
 
     const int tid = threadIdx.x, lane = tid % 64, m = lane % 16, gq = lane / 16;
@@ -209,312 +242,415 @@ __global__ __launch_bounds__(PT * 4, WPE) void walk_kernel(WalkArgs g) {
     const int K = w.K, P = w.P;
     const int64_t len = entry_length(g.lengths, b, g.L);
     const Decay dec(g.log_decay[h]);
-    const int e0 = w.rev ? 0 : 1, e1 = 1 - e0;
-    const float sc_carry = w.rev ? 1.0f : g.scale, sc_upd = w.rev ? g.scale : 1.0f;
-
-    // ---- state: tiles of 16 rows, one column of 16 per wave ----
-    // An accumulator pair becomes one bf16 operand if its rows are dealt out as
-    // n = 32 (kt / 2) + 8 (m / 4) + 4 (kt % 2) + m % 4.
-    const int col0 = tile * PT + wv * 16;
-    auto row_of = [&](int kt, int r) { return BF ? 32 * (kt / 2) + 8 * gq + 4 * (kt % 2) + r : 16 * kt + 4 * gq + r; };
-    f32x4 S[KT];
-    f32x4 D[SLOPE ? KT : 1];
-    auto each_state = [&](auto f) {
-        const int p = col0 + m;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = row_of(kt, r);
-                f(kt, r, n, p, n < K && p < P);
-            }
-    };
-    const int64_t run_at = (int64_t(role) * g.segments + seg) * g.run_stride + bh * K * P;  // STATE: of this run
-    {
-        // the output pass has one run more than the state pass
-        const int64_t from = (int64_t(role) * (g.segments - 1) + seg - 1) * g.run_stride + bh * K * P;
-        const bool own = seg == 0;
-        const float* src = own ? (w.s0 ? w.s0 + bh * K * P : nullptr) : STATE ? nullptr : g.run_state + from;
-        const int sn = own ? w.sn : P, sp = own ? w.sp : 1;
-        const float* dsrc = SLOPE && !STATE && !own ? g.run_slope + from : nullptr;
-        each_state([&](int kt, int r, int n, int p, bool ok) {
-            S[kt][r] = src && ok ? src[int64_t(n) * sn + int64_t(p) * sp] : 0.0f;
-            if (SLOPE) D[kt][r] = dsrc && ok ? dsrc[int64_t(n) * P + p] : 0.0f;
-        });
-    }
-
-    // ---- powers of lambda by position ----
-    float diag[4], base[4], up[TT], pw16 = 0.0f, pw32 = 0.0f;
-    if (!STATE) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = m - 4 * gq - r;  // row minus column inside a 16 x 16 tile of scores
-            diag[r] = d >= 0 ? g.scale * dec.pow(d) : 0.0f;
-            base[r] = g.scale * dec.pow(16 + d);
-        }
-#pragma unroll
-        for (int k = 0; k < TT; ++k) up[k] = sc_carry * dec.pow(16 * k + m + e0);
-        pw16 = dec.pow(16);
-        pw32 = dec.pow(32);
-    }
-    float wt[QB][E];  // weights of the chunk's tokens in the state
-    auto weights = [&](int nv) {
-#pragma unroll
-        for (int q = 0; q < QB; ++q)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int s = KB * q + E * gq + e;
-                wt[q][e] = s < nv ? sc_upd * dec.pow(nv - 1 - s + e1) : 0.0f;
-            }
-    };
-    weights(Q);
-    float keep = dec.pow(Q);
 
     // ---- the run's tokens: positions p0 .. p1 - 1; position i is token i, or len - 1 - i ----
+    // The first chunk is the partial one, its tokens in the last slots, so that
+    // the weights of the slots in the state are the same for every chunk.
     const int64_t p0 = int64_t(seg) * g.seg_len;
     const int64_t p1 = len < p0 + g.seg_len ? len : p0 + g.seg_len;
     const int nc = p1 > p0 ? int((p1 - p0 + Q - 1) / Q) : 0;
-    const int64_t ra = h / (g.H / w.ha), rb = h / (g.H / w.hb), rc = h / (g.H / w.hc);
-    const T* pa = static_cast<const T*>(w.a) + (b * g.L * w.ha + ra) * K;
-    const T* pb = static_cast<const T*>(w.b) + (b * g.L * w.hb + rb) * K;
-    const T* pc = static_cast<const T*>(w.c) + (b * g.L * w.hc + rc) * P;
-    const int sa = w.ha * K, sb = w.hb * K, sc = w.hc * P, so = int(g.H) * P;  // elements from token to token
-    auto valid = [&](int c) { const int64_t n = p1 - p0 - int64_t(c) * Q; return int(n < Q ? (n > 0 ? n : 0) : Q); };
-    auto first = [&](int c, int nv) {  // lowest token of chunk c
-        const int64_t p = p0 + int64_t(c) * Q;
-        return w.rev ? len - p - nv : p;
-    };
-    auto span = [](int nv, int64_t stride, int row) { return nv > 0 ? int(((nv - 1) * stride + row) * int(sizeof(T))) : 0; };
+    const int skip0 = int(nc * int64_t(Q) - (p1 > p0 ? p1 - p0 : 0));  // empty slots of chunk 0
+    // Loads and stores go through buffer resources of a chunk's Q rows, based
+    // at its lowest token; a lane's offsets stay the same from chunk to chunk
+    // (kInvalid: a column past the width, which reads 0 and is not stored).
+    // Chunk 0's empty slots are kInvalid too: nothing before the run is touched.
+    const int64_t t_first = w.rev ? len - (p0 - skip0) - Q : p0 - skip0;
+    const int64_t t_step = w.rev ? -Q : Q;
+    const int oes = w.o_f32 ? 4 : ES;
+    const int col0 = tile * PT + wv * 16;  // a compute wave's first state column
+    float total = 0.0f;                    // SLOPE
 
-    u32x4 ga[STATE ? 1 : NA], gb[NA], gc[NC];
-    auto load = [&](int c) {
-        const int nv = valid(c);
-        const int64_t t0 = first(c, nv);
-        const auto ra_ = buf_rsrc(pa + t0 * sa, span(nv, sa, K));
-        const auto rb_ = buf_rsrc(pb + t0 * sb, span(nv, sb, K));
-        const auto rc_ = buf_rsrc(pc + t0 * sc, span(nv, sc, P));
+    if (wv >= NW) {
+        // ================================ supply ================================
+        const int st = tid - 64 * NW;
+        const int64_t ra = h / (g.H / w.ha), rb = h / (g.H / w.hb), rc = h / (g.H / w.hc);
+        const T* pa = static_cast<const T*>(w.a) + (b * g.L * w.ha + ra) * K;
+        const T* pb = static_cast<const T*>(w.b) + (b * g.L * w.hb + rb) * K;
+        const T* pc = static_cast<const T*>(w.c) + (b * g.L * w.hc + rc) * P;
+        const int sa = w.ha * K, sb = w.hb * K, sc = w.hc * P;  // elements from token to token
+        constexpr int RA = NS / (KD / V), RC = NS / (PT / V);   // rows from one of a thread's pieces to the next
+        const int ia = st / (KD / V), ca = st % (KD / V) * V, ic = st / (PT / V), cc = st % (PT / V) * V;
+        const int rowa = w.rev ? Q - 1 - ia - (NA - 1) * RA : ia, rowc = w.rev ? Q - 1 - ic - (NC - 1) * RC : ic;
+        const int va = ca < K ? (rowa * sa + ca) * ES : kInvalid, vb = ca < K ? (rowa * sb + ca) * ES : kInvalid;
+        const int vc = tile * PT + cc < P ? (rowc * sc + tile * PT + cc) * ES : kInvalid;
+        u32x4 ga[STATE ? 1 : NA], gb[NA], gc[NC];
+        auto load = [&](int c, int skip) {  // (past the last chunk: nothing, zeros)
+            const int64_t t0 = t_first + t_step * c;
+            const int on = c < nc ? ES : 0;
+            const auto ra_ = buf_rsrc(pa + t0 * sa, ((Q - 1) * sa + K) * on);
+            const auto rb_ = buf_rsrc(pb + t0 * sb, ((Q - 1) * sb + K) * on);
+            const auto rc_ = buf_rsrc(pc + t0 * sc, ((Q - 1) * sc + P) * on);
+            auto get = [](__amdgpu_buffer_rsrc_t r, int v, int s) {
+                return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, v, s, 0));
+            };
 #pragma unroll
-        for (int k = 0; k < NA; ++k) {
-            const int i = (tid + NTH * k) / (KD / V), col = (tid + NTH * k) % (KD / V) * V;
-            const int row = w.rev ? nv - 1 - i : i;
-            const bool ok = i < nv && col < K;
-            if (!STATE)
-                ga[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                      ra_, ok ? (row * sa + col) * int(sizeof(T)) : kInvalid, 0, 0));
-            gb[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  rb_, ok ? (row * sb + col) * int(sizeof(T)) : kInvalid, 0, 0));
-        }
+            for (int k = 0; k < NA; ++k) {
+                const int up_ = (w.rev ? NA - 1 - k : k) * RA;
+                const bool ok = ia + k * RA >= skip;
+                if (!STATE) ga[k] = get(ra_, ok ? va : kInvalid, up_ * sa * ES);
+                gb[k] = get(rb_, ok ? vb : kInvalid, up_ * sb * ES);
+            }
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int i = (tid + NTH * k) / (PT / V), col = tile * PT + (tid + NTH * k) % (PT / V) * V;
-            const int row = w.rev ? nv - 1 - i : i;
-            gc[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  rc_, i < nv && col < P ? (row * sc + col) * int(sizeof(T)) : kInvalid, 0, 0));
-        }
-    };
-    if (!STATE) {  // score tiles above the diagonal that an operand still covers stay zero
-        for (int i = tid; i < Q * Tile<T, Q>::kStride * int(sizeof(T)) / 16; i += NTH)
+            for (int k = 0; k < NC; ++k)
+                gc[k] = get(rc_, ic + k * RC >= skip ? vc : kInvalid, (w.rev ? NC - 1 - k : k) * RC * sc * ES);
+        };
+        auto stage = [&](int c) {
+            T* As = As2[STATE ? 0 : c & 1];
+            T* Bs = Bs2[c & 1];
+            T* Cs = Cs2[c & 1];
 #pragma unroll
-            for (int k = 0; k < NPS; ++k) reinterpret_cast<u32x4*>(Ps[k])[i] = u32x4{0, 0, 0, 0};
-    }
-    float total = 0.0f;  // SLOPE
-    if (nc > 0) load(0);
-    for (int c = 0; c < nc; ++c) {
-        const int nv = valid(c);
-        if (nv < Q) {
-            weights(nv);
-            keep = dec.pow(nv);
-        }
-        __syncthreads();  // the reads of the last chunk's tiles are done
+            for (int k = 0; k < NA; ++k) {
+                if (!STATE) *reinterpret_cast<u32x4*>(As + at<T, KD>(ia + k * RA, ca)) = ga[k];
+                *reinterpret_cast<u32x4*>(Bs + at<T, KD>(ia + k * RA, ca)) = gb[k];
+            }
 #pragma unroll
-        for (int k = 0; k < NA; ++k) {
-            const int i = (tid + NTH * k) / (KD / V), col = (tid + NTH * k) % (KD / V) * V;
-            if (!STATE) *reinterpret_cast<u32x4*>(As + at<T, KD>(i, col)) = ga[k];
-            *reinterpret_cast<u32x4*>(Bs + at<T, KD>(i, col)) = gb[k];
-        }
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int i = (tid + NTH * k) / (PT / V), col = (tid + NTH * k) % (PT / V) * V;
-            *reinterpret_cast<u32x4*>(Cs + at<T, PT>(i, col)) = gc[k];
-        }
-        load(c + 1);  // in flight during this chunk (nothing past the last one)
-        __syncthreads();
-
-        f32x4 o[TT], o2[SLOPE && !STATE ? TT : 1];
+            for (int k = 0; k < NC; ++k) *reinterpret_cast<u32x4*>(Cs + at<T, PT>(ic + k * RC, cc)) = gc[k];
+        };
+        load(0, skip0);
+        // powers of lambda inside a 16 x 16 tile of scores, by row minus column, and between tiles
+        float diag[4], base[4], pw16 = 0.0f, pw32 = 0.0f;
         if (!STATE) {
-            // ---- carry-in, transposed: o[p][t] = sum_n H[n][p] a[t][n] ----
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                o[t] = f32x4{};
-                if (SLOPE) o2[t] = f32x4{};
+            for (int r = 0; r < 4; ++r) {
+                const int d = m - 4 * gq - r;
+                diag[r] = d >= 0 ? g.scale * dec.pow(d) : 0.0f;
+                base[r] = g.scale * dec.pow(16 + d);
+            }
+            pw16 = dec.pow(16);
+            pw32 = dec.pow(32);
+            // score tiles above the diagonal that an operand still covers stay zero
+            for (int i = st; i < Q * Tile<T, Q>::kStride * ES / 16; i += NS)
+#pragma unroll
+                for (int k = 0; k < NPS; ++k) reinterpret_cast<u32x4*>(Ps[k])[i] = u32x4{0, 0, 0, 0};
+        }
+        // Scores of chunk c, transposed: a lane has 4 consecutive s of row t; tiles (t, s), s <= t, dealt to the waves.
+        auto scores = [&](int c) {
+            const T* As = As2[STATE ? 0 : c & 1];
+            const T* Bs = Bs2[c & 1];
+            constexpr int N = TT * (TT + 1) / 2, R = (N + kSupply - 1) / kSupply;
+            int ti[R], si[R];
+            f32x4 acc[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {  // (a wave without a last tile forms another's again, to the same values)
+                int n = r * kSupply + wv - NW;
+                n = n < N ? n : N - 1;
+                ti[r] = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3;
+                si[r] = n - ti[r] * (ti[r] + 1) / 2;
+                acc[r] = f32x4{};
             }
 #pragma unroll
             for (int kb = 0; kb < KD / KB; ++kb) {
-                Frag hs[O::TS], hd[O::TS];
-                float v[E];
+                Frag fa[R], fb[R];
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = S[BF ? 2 * kb + e / 4 : kb][e % 4];
-                O::split(v, hs);
-                if (SLOPE) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] = D[BF ? 2 * kb + e / 4 : kb][e % 4];
-                    O::split(v, hd);
+                for (int r = 0; r < R; ++r) {
+                    fb[r] = row_frag<T, KD>(Bs, 16 * si[r], KB * kb, lane);
+                    fa[r] = row_frag<T, KD>(As, 16 * ti[r], KB * kb, lane);
                 }
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const Frag f = row_frag<T, KD>(As, 16 * t, KB * kb, lane);
-#pragma unroll
-                    for (int k = 0; k < O::TS; ++k) {
-                        o[t] = O::mfma(hs[k], f, o[t]);
-                        if (SLOPE) o2[t] = O::mfma(hd[k], f, o2[t]);
-                    }
-                }
+                for (int r = 0; r < R; ++r) acc[r] = O::mfma(fb[r], fa[r], acc[r]);
             }
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                if (SLOPE) o2[t] = (o2[t] + o[t] * float(16 * t + m + 1)) * up[t];
-                o[t] *= up[t];
-            }
-            // ---- scores, transposed: lane has 4 consecutive s of row t; tiles (t, s), s <= t, dealt to the waves ----
-            for (int n = wv; n < TT * (TT + 1) / 2; n += NW) {
-                const int ti = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, si = n - ti * (ti + 1) / 2;
-                f32x4 acc = {};
-#pragma unroll
-                for (int kb = 0; kb < KD / KB; ++kb)
-                    acc = O::mfma(row_frag<T, KD>(Bs, 16 * si, KB * kb, lane), row_frag<T, KD>(As, 16 * ti, KB * kb, lane), acc);
-                const int t = 16 * ti + m, s = 16 * si + 4 * gq;
-                const float far = ti - si < 2 ? 1.0f : ti - si == 2 ? pw16 : pw32;
+            for (int i = 0; i < R; ++i) {
+                const int t = 16 * ti[i] + m, s = 16 * si[i] + 4 * gq, gap = ti[i] - si[i];
+                const float far = gap < 2 ? 1.0f : gap == 2 ? pw16 : pw32;
                 float v[4], v2[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     // (a masked score may be infinite or NaN: selected, not multiplied away)
-                    v[r] = ti == si ? (m >= 4 * gq + r ? acc[r] * diag[r] : 0.0f) : acc[r] * (base[r] * far);
+                    v[r] = gap == 0 ? (m >= 4 * gq + r ? acc[i][r] * diag[r] : 0.0f) : acc[i][r] * (base[r] * far);
                     v2[r] = v[r] * float(t - s - r);
                 }
-                auto put = [&](int first_tile, const float (&x)[4]) {
+                auto put = [&](int first_tile, int terms, const float (&x)[4]) {
                     if constexpr (BF) {
-                        float y[4];
+                        float y[4];  // (as split)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) y[r] = x[r];
 #pragma unroll
-                        for (int k = 0; k < O::TP; ++k) {
-                            const u32x2 q = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-                            *reinterpret_cast<u32x2*>(Ps[first_tile + k] + at<T, Q>(t, s)) = q;
-                            y[0] -= bf16_lo(q[0]); y[1] -= bf16_hi(q[0]);
-                            y[2] -= bf16_lo(q[1]); y[3] -= bf16_hi(q[1]);
+                        for (int k = 0; k < 3; ++k) {
+                            if (k >= terms) break;
+                            *reinterpret_cast<u32x2*>(Ps[first_tile + k] + at<T, Q>(t, s)) =
+                                k == 1 && terms == 2 ? u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])}
+                                                     : u32x2{O::upper_halves(y[0], y[1]), O::upper_halves(y[2], y[3])};
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) y[r] -= bf16_hi(__float_as_uint(y[r]));
                         }
                     } else {
                         *reinterpret_cast<f32x4*>(Ps[first_tile] + at<T, Q>(t, s)) = f32x4{x[0], x[1], x[2], x[3]};
                     }
                 };
-                put(0, v);
-                if (SLOPE) put(O::TP, v2);
+                put(0, TP, v);
+                if (SLOPE) put(TP, TD, v2);
+            }
+        };
+        // Outputs of chunk c: whole rows of the workgroup's columns.
+        const int so = int(g.H) * P;
+        auto store = [&](int c) {
+            const auto ro = buf_rsrc(static_cast<T*>(w.o) + ((b * g.L + t_first + t_step * c) * g.H + h) * P, ((Q - 1) * so + P) * ES);
+            const int skip = c == 0 ? skip0 : 0;
+            u32x4 x[NC];
+#pragma unroll
+            for (int k = 0; k < NC; ++k) x[k] = *reinterpret_cast<const u32x4*>(Os + (ic + k * RC) * SO + cc);
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                const int i = ic + k * RC, row = w.rev ? Q - 1 - i : i;
+                // (no scalar offset: see the compute waves' stores)
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    x[k], ro, i >= skip && tile * PT + cc < P ? (row * so + tile * PT + cc) * ES : kInvalid, 0, 0);
+            }
+        };
+        if (nc > 0) {
+            stage(0);
+            load(1, 0);
+            __syncthreads();
+            if (!STATE) {
+                scores(0);
+                __syncthreads();
+            }
+        }
+        for (int c = 0; c < nc; ++c) {
+            stage(c + 1);  // (past the last chunk: zeros that nothing reads)
+            load(c + 2, 0);
+            if (!STATE) {
+                __syncthreads();
+                if (VIA && !w.o_f32) store(c);
+                if (c + 1 < nc) scores(c + 1);
             }
             __syncthreads();
         }
-        // ---- outputs and state over the chunk's tokens ----
-        Frag cf[QB];
+    } else {
+        // ================================ compute ================================
+        const int e0 = w.rev ? 0 : 1, e1 = 1 - e0;
+        const float sc_carry = w.rev ? 1.0f : g.scale, sc_upd = w.rev ? g.scale : 1.0f;
+        // ---- state: tiles of 16 rows, one column of 16 per wave ----
+        // An accumulator pair becomes one bf16 operand if its rows are dealt out as
+        // n = 32 (kt / 2) + 8 (m / 4) + 4 (kt % 2) + m % 4.
+        auto row_of = [&](int kt, int r) { return BF ? 32 * (kt / 2) + 8 * gq + 4 * (kt % 2) + r : 16 * kt + 4 * gq + r; };
+        f32x4 S[KT];
+        f32x4 D[SLOPE ? KT : 1];
+        auto each_state = [&](auto f) {
+            const int p = col0 + m;
 #pragma unroll
-        for (int q = 0; q < QB; ++q) cf[q] = col_frag<T, PT>(Cs, KB * q, wv * 16, 4, lane);
-        if (!STATE) {
+            for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int q = 0; q < QB; ++q) {
-                    if (KB * q > 16 * t + 15) continue;
-#pragma unroll
-                    for (int k = 0; k < NPS; ++k) {
-                        const Frag f = row_frag<T, Q>(Ps[k], 16 * t, KB * q, lane);
-                        if (k < O::TP) o[t] = O::mfma(cf[q], f, o[t]);
-                        else o2[t] = O::mfma(cf[q], f, o2[t]);
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const int n = row_of(kt, r);
+                    f(kt, r, n, p, n < K && p < P);
                 }
-            // ---- store: token 16 t + m, columns 4 gq .. 4 gq + 3 of the wave's 16 ----
-            const int64_t t0 = first(c, nv);
-            const int64_t row0 = ((b * g.L + t0) * g.H + h) * P;
-            const int es = w.o_f32 ? 4 : int(sizeof(T));
-            const auto ro = buf_rsrc(static_cast<char*>(w.o) + row0 * es, nv > 0 ? ((nv - 1) * so + P) * es : 0);
-            const auto rf = buf_rsrc(SLOPE ? static_cast<const T*>(g.factor) + row0 : nullptr, SLOPE ? span(nv, so, P) : 0);
-            const int p = col0 + 4 * gq;
+        };
+        const int64_t run_at = (int64_t(role) * g.segments + seg) * g.run_stride + bh * K * P;  // STATE: of this run
+        {
+            // the output pass has one run more than the state pass
+            const int64_t from = (int64_t(role) * (g.segments - 1) + seg - 1) * g.run_stride + bh * K * P;
+            const bool own = seg == 0;
+            const float* src = own ? (w.s0 ? w.s0 + bh * K * P : nullptr) : STATE ? nullptr : g.run_state + from;
+            const int sn = own ? w.sn : P, sp = own ? w.sp : 1;
+            const float* dsrc = SLOPE && !STATE && !own ? g.run_slope + from : nullptr;
+            each_state([&](int kt, int r, int n, int p, bool ok) {
+                S[kt][r] = src && ok ? src[int64_t(n) * sn + int64_t(p) * sp] : 0.0f;
+                if (SLOPE) D[kt][r] = dsrc && ok ? dsrc[int64_t(n) * P + p] : 0.0f;
+            });
+        }
+
+        float up[TT];  // of the entering state in the outputs
+        if (!STATE)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const int i = 16 * t + m, row = w.rev ? nv - 1 - i : i;
-                const int off = i < nv && p < P ? row * so + p : -1;
+            for (int k = 0; k < TT; ++k) up[k] = sc_carry * dec.pow(16 * k + m + e0);
+        // weights of the chunk's tokens in the state: token KB q + s by we[s] wq[q]
+        float we[E], wq[QB];
+#pragma unroll
+        for (int e = 0; e < E; ++e) we[e] = dec.pow(KB - 1 - E * gq - e + e1);
+#pragma unroll
+        for (int q = 0; q < QB; ++q) wq[q] = sc_upd * dec.pow(KB * (QB - 1 - q));
+
+        float keep = dec.pow(Q);  // of the entering state over a chunk
+        const int so = int(g.H) * P, po = col0 + 4 * gq;  // a lane's 4 output columns
+        const int vo = po < P ? (w.rev ? 15 - m : m) * so + po : kInvalid;  // (elements)
+        if (nc > 0) {
+            __syncthreads();
+            if (!STATE) __syncthreads();
+        }
+        for (int c = 0; c < nc; ++c) {
+            const int skip = c == 0 ? skip0 : 0, nv = Q - skip;
+            const T* As = As2[STATE ? 0 : c & 1];
+            const T* Bs = Bs2[c & 1];
+            const T* Cs = Cs2[c & 1];
+            if (c < 2 && skip0 > 0) {  // into, and out of, the partial chunk
+                keep = dec.pow(nv);
+                if (!STATE)
+#pragma unroll
+                    for (int k = 0; k < TT; ++k) {
+                        const int n = 16 * k + m - skip;
+                        up[k] = sc_carry * dec.pow((n > 0 ? n : 0) + e0);
+                    }
+            }
+            Frag cf[QB];
+#pragma unroll
+            for (int q = 0; q < QB; ++q) cf[q] = col_frag<T, PT>(Cs, KB * q, wv * 16, 4, lane);
+            if (!STATE) {
+                // ---- carry-in, transposed: o[p][t] = sum_n H[n][p] a[t][n] ----
+                f32x4 o[TT], o2[SLOPE ? TT : 1];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    o[t] = f32x4{};
+                    if (SLOPE) o2[t] = f32x4{};
+                }
+#pragma unroll
+                for (int kb = 0; kb < KD / KB; ++kb) {
+                    Frag hs[TS], f[TT];
+                    float v[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] = S[BF ? 2 * kb + e / 4 : kb][e % 4];
+                    O::template split<TS, true>(v, hs);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) f[t] = row_frag<T, KD>(As, 16 * t, KB * kb, lane);
+                    // (consecutive products go to different accumulators; the slope's third term apart)
+#pragma unroll
+                    for (int k = 0; k < TS; ++k)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) {
+                            if (k < O::TS) o[t] = O::mfma(hs[k], f[t], o[t]);
+                            else o2[t] = O::mfma(hs[k], f[t], o2[t]);
+                        }
+                }
                 if (SLOPE) {
-                    const int fo = off >= 0 ? off * int(sizeof(T)) : kInvalid;
-                    f32x4 f;
-                    if constexpr (BF) {
-                        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rf, fo, 0, 0));
-                        f = f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
-                    } else {
-                        f = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rf, fo, 0, 0));
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) o2[t] = (o2[t] + o[t]) * float(16 * t + m - skip + 1);
+#pragma unroll
+                    for (int kb = 0; kb < KD / KB; ++kb) {
+                        Frag hd[TS], f[TT];
+                        float v[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) v[e] = D[BF ? 2 * kb + e / 4 : kb][e % 4];
+                        O::template split<TS, true>(v, hd);
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) f[t] = row_frag<T, KD>(As, 16 * t, KB * kb, lane);
+#pragma unroll
+                        for (int k = 0; k < TS; ++k)
+#pragma unroll
+                            for (int t = 0; t < TT; ++t) o2[t] = O::mfma(hd[k], f[t], o2[t]);
                     }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) total = off >= 0 ? fmaf(o2[t][r], f[r], total) : total;
                 }
-                if (!BF || w.o_f32) {
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[t]), ro, off >= 0 ? off * 4 : kInvalid, 0, 0);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    if (SLOPE) o2[t] *= up[t];
+                    o[t] *= up[t];
+                }
+                // ---- scores times c ----
+#pragma unroll
+                for (int q = 0; q < QB; ++q)
+#pragma unroll
+                    for (int k = 0; k < NPS; ++k)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) {
+                            if (KB * q > 16 * t + 15) continue;
+                            const Frag f = row_frag<T, Q>(Ps[k], 16 * t, KB * q, lane);
+                            if (k < TP) o[t] = O::mfma(cf[q], f, o[t]);
+                            else o2[t] = O::mfma(cf[q], f, o2[t]);
+                        }
+                // ---- store: token 16 t + m, columns 4 gq .. 4 gq + 3 of the wave's 16 ----
+                const int64_t row0 = ((b * g.L + t_first + t_step * c) * g.H + h) * P;
+                if constexpr (SLOPE) {
+                    const auto rf = buf_rsrc(static_cast<const T*>(g.factor) + row0, ((Q - 1) * so + P) * ES);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        const bool ok = vo >= 0 && 16 * t + m >= skip;
+                        const int fo = ok ? (vo + (w.rev ? TT - 1 - t : t) * 16 * so) * ES : kInvalid;
+                        f32x4 f;
+                        if constexpr (BF) {
+                            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rf, fo, 0, 0));
+                            f = f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
+                        } else {
+                            f = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rf, fo, 0, 0));
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) total = ok ? fmaf(o2[t][r], f[r], total) : total;
+                    }
+                }
+                if (VIA && !w.o_f32) {
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+                        *reinterpret_cast<u32x2*>(Os + (16 * t + m) * SO + wv * 16 + 4 * gq) =
+                            u32x2{pack_bf16x2(o[t][0], o[t][1]), pack_bf16x2(o[t][2], o[t][3])};
                 } else {
-                    const u32x2 q = {pack_bf16x2(o[t][0], o[t][1]), pack_bf16x2(o[t][2], o[t][3])};
-                    __builtin_amdgcn_raw_buffer_store_b64(q, ro, off >= 0 ? off * 2 : kInvalid, 0, 0);
+                    const auto ro = buf_rsrc(static_cast<char*>(w.o) + row0 * oes, ((Q - 1) * so + P) * oes);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        // The row offset goes into the lane's offset, not into a scalar one: with a
+                        // scalar offset the compiler lets the next instruction overwrite the 16
+                        // bytes' registers, and gfx950 has then stored the new value (seen: the
+                        // first of the four).
+                        const bool ok = vo >= 0 && 16 * t + m >= skip;
+                        const int at_ = ok ? (vo + (w.rev ? TT - 1 - t : t) * 16 * so) * oes : kInvalid;
+                        if (BF && !w.o_f32)
+                            __builtin_amdgcn_raw_buffer_store_b64(
+                                u32x2{pack_bf16x2(o[t][0], o[t][1]), pack_bf16x2(o[t][2], o[t][3])}, ro, at_, 0, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[t]), ro, at_, 0, 0);
+                    }
                 }
+                __syncthreads();
             }
-        }
-        // ---- state: H <- lambda^n H + B^T (w c) ----
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            if (SLOPE) D[kt] = (D[kt] + S[kt] * float(nv)) * keep;
-            S[kt] *= keep;
-        }
-#pragma unroll
-        for (int q = 0; q < QB; ++q) {
-            Frag cw[O::TU], cd[O::TU];
-            float v[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = wt[q][e] * O::value(cf[q], e);
-            O::split(v, cw);
-            if (SLOPE) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] *= float(nv - 1 - (KB * q + E * gq + e) + e1);
-                O::split(v, cd);
-            }
+            // ---- state: H <- lambda^n H + B^T (w c) ----
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
-                const Frag f = BF ? col_frag<T, KD>(Bs, KB * q, 32 * (kt / 2) + 4 * (kt % 2), 8, lane)
-                                  : col_frag<T, KD>(Bs, KB * q, 16 * kt, 4, lane);
+                if (SLOPE) D[kt] = (D[kt] + S[kt] * float(nv)) * keep;
+                S[kt] *= keep;
+            }
 #pragma unroll
-                for (int k = 0; k < O::TU; ++k) {
-                    S[kt] = O::mfma(f, cw[k], S[kt]);
-                    if (SLOPE) D[kt] = O::mfma(f, cd[k], D[kt]);
+            for (int q = 0; q < QB; ++q) {
+                Frag cw[O::TU], cd[O::TU];
+                float v[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = we[e] * wq[q] * O::value(cf[q], e);
+                O::template split<O::TU, false>(v, cw);
+                if (SLOPE) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] *= float(Q - 1 - (KB * q + E * gq + e) + e1);
+                    O::template split<O::TU, false>(v, cd);
+                }
+#pragma unroll
+                for (int kt = 0; kt < KT; kt += 4) {
+                    Frag f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f[i] = BF ? col_frag<T, KD>(Bs, KB * q, 32 * ((kt + i) / 2) + 4 * (i % 2), 8, lane)
+                                  : col_frag<T, KD>(Bs, KB * q, 16 * (kt + i), 4, lane);
+#pragma unroll
+                    for (int k = 0; k < O::TU; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            S[kt + i] = O::mfma(f[i], cw[k], S[kt + i]);
+                            if (SLOPE) D[kt + i] = O::mfma(f[i], cd[k], D[kt + i]);
+                        }
                 }
             }
+            __syncthreads();
         }
-    }
 
-    // ---- the state leaving the run ----
-    if (STATE) {
-        each_state([&](int kt, int r, int n, int p, bool ok) {
-            if (ok) {
-                g.run_state[run_at + int64_t(n) * P + p] = S[kt][r];
-                if (SLOPE) g.run_slope[run_at + int64_t(n) * P + p] = D[kt][r];
+        // ---- the state leaving the run ----
+        if (STATE) {
+            each_state([&](int kt, int r, int n, int p, bool ok) {
+                if (ok) {
+                    g.run_state[run_at + int64_t(n) * P + p] = S[kt][r];
+                    if (SLOPE) g.run_slope[run_at + int64_t(n) * P + p] = D[kt][r];
+                }
+            });
+        } else if (seg == g.segments - 1) {
+            if (w.s1) {
+                float* dst = w.s1 + bh * K * P;
+                each_state([&](int kt, int r, int n, int p, bool ok) {
+                    if (ok) dst[int64_t(n) * w.sn + int64_t(p) * w.sp] = S[kt][r];
+                });
             }
-        });
-        return;
-    }
-    if (seg == g.segments - 1) {
-        if (w.s1) {
-            float* dst = w.s1 + bh * K * P;
-            each_state([&](int kt, int r, int n, int p, bool ok) {
-                if (ok) dst[int64_t(n) * w.sn + int64_t(p) * w.sp] = S[kt][r];
-            });
-        }
-        if (SLOPE && g.dlast) {
-            const float* src = g.dlast + bh * K * P;
-            each_state([&](int kt, int r, int n, int p, bool ok) {
-                if (ok) total = fmaf(D[kt][r], src[int64_t(n) * w.sn + int64_t(p) * w.sp], total);
-            });
+            if (SLOPE && g.dlast) {
+                const float* src = g.dlast + bh * K * P;
+                each_state([&](int kt, int r, int n, int p, bool ok) {
+                    if (ok) total = fmaf(D[kt][r], src[int64_t(n) * w.sn + int64_t(p) * w.sp], total);
+                });
+            }
         }
     }
+    if (STATE) return;
     // ---- zeros behind the entry's tokens, as far as they lie in this run's stretch ----
     if (len < g.L && len < p0 + g.seg_len) {
         const int64_t z0 = len > p0 ? len : p0, z1 = p0 + g.seg_len < g.L ? p0 + g.seg_len : g.L;
@@ -530,7 +666,7 @@ __global__ __launch_bounds__(PT * 4, WPE) void walk_kernel(WalkArgs g) {
 #pragma unroll
         for (int x = 32; x; x >>= 1) total += __shfl_xor(total, x, 64);
         __syncthreads();
-        if (lane == 0) red[wv] = total;
+        if (lane == 0 && wv < NW) red[wv] = total;
         __syncthreads();
         // [batch][H][segment * tiles + tile]
         if (tid == 0) {
@@ -625,15 +761,12 @@ __global__ __launch_bounds__(256) void carry_kernel(CarryArgs g) {
     }
 }
 
-// Registers of two waves a SIMD hold a walk; the slope's second state at widths
-// over 64 takes those of one (its workgroups have 4 waves then).
 template <typename T, int Q, int KD, int PT, bool SLOPE>
 void launch_walk(WalkArgs g, int64_t bh, bool state, hipStream_t st) {
-    constexpr int WPE = PT == 64 && (KD == 256 || (SLOPE && KD == 128)) ? 1 : 2;
     if (state) --g.segments;
-    const dim3 grid(unsigned(bh * g.segments * g.roles * g.tiles)), block(PT * 4);
-    if (state) hipLaunchKernelGGL((walk_kernel<T, Q, KD, PT, true, SLOPE, WPE>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((walk_kernel<T, Q, KD, PT, false, SLOPE, WPE>), grid, block, 0, st, g);
+    const dim3 grid(unsigned(bh * g.segments * g.roles * g.tiles)), block(PT * 4 + kSupply * 64);
+    if (state) hipLaunchKernelGGL((walk_kernel<T, Q, KD, PT, true, SLOPE>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((walk_kernel<T, Q, KD, PT, false, SLOPE>), grid, block, 0, st, g);
 }
 template <typename T, int Q, int KD>
 void launch_walk_pt(const WalkArgs& g, int64_t bh, int pt, bool state, bool slope, hipStream_t st) {
@@ -752,15 +885,22 @@ hipError_t bwd(const LinattnTensors& t, const LinattnShape& s, const LinattnPlan
 
 }  // namespace
 
+// Runs: a workgroup fills a CU (its LDS), and a second round of workgroups
+// costs as much as the first, while the state pass and the carries of runs
+// cost about as much as half the outputs. So a launch that leaves CUs idle is
+// cut into as many runs as still fit one round of the 256 CUs, of 128 tokens
+// at least (measured, us at 1, 2, 4, 8, 16, 32 runs: b1 L32771, 16 heads of 128
+// 1670 1166 597 315 200 226; b1 L2048, 16 heads 114 93 60 46 43 68; b4 L2048,
+// 32 heads 117 105 135 182; b8, 32 heads 160 201 267).
 LinattnPlan linattn_plan(const LinattnShape& s, int32_t requested, bool backward) {
     int64_t S = requested;
     if (S == 0) {
-        S = 1;
-        const int64_t groups = s.batch * s.heads * ((s.dv + 127) / 128) * (backward ? 2 : 1);
-        if (groups > 0 && groups < 512) S = (512 + groups - 1) / groups;
-        const int64_t most = s.L / (4 * kRun);
+        // the backward's launches hold the walks of dk and dv, or one walk and its slope by halves
+        const int64_t wide = backward && s.dk > s.dv ? s.dk : s.dv;
+        const int64_t groups = s.batch * s.heads * ((wide + 127) / 128) * (backward && s.dk == s.dv ? 2 : 1);
+        S = groups > 0 ? 256 / groups : 1;
+        const int64_t most = s.L / 128;
         if (S > most) S = most;
-        if (S > 1024) S = 1024;
         if (S < 1) S = 1;
     }
     LinattnPlan p{1, s.L};
