@@ -34,7 +34,7 @@ struct GnArgs {
     // work split
     int32_t D, lanes;   // channels of a group; vectors of a row of it
     int32_t sub, gb;    // rows kernel: lanes of an instance, groups of a workgroup
-    int64_t per;        // rows kernel: rows of a workgroup; block kernel: rows of a slab
+    int64_t per;        // rows kernel: rows of a workgroup; block kernel: entries of a run, or rows of a slab
     int32_t slabs;
     float* stats;       // per instance and slab: (mean, M2), backward (sum e, sum e xh)
     float* part;        // partial column sums: [part][2][C] of du xh and du; null: not wanted
@@ -102,6 +102,18 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     float s = red[0];
     for (int i = 1; i < waves; ++i) s += red[i];
     return s;
+}
+
+// cols[0][i] = the sum over r < n of cols[r][i], i < width: halves folded onto
+// each other, a fixed order. Called by all threads.
+__device__ __forceinline__ void fold_rows(float* cols, int n, int width) {
+    while (n > 1) {
+        const int half = (n + 1) / 2;
+        __syncthreads();
+        for (int i = threadIdx.x; i < (n - half) * width; i += blockDim.x) cols[i] += cols[half * width + i];
+        n = half;
+    }
+    __syncthreads();
 }
 
 // ---- rows: S = 1 ----------------------------------------------------------------
@@ -235,12 +247,8 @@ __global__ __launch_bounds__(256) void rows_kernel(GnArgs a) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
                         cols[ri * width + gi * a.D + (l + a.sub * k) * V + i] = which ? sb[k][i] : sw[k][i];
-            __syncthreads();
-            for (int c = tid; c < width && c < have; c += 256) {
-                float s = cols[c];
-                for (int r = 1; r < step; ++r) s += cols[r * width + c];
-                out[which * a.C + c] = s;
-            }
+            fold_rows(cols, step, width);
+            for (int c = tid; c < width && c < have; c += 256) out[which * a.C + c] = cols[c];
         }
     }
 }
@@ -250,177 +258,184 @@ __global__ __launch_bounds__(256) void rows_kernel(GnArgs a) {
 // Thread (r, v) takes vector v of rows r, r + rs, ... of the slab, K of them in
 // registers; threads past the last whole row idle.
 enum { kFused = 0, kStats = 1, kApply = 2 };
-constexpr int kFwdK = 8, kBwdK = 4;
+// Vectors of V values a thread holds of each tensor: 32 values (16 of the three
+// tensors of a gated backward), which the registers of 16 waves a CU take; and
+// two where that is enough, for more waves.
+constexpr int held(bool bwd, bool gate, int V) {
+    const int k = (bwd && gate ? 16 : 32) / V;
+    return k < 16 ? k : 16;
+}
 
-template <typename T, int V, bool BWD, int MODE>
+// Where a whole instance fits (kFused), a workgroup takes `per` entries of its
+// group one after the other, the weights kept and the column sums joined once.
+template <typename T, int V, int K, bool BWD, bool GATE, int MODE>
 __global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
-    constexpr int K = BWD ? kBwdK : kFwdK;
     __shared__ float red[16];
     __shared__ float cols[BWD && MODE != kApply ? 1024 * V : 1];
     const int tid = threadIdx.x, rs = int(blockDim.x) / a.lanes, r0 = tid / a.lanes, v = tid % a.lanes;
-    const int64_t inst = blockIdx.x / a.slabs, slab = blockIdx.x % a.slabs;
-    const int64_t n = inst / a.G, g = inst % a.G;
-    const int64_t s0 = slab * a.per, s1 = s0 + a.per < a.S ? s0 + a.per : a.S;
-    const bool gate = a.act == SELSCAN_ACT_GATE, live = r0 < rs;
+    // kFused: group g of entries n0 .. n1 - 1; else slab `slab` of instance (n0, g)
+    const int64_t slab = MODE == kFused ? 0 : blockIdx.x % a.slabs, unit = MODE == kFused ? blockIdx.x : blockIdx.x / a.slabs;
+    const int64_t g = unit % a.G, n0 = MODE == kFused ? unit / a.G * a.per : unit / a.G;
+    const int64_t n1 = MODE != kFused ? n0 + 1 : n0 + a.per < a.N ? n0 + a.per : a.N;
+    const int64_t s0 = MODE == kFused ? 0 : slab * a.per;
+    const int64_t s1 = MODE == kFused || s0 + a.per > a.S ? a.S : s0 + a.per;
+    const bool live = r0 < rs;
     const int64_t c = g * a.D + int64_t(v) * V;
-    const int64_t base = n * a.S * a.C + c;
-    raw_t<T, V> x[K], z[K], dy[K];
-    bool in[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int64_t s = s0 + r0 + int64_t(rs) * k;
-        in[k] = live && s < s1;
-        if (!in[k]) continue;
-        x[k] = load_raw<T, V>(a.x, base + s * a.C);
-        if ((BWD || MODE != kStats) && gate) z[k] = load_raw<T, V>(a.z, base + s * a.C);
-        if (BWD) dy[k] = load_raw<T, V>(a.dy, base + s * a.C);
-    }
-    auto values = [&](const raw_t<T, V>& r, float (&f)[V]) { unpack<T, V>(r, f); };
     const float cnt = float(s1 - s0) * float(a.D), all = float(a.S) * float(a.D);
-    float w[V], b[V];
+    float w[V], b[V], sw[BWD ? V : 1], sb[BWD ? V : 1];
     if (BWD || MODE != kStats) {
         load_affine<V>(live ? a.weight : nullptr, c, 1.0f, w);
         load_affine<V>(live ? a.bias : nullptr, c, 0.0f, b);
     }
-    if (!BWD) {
-        float mean, var;
-        if (MODE != kApply) {
-            float s = 0.0f;
+    if (BWD)
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float f[V];
-                if (!in[k]) continue;
-                values(x[k], f);
-#pragma unroll
-                for (int i = 0; i < V; ++i) s += f[i];
-            }
-            mean = block_sum(s, red) / cnt;
-            s = 0.0f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float f[V];
-                if (!in[k]) continue;
-                values(x[k], f);
-#pragma unroll
-                for (int i = 0; i < V; ++i) s = fmaf(f[i] - mean, f[i] - mean, s);
-            }
-            var = block_sum(s, red);
-            if (MODE == kStats) {
-                if (tid == 0) {
-                    a.stats[2 * int64_t(blockIdx.x)] = mean;
-                    a.stats[2 * int64_t(blockIdx.x) + 1] = var;
-                }
-                return;
-            }
-        } else {
-            const float* st = a.stats + 2 * inst * a.slabs;
-            auto rows = [&](int i) { return float(i + 1 < a.slabs ? a.per : a.S - int64_t(i) * a.per) * float(a.D); };
-            float s = 0.0f;
-            for (int i = tid; i < a.slabs; i += blockDim.x) s = fmaf(st[2 * i], rows(i), s);
-            mean = block_sum(s, red) / all;
-            s = 0.0f;
-            for (int i = tid; i < a.slabs; i += blockDim.x) {
-                const float d = st[2 * i] - mean;
-                s += fmaf(d * d, rows(i), st[2 * i + 1]);
-            }
-            var = block_sum(s, red);
-        }
-        const float rstd = 1.0f / sqrtf(var / all + a.eps);
-        if (a.mean && slab == 0 && tid == 0) {
-            a.mean[inst] = mean;
-            a.rstd[inst] = rstd;
-        }
+        for (int i = 0; i < V; ++i) sw[i] = sb[i] = 0.0f;
+    for (int64_t n = n0; n < n1; ++n) {
+        const int64_t inst = n * a.G + g, base = n * a.S * a.C + c;
+        raw_t<T, V> x[K], z[GATE ? K : 1], dy[BWD ? K : 1];
+        bool in[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            const int64_t s = s0 + r0 + int64_t(rs) * k;
+            in[k] = live && s < s1;
             if (!in[k]) continue;
-            float f[V], zz[V], y[V];
-            values(x[k], f);
-            if (gate) values(z[k], zz);
-#pragma unroll
-            for (int i = 0; i < V; ++i) y[i] = activate(fmaf((f[i] - mean) * rstd, w[i], b[i]), a.act, gate ? zz[i] : 0.0f);
-            store_vec<T, V>(a.y, base + (s0 + r0 + int64_t(rs) * k) * a.C, y);
+            x[k] = load_raw<T, V>(a.x, base + s * a.C);
+            if ((BWD || MODE != kStats) && GATE) z[k] = load_raw<T, V>(a.z, base + s * a.C);
+            if (BWD) dy[k] = load_raw<T, V>(a.dy, base + s * a.C);
         }
-    } else {
-        const float mean = a.mean[inst], rstd = a.rstd[inst];
-        // xh, du and dz of vector k
-        auto grads = [&](int k, float (&xh)[V], float (&du)[V], float (&dz)[V]) {
-            float f[V], zz[V], gy[V];
-            values(x[k], f);
-            values(dy[k], gy);
-            if (gate) values(z[k], zz);
+        if constexpr (!BWD) {
+            float mean, var;
+            if (MODE != kApply) {
+                float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                xh[i] = (f[i] - mean) * rstd;
-                du[i] = grad_u(a.act, fmaf(xh[i], w[i], b[i]), gy[i], gate ? zz[i] : 0.0f, &dz[i]);
+                for (int k = 0; k < K; ++k) {
+                    float f[V];
+                    if (!in[k]) continue;
+                    unpack<T, V>(x[k], f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s += f[i];
+                }
+                mean = block_sum(s, red) / cnt;
+                s = 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    float f[V];
+                    if (!in[k]) continue;
+                    unpack<T, V>(x[k], f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s = fmaf(f[i] - mean, f[i] - mean, s);
+                }
+                var = block_sum(s, red);
+                if (MODE == kStats) {
+                    if (tid == 0) {
+                        a.stats[2 * int64_t(blockIdx.x)] = mean;
+                        a.stats[2 * int64_t(blockIdx.x) + 1] = var;
+                    }
+                    return;
+                }
+            } else {
+                const float* st = a.stats + 2 * inst * a.slabs;
+                auto rows = [&](int i) { return float(i + 1 < a.slabs ? a.per : a.S - int64_t(i) * a.per) * float(a.D); };
+                float s = 0.0f;
+                for (int i = tid; i < a.slabs; i += blockDim.x) s = fmaf(st[2 * i], rows(i), s);
+                mean = block_sum(s, red) / all;
+                s = 0.0f;
+                for (int i = tid; i < a.slabs; i += blockDim.x) {
+                    const float d = st[2 * i] - mean;
+                    s += fmaf(d * d, rows(i), st[2 * i + 1]);
+                }
+                var = block_sum(s, red);
             }
-        };
-        float m1, m2;
-        if (MODE != kApply) {
-            float s1_ = 0.0f, s2_ = 0.0f, sw[V], sb[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) sw[i] = sb[i] = 0.0f;
+            const float rstd = 1.0f / sqrtf(var / all + a.eps);
+            if (a.mean && slab == 0 && tid == 0) {
+                a.mean[inst] = mean;
+                a.rstd[inst] = rstd;
+            }
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!in[k]) continue;
-                float xh[V], du[V], dz[V];
-                grads(k, xh, du, dz);
+                float f[V], zz[V], y[V];
+                unpack<T, V>(x[k], f);
+                if constexpr (GATE) unpack<T, V>(z[k], zz);
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] = activate(fmaf((f[i] - mean) * rstd, w[i], b[i]), a.act, GATE ? zz[i] : 0.0f);
+                store_vec<T, V>(a.y, base + (s0 + r0 + int64_t(rs) * k) * a.C, y);
+            }
+        } else {
+            const float mean = a.mean[inst], rstd = a.rstd[inst];
+            // xh, du and dz of vector k
+            auto grads = [&](int k, float (&xh)[V], float (&du)[V], float (&dz)[V]) {
+                float f[V], zz[V], gy[V];
+                unpack<T, V>(x[k], f);
+                unpack<T, V>(dy[k], gy);
+                if constexpr (GATE) unpack<T, V>(z[k], zz);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    sw[i] = fmaf(du[i], xh[i], sw[i]);
-                    sb[i] += du[i];
+                    xh[i] = (f[i] - mean) * rstd;
+                    du[i] = grad_u(a.act, fmaf(xh[i], w[i], b[i]), gy[i], GATE ? zz[i] : 0.0f, &dz[i]);
                 }
-            }
+            };
+            float m1, m2;
+            if (MODE != kApply) {
+                float p1 = 0.0f, p2 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                s1_ = fmaf(sb[i], w[i], s1_);
-                s2_ = fmaf(sw[i], w[i], s2_);
-            }
-            m1 = block_sum(s1_, red);
-            m2 = block_sum(s2_, red);
-            if (a.part) {  // this slab's column sums, its rows joined in order
-                float* out = a.part + (n * a.slabs + slab) * 2 * a.C + g * a.D;
-                for (int which = 0; which < 2; ++which) {
-                    __syncthreads();
-                    if (live)
+                for (int k = 0; k < K; ++k) {
+                    if (!in[k]) continue;
+                    float xh[V], du[V], dz[V];
+                    grads(k, xh, du, dz);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) cols[(r0 * a.lanes + v) * V + i] = which ? sb[i] : sw[i];
-                    __syncthreads();
-                    for (int i = tid; i < a.D; i += blockDim.x) {
-                        float s = cols[i];
-                        for (int r = 1; r < rs; ++r) s += cols[r * a.D + i];
-                        out[which * a.C + i] = s;
+                    for (int i = 0; i < V; ++i) {
+                        p1 = fmaf(du[i], w[i], p1);
+                        p2 = fmaf(du[i] * w[i], xh[i], p2);
+                        sw[i] = fmaf(du[i], xh[i], sw[i]);
+                        sb[i] += du[i];
                     }
                 }
-            }
-            if (MODE == kStats) {
-                if (tid == 0) {
+                m1 = block_sum(p1, red);
+                m2 = block_sum(p2, red);
+                if (MODE == kStats && tid == 0) {
                     a.stats[2 * int64_t(blockIdx.x)] = m1;
                     a.stats[2 * int64_t(blockIdx.x) + 1] = m2;
                 }
-                return;
+            } else {
+                const float* st = a.stats + 2 * inst * a.slabs;
+                float p1 = 0.0f, p2 = 0.0f;
+                for (int i = tid; i < a.slabs; i += blockDim.x) {
+                    p1 += st[2 * i];
+                    p2 += st[2 * i + 1];
+                }
+                m1 = block_sum(p1, red);
+                m2 = block_sum(p2, red);
             }
-        } else {
-            const float* st = a.stats + 2 * inst * a.slabs;
-            float p1 = 0.0f, p2 = 0.0f;
-            for (int i = tid; i < a.slabs; i += blockDim.x) {
-                p1 += st[2 * i];
-                p2 += st[2 * i + 1];
+            m1 /= all;
+            m2 /= all;
+            if (MODE != kStats) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (!in[k]) continue;
+                    float xh[V], du[V], dz[V], dx[V];
+                    grads(k, xh, du, dz);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) dx[i] = rstd * (du[i] * w[i] - m1 - xh[i] * m2);
+                    const int64_t at = base + (s0 + r0 + int64_t(rs) * k) * a.C;
+                    store_vec<T, V>(a.dx, at, dx);
+                    if (GATE) store_vec<T, V>(a.dz, at, dz);
+                }
             }
-            m1 = block_sum(p1, red);
-            m2 = block_sum(p2, red);
         }
-        m1 /= all;
-        m2 /= all;
+    }
+    if constexpr (BWD && MODE != kApply) {
+        if (a.part) {  // the column sums, the threads' rows joined in a fixed order
+            const int64_t at = MODE == kFused ? unit / a.G : n0 * a.slabs + slab;
+            float* out = a.part + at * 2 * a.C + g * a.D;
+            for (int which = 0; which < 2; ++which) {
+                __syncthreads();
+                if (live)
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (!in[k]) continue;
-            float xh[V], du[V], dz[V], dx[V];
-            grads(k, xh, du, dz);
-#pragma unroll
-            for (int i = 0; i < V; ++i) dx[i] = rstd * (du[i] * w[i] - m1 - xh[i] * m2);
-            const int64_t at = base + (s0 + r0 + int64_t(rs) * k) * a.C;
-            store_vec<T, V>(a.dx, at, dx);
-            if (gate) store_vec<T, V>(a.dz, at, dz);
+                    for (int i = 0; i < V; ++i) cols[(r0 * a.lanes + v) * V + i] = which ? sb[i] : sw[i];
+                fold_rows(cols, rs, a.D);
+                for (int i = tid; i < a.D; i += blockDim.x) out[which * a.C + i] = cols[i];
+            }
         }
     }
 }
@@ -505,26 +520,30 @@ __global__ __launch_bounds__(256) void plain_cols_kernel(GnArgs a) {
     a.part[(int64_t(blockIdx.x) * 2 + 1) * a.C + c] = sb;
 }
 
-// dweight (y 0) and dbias (y 1): the partial sums of 16 interleaved rows of
-// parts, joined in order; 64 columns per workgroup.
+// Column sums over runs of kJoin parts (grid z), 16 interleaved rows of them
+// joined in order; 64 columns per workgroup, du xh (y 0) and du (y 1). The
+// last stage (one run) writes dweight and dbias, the others out[run][2][C].
+constexpr int kJoin = 256;
 __global__ __launch_bounds__(1024) void cols_sum_kernel(const float* __restrict__ part, int parts, int64_t C,
-                                                        float* __restrict__ dweight, float* __restrict__ dbias) {
+                                                        float* __restrict__ out, float* __restrict__ dweight,
+                                                        float* __restrict__ dbias) {
     __shared__ float red[16][64];
-    const int col = threadIdx.x % 64, r = threadIdx.x / 64;
+    const int col = threadIdx.x % 64, r = threadIdx.x / 64, run = blockIdx.z;
     const int64_t c = int64_t(blockIdx.x) * 64 + col;
-    float* out = blockIdx.y ? dbias : dweight;
-    if (!out) return;
+    float* to = out ? out + (int64_t(run) * 2 + blockIdx.y) * C : blockIdx.y ? dbias : dweight;
+    if (!to) return;
+    const int k1 = (run + 1) * kJoin < parts ? (run + 1) * kJoin : parts;
     float s = 0.0f;
     if (c < C) {
 #pragma unroll 4
-        for (int k = r; k < parts; k += 16) s += part[(int64_t(k) * 2 + blockIdx.y) * C + c];
+        for (int k = run * kJoin + r; k < k1; k += 16) s += part[(int64_t(k) * 2 + blockIdx.y) * C + c];
     }
     red[r][col] = s;
     __syncthreads();
     if (r == 0 && c < C) {
 #pragma unroll
         for (int k = 1; k < 16; ++k) s += red[k][col];
-        out[c] = s;
+        to[c] = s;
     }
 }
 
@@ -532,7 +551,7 @@ __global__ __launch_bounds__(1024) void cols_sum_kernel(const float* __restrict_
 
 struct Plan {
     enum Kind { kRows, kBlock, kPlain } kind;
-    int V, KV;
+    int V, KV;  // values of a vector; vectors a thread holds
     int sub, gb;
     int64_t per;
     int slabs, threads;
@@ -566,16 +585,24 @@ Plan plan_of(const GroupnormShape& s, bool bwd) {
         p.parts = ceil_div(s.N, p.per);
     } else if (lanes <= 1024) {
         p.kind = Plan::kBlock;
-        const int K = bwd ? kBwdK : kFwdK;
+        const int K = held(bwd, s.act == SELSCAN_ACT_GATE, p.V);
         // threads for two vectors each, whole waves, at least one row
         int64_t t = ceil_div(s.S * lanes, 2);
         t = t < lanes ? lanes : t;
         t = t > 1024 ? 1024 : t;
         p.threads = int(ceil_div(t, 64) * 64);
         const int64_t rs = p.threads / lanes;
-        p.per = rs * K;
-        p.slabs = int(ceil_div(s.S, p.per));
-        p.parts = s.N * p.slabs;
+        p.slabs = int(ceil_div(s.S, rs * K));
+        p.KV = s.S <= 2 * rs ? 2 : K;
+        if (p.slabs == 1) {
+            // runs of entries: workgroups for the threads the chip holds, twice those in the forward
+            const int64_t want = ceil_div(int64_t(256) * (bwd ? 2048 : 4096) / p.threads, s.G);
+            p.per = ceil_div(s.N, want);
+            p.parts = ceil_div(s.N, p.per);
+        } else {
+            p.per = rs * K;
+            p.parts = s.N * p.slabs;
+        }
     } else {
         p.kind = Plan::kPlain;
         p.threads = 1024;
@@ -602,6 +629,21 @@ GnArgs args_of(const GroupnormTensors& t, const GroupnormShape& s, const Plan& p
     return a;
 }
 
+template <typename T, int V, bool BWD, bool GATE>
+void launch_block(const GnArgs& a, const Plan& p, hipStream_t st) {
+    constexpr int K = held(BWD, GATE, V);
+    const dim3 block(unsigned(p.threads));
+    if (a.slabs == 1) {
+        const dim3 grid(unsigned(ceil_div(a.N, a.per) * a.G));
+        if (p.KV == 2) hipLaunchKernelGGL((block_kernel<T, V, 2, BWD, GATE, kFused>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kFused>), grid, block, 0, st, a);
+    } else {
+        const dim3 grid(unsigned(a.N * a.G * a.slabs));
+        hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kStats>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kApply>), grid, block, 0, st, a);
+    }
+}
+
 template <typename T, int V, bool BWD>
 void launch_v(const GnArgs& a, const Plan& p, hipStream_t st) {
     if (p.kind == Plan::kRows) {
@@ -615,13 +657,8 @@ void launch_v(const GnArgs& a, const Plan& p, hipStream_t st) {
         hipLaunchKernelGGL((rows_kernel<T, V, 1, BWD>), grid, dim3(256), 0, st, a);
         return;
     }
-    const dim3 grid(unsigned(a.N * a.G * a.slabs)), block(unsigned(p.threads));
-    if (a.slabs == 1) {
-        hipLaunchKernelGGL((block_kernel<T, V, BWD, kFused>), grid, block, 0, st, a);
-    } else {
-        hipLaunchKernelGGL((block_kernel<T, V, BWD, kStats>), grid, block, 0, st, a);
-        hipLaunchKernelGGL((block_kernel<T, V, BWD, kApply>), grid, block, 0, st, a);
-    }
+    if (a.act == SELSCAN_ACT_GATE) launch_block<T, V, BWD, true>(a, p, st);
+    else launch_block<T, V, BWD, false>(a, p, st);
 }
 
 template <typename T, bool BWD>
@@ -646,12 +683,15 @@ bool groupnorm_fits(const GroupnormShape& s, bool backward) {
     if (s.N * s.S * s.C == 0) return true;
     const Plan p = plan_of(s, backward);
     if (p.kind == Plan::kRows) return true;
-    return p.parts <= INT32_MAX && s.N * s.G * p.slabs * p.threads < (int64_t(1) << 32);
+    return p.parts <= (int64_t(1) << 22) && s.N * s.G * p.slabs * p.threads < (int64_t(1) << 32);
 }
 
 size_t groupnorm_workspace_bytes(const GroupnormShape& s, bool backward) {
     const Plan p = plan_of(s, backward);
-    return stats_bytes(s, p) + (backward ? size_t(p.parts) * 2 * s.C * sizeof(float) : 0);
+    // the partial column sums, and where they are joined in stages those of the first stage
+    const size_t cols = size_t(2) * s.C * sizeof(float);
+    return stats_bytes(s, p) +
+           (backward ? (size_t(p.parts) + (p.parts > kJoin ? size_t(ceil_div(p.parts, kJoin)) : 0)) * cols : 0);
 }
 
 hipError_t launch_groupnorm(const GroupnormTensors& t, const GroupnormShape& s, void* workspace, hipStream_t stream) {
@@ -672,9 +712,25 @@ hipError_t launch_groupnorm_bwd(const GroupnormTensors& t, const GroupnormShape&
     a.part = t.dweight || t.dbias ? part : nullptr;
     if (s.dtype == DType::BF16) launch<bf16_bits, true>(a, p, stream);
     else launch<float, true>(a, p, stream);
-    if (a.part)
-        hipLaunchKernelGGL(cols_sum_kernel, dim3(unsigned(ceil_div(s.C, 64)), 2), dim3(1024), 0, stream, part,
-                           int(p.parts), s.C, t.dweight, t.dbias);
+    if (a.part) {
+        // Joined in stages of kJoin. The parts of a stage lie where those of the
+        // stage before last did: at most 1 / kJoin of them each time.
+        const dim3 block(1024);
+        float* from = part;
+        float* to = part + p.parts * 2 * s.C;
+        int64_t n = p.parts;
+        while (n > kJoin) {
+            const int64_t m = ceil_div(n, kJoin);
+            hipLaunchKernelGGL(cols_sum_kernel, dim3(unsigned(ceil_div(s.C, 64)), 2, unsigned(m)), block, 0, stream,
+                               from, int(n), s.C, to, nullptr, nullptr);
+            float* t_ = from;
+            from = to;
+            to = t_;
+            n = m;
+        }
+        hipLaunchKernelGGL(cols_sum_kernel, dim3(unsigned(ceil_div(s.C, 64)), 2), block, 0, stream, from, int(n), s.C,
+                           nullptr, t.dweight, t.dbias);
+    }
     return hipGetLastError();
 }
 

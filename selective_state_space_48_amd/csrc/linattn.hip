@@ -18,6 +18,10 @@ namespace {
 
 constexpr int kCols = 64;   // state columns of a workgroup of the step
 constexpr int kRun = 64;    // run lengths are multiples of this
+// States of more bytes than this are read and written past the caches in a step
+// (the 256 MB of them keep a smaller one from token to token: us per step with
+// and without, 671 MB 236 and 256, 284 MB 97 and 89, 134 MB 49 and 41).
+constexpr int64_t kStreamBytes = int64_t(384) << 20;
 
 // ---- operands of the matrix products ---------------------------------------
 //
@@ -701,31 +705,58 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__
     }
 }
 
-template <typename T>
+// One token: the state is read and written once (the step is bound by that
+// traffic). A workgroup takes 64 state columns of one head; thread (nq, p4) its
+// columns 4 p4 .. 4 p4 + 3 of rows nq + 16 i, all loaded before the first is
+// used, so that a wave moves four whole 256-byte rows per access; the outputs'
+// 16 partial sums per column meet in LDS and are added in order. STREAM: past
+// the caches (non-temporal).
+template <typename T, int R, bool STREAM>
 __global__ __launch_bounds__(256) void linattn_step_kernel(float* __restrict__ state, const T* __restrict__ q,
                                                            const T* __restrict__ k, const T* __restrict__ v,
                                                            const float* __restrict__ log_decay, T* __restrict__ y,
                                                            int64_t H, int64_t hkv, int dk, int dv, float scale) {
-    __shared__ float red[4][kCols];
-    const int tid = threadIdx.x, p = tid % kCols, r = tid / kCols;
+    __shared__ float red[16][kCols];
+    const int tid = threadIdx.x, p4 = tid % 16, nq = tid / 16;
     const int tiles = (dv + kCols - 1) / kCols;
     const int64_t bh = blockIdx.x / tiles, b = bh / H, h = bh % H, j = b * hkv + h / (H / hkv);
-    const int col = int(blockIdx.x % tiles) * kCols + p;
-    const bool live = col < dv;
-    const float lam = expf(log_decay[h]);
-    const float vv = live ? to_f32(v[j * dv + col]) : 0.0f;
-    float o = 0.0f;
-    if (live) {
-        for (int n = r; n < dk; n += 4) {
-            float* s = state + (bh * dk + n) * dv + col;
-            const float u = fmaf(to_f32(k[j * dk + n]), vv, lam * *s);
-            *s = u;
-            o = fmaf(to_f32(q[bh * dk + n]), u, o);
+    const int col = int(blockIdx.x % tiles) * kCols + 4 * p4;
+    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (col < dv) {  // (dv is a multiple of 4)
+        f32x4* S = reinterpret_cast<f32x4*>(state + bh * dk * dv + col);
+        f32x4 s[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int n = nq + 16 * i;
+            if (n < dk) s[i] = STREAM ? __builtin_nontemporal_load(S + n * (dv / 4)) : S[n * (dv / 4)];
+        }
+        const float lam = Decay(log_decay[h]).pow(1);
+        float vv[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) vv[c] = to_f32(v[j * dv + col + c]);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int n = nq + 16 * i;
+            if (n >= dk) continue;
+            const float kk = to_f32(k[j * dk + n]), qq = to_f32(q[bh * dk + n]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                s[i][c] = fmaf(kk, vv[c], lam * s[i][c]);
+                o[c] = fmaf(qq, s[i][c], o[c]);
+            }
+            if (STREAM) __builtin_nontemporal_store(s[i], S + n * (dv / 4));
+            else S[n * (dv / 4)] = s[i];
         }
     }
-    red[r][p] = o;
+    *reinterpret_cast<f32x4*>(&red[nq][4 * p4]) = f32x4{o[0], o[1], o[2], o[3]};
     __syncthreads();
-    if (r == 0 && live) y[bh * dv + col] = from_f32<T>(scale * (red[0][p] + red[1][p] + red[2][p] + red[3][p]));
+    const int c = int(blockIdx.x % tiles) * kCols + tid;
+    if (tid < kCols && c < dv) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += red[i][tid];
+        y[bh * dv + c] = from_f32<T>(scale * sum);
+    }
 }
 
 // Workgroups of 256 threads for n items taken in strides: a grid has fewer than 2^32 threads.
@@ -933,19 +964,32 @@ hipError_t launch_linattn_bwd(const LinattnTensors& t, const LinattnShape& s, co
     return s.dtype == DType::BF16 ? bwd<bf16_bits>(t, s, p, workspace, stream) : bwd<float>(t, s, p, workspace, stream);
 }
 
+namespace {
+template <typename T, int R>
+void step(float* state, const void* q, const void* k, const void* v, const float* log_decay, void* y,
+          const LinattnShape& s, float scale, hipStream_t st) {
+    const dim3 grid(unsigned(s.batch * s.heads * col_tiles(s.dv))), block(256);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, st, state, static_cast<const T*>(q), static_cast<const T*>(k),
+                           static_cast<const T*>(v), log_decay, static_cast<T*>(y), s.heads, s.kv_heads, int(s.dk),
+                           int(s.dv), scale);
+    };
+    if (state_floats(s) * 4 > kStreamBytes) go(linattn_step_kernel<T, R, true>);
+    else go(linattn_step_kernel<T, R, false>);
+}
+template <typename T>
+void step_rows(float* state, const void* q, const void* k, const void* v, const float* log_decay, void* y,
+               const LinattnShape& s, float scale, hipStream_t st) {
+    if (s.dk <= 64) step<T, 4>(state, q, k, v, log_decay, y, s, scale, st);
+    else if (s.dk <= 128) step<T, 8>(state, q, k, v, log_decay, y, s, scale, st);
+    else step<T, 16>(state, q, k, v, log_decay, y, s, scale, st);
+}
+}  // namespace
+
 hipError_t launch_linattn_step(float* state, const void* q, const void* k, const void* v, const float* log_decay,
                                void* y, const LinattnShape& s, float scale, hipStream_t stream) {
-    const dim3 grid(unsigned(s.batch * s.heads * col_tiles(s.dv))), block(256);
-    const int dk = int(s.dk), dv = int(s.dv);
-    if (s.dtype == DType::BF16)
-        hipLaunchKernelGGL((linattn_step_kernel<bf16_bits>), grid, block, 0, stream, state,
-                           static_cast<const bf16_bits*>(q), static_cast<const bf16_bits*>(k),
-                           static_cast<const bf16_bits*>(v), log_decay, static_cast<bf16_bits*>(y), s.heads,
-                           s.kv_heads, dk, dv, scale);
-    else
-        hipLaunchKernelGGL((linattn_step_kernel<float>), grid, block, 0, stream, state, static_cast<const float*>(q),
-                           static_cast<const float*>(k), static_cast<const float*>(v), log_decay,
-                           static_cast<float*>(y), s.heads, s.kv_heads, dk, dv, scale);
+    if (s.dtype == DType::BF16) step_rows<bf16_bits>(state, q, k, v, log_decay, y, s, scale, stream);
+    else step_rows<float>(state, q, k, v, log_decay, y, s, scale, stream);
     return hipGetLastError();
 }
 
