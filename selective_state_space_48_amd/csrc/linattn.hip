@@ -92,17 +92,29 @@ template <> struct Ops<float> {
     static __device__ __forceinline__ float value(const Frag& f, int e) { return f[e]; }
 };
 
-// A tile in LDS: rows of W elements and a pad, so that 16 rows' same 16-byte
-// piece (operands along rows) lie on 16 different pieces modulo 256 bytes (an
-// odd number of pieces from row to row), and every address is a lane's base
-// plus a constant. For bf16 the pad of 3 pieces keeps the transposed reads
-// (rows j, j + 8, j < 4, of four pieces) to 3 lanes a bank; for fp32 one piece
-// makes the reads of rows 4 g + e, columns m conflict-free.
-template <typename T, int W> struct Tile {
-    static constexpr int kStride = W + (sizeof(T) == 2 ? 24 : 4);
+// A tile in LDS. Padded: rows of W elements and a pad, so that 16 rows' same
+// 16-byte piece (operands along rows, 16 lanes at a time) lie on 16 different
+// pieces modulo 256 bytes (an odd number of pieces from row to row), and every
+// address is a lane's base plus a constant; for fp32 the pad of one piece
+// makes the reads of rows 4 g + e, columns m conflict-free too. X (bf16 tiles
+// that are mostly read transposed): no pad, a row's pieces permuted by an XOR
+// with a function of the row, which spreads those rows just as well and puts
+// the halves of four pieces of rows j, j + 8 (j < 4; 32 lanes at a time) on
+// every bank twice, the least that half pieces allow (the pad: three times).
+template <typename T, int W, bool X> struct Tile {
+    static constexpr bool kX = X && sizeof(T) == 2;
+    static constexpr int kStride = kX ? W : W + (sizeof(T) == 2 ? 24 : 4);
 };
-template <typename T, int W>
-__device__ __forceinline__ int at(int row, int col) { return row * Tile<T, W>::kStride + col; }
+template <typename T, int W, bool X>
+__device__ __forceinline__ int at(int row, int col) {
+    if constexpr (Tile<T, W, X>::kX) {
+        const int f = W == 64 ? ((row & 2) << 1) | ((row >> 2) & 1) | ((row >> 2) & 2)
+                              : ((row & 3) << 2) | ((row >> 2) & 1) | ((row >> 2) & 2);
+        return row * W + (((col >> 3) ^ f) << 3) + (col & 7);
+    } else {
+        return row * Tile<T, W, X>::kStride + col;
+    }
+}
 
 __device__ __forceinline__ bf16x4 ldtr(const bf16_bits* p) {
     typedef short s4 __attribute__((ext_vector_type(4)));
@@ -112,26 +124,26 @@ __device__ __forceinline__ bf16x4 ldtr(const bf16_bits* p) {
 }
 
 // Operand along the tile's rows: row r0 + m, columns k0 + E g ...
-template <typename T, int W>
+template <typename T, int W, bool X = false>
 __device__ __forceinline__ typename Ops<T>::Frag row_frag(const T* tile, int r0, int k0, int lane) {
     using O = Ops<T>;
-    return *reinterpret_cast<const typename O::Frag*>(tile + at<T, W>(r0 + lane % 16, k0 + O::E * (lane / 16)));
+    return *reinterpret_cast<const typename O::Frag*>(tile + at<T, W, X>(r0 + lane % 16, k0 + O::E * (lane / 16)));
 }
 // Operand down the tile's columns: the contraction runs over rows k0 + E g ..,
 // index m is column c0 + (m / 4) step + m % 4. The LDS transpose read hands
 // lane m of a 16-lane group the elements m % 4 of what lanes 4 e + m / 4 read,
 // e = 0..3 (4 rows of 16 columns, transposed).
-template <typename T, int W>
+template <typename T, int W, bool X = false>
 __device__ __forceinline__ typename Ops<T>::Frag col_frag(const T* tile, int k0, int c0, int step, int lane) {
     const int g = lane / 16, m = lane % 16;
     if constexpr (sizeof(T) == 2) {
         const int row = k0 + 8 * g + m / 4, col = c0 + (m % 4) * step;
-        const bf16x4 lo = ldtr(tile + at<T, W>(row, col)), hi = ldtr(tile + at<T, W>(row + 4, col));
+        const bf16x4 lo = ldtr(tile + at<T, W, X>(row, col)), hi = ldtr(tile + at<T, W, X>(row + 4, col));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
         f32x4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = tile[at<T, W>(k0 + 4 * g + e, c0 + (m / 4) * step + m % 4)];
+        for (int e = 0; e < 4; ++e) v[e] = tile[at<T, W, X>(k0 + 4 * g + e, c0 + (m / 4) * step + m % 4)];
         return v;
     }
 }
@@ -219,16 +231,16 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
     constexpr bool BF = sizeof(T) == 2;
     constexpr int NA = Q * KD / V / NS;    // 16-byte pieces of a or b per supply thread
     constexpr int NC = Q * PT / V / NS;
-    constexpr int SA = Q * Tile<T, KD>::kStride, SC = Q * Tile<T, PT>::kStride;
+    constexpr int SA = Q * Tile<T, KD, false>::kStride, SB = Q * Tile<T, KD, true>::kStride, SC = Q * Tile<T, PT, false>::kStride;
     // terms of the states in the outputs and of the scores; the slope is an fp32
     // result, so its operands (the entering states, its own scores) take three
     constexpr int TS = SLOPE && BF ? 3 : O::TS, TP = O::TP, TD = BF ? 3 : 1;
     constexpr int NPS = TP + (SLOPE ? TD : 0);
     constexpr bool VIA = BF && !SLOPE;  // outputs through LDS (SLOPE: no room left)
     __shared__ alignas(16) T As2[STATE ? 1 : 2][STATE ? 16 : SA];  // chunks c (even, odd)
-    __shared__ alignas(16) T Bs2[2][SA];
+    __shared__ alignas(16) T Bs2[2][SB];
     __shared__ alignas(16) T Cs2[2][SC];
-    __shared__ alignas(16) T Ps[STATE ? 1 : NPS][STATE ? 16 : Q * Tile<T, Q>::kStride];
+    __shared__ alignas(16) T Ps[STATE ? 1 : NPS][STATE ? 16 : Q * Tile<T, Q, false>::kStride];
     // bf16 outputs go through LDS: stored in whole rows by the supply waves
     constexpr int SO = PT + 8;
     __shared__ alignas(16) T Os[STATE || !VIA ? 16 : Q * SO];
@@ -304,11 +316,11 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             T* Cs = Cs2[c & 1];
 #pragma unroll
             for (int k = 0; k < NA; ++k) {
-                if (!STATE) *reinterpret_cast<u32x4*>(As + at<T, KD>(ia + k * RA, ca)) = ga[k];
-                *reinterpret_cast<u32x4*>(Bs + at<T, KD>(ia + k * RA, ca)) = gb[k];
+                if (!STATE) *reinterpret_cast<u32x4*>(As + at<T, KD, false>(ia + k * RA, ca)) = ga[k];
+                *reinterpret_cast<u32x4*>(Bs + at<T, KD, true>(ia + k * RA, ca)) = gb[k];
             }
 #pragma unroll
-            for (int k = 0; k < NC; ++k) *reinterpret_cast<u32x4*>(Cs + at<T, PT>(ic + k * RC, cc)) = gc[k];
+            for (int k = 0; k < NC; ++k) *reinterpret_cast<u32x4*>(Cs + at<T, PT, false>(ic + k * RC, cc)) = gc[k];
         };
         load(0, skip0);
         // powers of lambda inside a 16 x 16 tile of scores, by row minus column, and between tiles
@@ -323,7 +335,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             pw16 = dec.pow(16);
             pw32 = dec.pow(32);
             // score tiles above the diagonal that an operand still covers stay zero
-            for (int i = st; i < Q * Tile<T, Q>::kStride * ES / 16; i += NS)
+            for (int i = st; i < Q * Tile<T, Q, false>::kStride * ES / 16; i += NS)
 #pragma unroll
                 for (int k = 0; k < NPS; ++k) reinterpret_cast<u32x4*>(Ps[k])[i] = u32x4{0, 0, 0, 0};
         }
@@ -347,7 +359,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                 Frag fa[R], fb[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    fb[r] = row_frag<T, KD>(Bs, 16 * si[r], KB * kb, lane);
+                    fb[r] = row_frag<T, KD, true>(Bs, 16 * si[r], KB * kb, lane);
                     fa[r] = row_frag<T, KD>(As, 16 * ti[r], KB * kb, lane);
                 }
 #pragma unroll
@@ -372,14 +384,14 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
 #pragma unroll
                         for (int k = 0; k < 3; ++k) {
                             if (k >= terms) break;
-                            *reinterpret_cast<u32x2*>(Ps[first_tile + k] + at<T, Q>(t, s)) =
+                            *reinterpret_cast<u32x2*>(Ps[first_tile + k] + at<T, Q, false>(t, s)) =
                                 k == 1 && terms == 2 ? u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])}
                                                      : u32x2{O::upper_halves(y[0], y[1]), O::upper_halves(y[2], y[3])};
 #pragma unroll
                             for (int r = 0; r < 4; ++r) y[r] -= bf16_hi(__float_as_uint(y[r]));
                         }
                     } else {
-                        *reinterpret_cast<f32x4*>(Ps[first_tile] + at<T, Q>(t, s)) = f32x4{x[0], x[1], x[2], x[3]};
+                        *reinterpret_cast<f32x4*>(Ps[first_tile] + at<T, Q, false>(t, s)) = f32x4{x[0], x[1], x[2], x[3]};
                     }
                 };
                 put(0, TP, v);
@@ -617,8 +629,8 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                     Frag f[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        f[i] = BF ? col_frag<T, KD>(Bs, KB * q, 32 * ((kt + i) / 2) + 4 * (i % 2), 8, lane)
-                                  : col_frag<T, KD>(Bs, KB * q, 16 * (kt + i), 4, lane);
+                        f[i] = BF ? col_frag<T, KD, true>(Bs, KB * q, 32 * ((kt + i) / 2) + 4 * (i % 2), 8, lane)
+                                  : col_frag<T, KD, true>(Bs, KB * q, 16 * (kt + i), 4, lane);
 #pragma unroll
                     for (int k = 0; k < O::TU; ++k)
 #pragma unroll
