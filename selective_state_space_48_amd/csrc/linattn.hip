@@ -186,6 +186,12 @@ struct WalkArgs {
     const void* factor;
     const float* dlast;
     float* part;
+    // sums of an earlier launch's part, joined here: sum_out[h] over the batch
+    // and sum_n workgroups of each (entry, head)
+    const float* sum_part;
+    float* sum_out;
+    int32_t sum_n;
+    int64_t batch;
 };
 
 __device__ __forceinline__ int64_t entry_length(const int32_t* lengths, int64_t b, int64_t L) {
@@ -432,6 +438,14 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                 if (c + 1 < nc) scores(c + 1);
             }
             __syncthreads();
+        }
+        if (!STATE && !SLOPE && g.sum_out && wv == NW && b == 0 && seg == 0 && tile == 0 && role == 0) {
+            double s = 0.0;  // (lanes in turn, then halves: a fixed order)
+            for (int64_t i = lane; i < g.batch * g.sum_n; i += 64)
+                s += g.sum_part[(i / g.sum_n * g.H + h) * g.sum_n + i % g.sum_n];
+#pragma unroll
+            for (int x = 32; x; x >>= 1) s += __shfl_xor(s, x, 64);
+            if (lane == 0) g.sum_out[h] = float(s);
         }
     } else {
         // ================================ compute ================================
@@ -692,22 +706,16 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
     }
 }
 
-// dlog_decay[h] = sum over b and column tiles of the slope walk's sums, in order.
-__global__ __launch_bounds__(64) void slope_sum_kernel(const float* __restrict__ part, float* __restrict__ out,
-                                                       int64_t batch, int64_t H, int tiles) {
-    const int64_t h = int64_t(blockIdx.x) * 64 + threadIdx.x;
-    if (h >= H) return;
-    double s = 0.0;
-    for (int64_t b = 0; b < batch; ++b)
-        for (int i = 0; i < tiles; ++i) s += part[(b * H + h) * tiles + i];
-    out[h] = float(s);
-}
-
-// out[row, j, :] = sum of the heads' partial gradients that read kv head j, in order.
+// out[row, j, :] = sum of the heads' partial gradients that read kv head j, in
+// order; dk (grid y 0) and dv (1).
 template <typename T>
-__global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__ part, T* __restrict__ out,
-                                                       int64_t n, int64_t H, int64_t hkv, int D) {
-    const int64_t per = H / hkv;
+__global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__ pk, const float* __restrict__ pv,
+                                                       T* __restrict__ dk, T* __restrict__ dv, int64_t rows,
+                                                       int64_t H, int64_t hkv, int wk, int wv) {
+    const float* part = blockIdx.y ? pv : pk;
+    T* out = blockIdx.y ? dv : dk;
+    const int D = blockIdx.y ? wv : wk;
+    const int64_t per = H / hkv, n = rows * hkv * D;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
         const int64_t d = i % D, j = i / D % hkv, row = i / D / hkv;
         const float* p = part + (row * H + j * per) * D + d;
@@ -772,7 +780,7 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(float* __restrict__ s
 }
 
 // Workgroups of 256 threads for n items taken in strides: a grid has fewer than 2^32 threads.
-dim3 grid_of(int64_t n) { return dim3(unsigned(n < (int64_t(1) << 30) ? (n + 255) / 256 : int64_t(1) << 22)); }
+dim3 grid_of(int64_t n) { return dim3(unsigned(n < (int64_t(1) << 29) ? (n + 255) / 256 : int64_t(1) << 21)); }
 
 int col_tiles(int64_t P) { return int((P + kCols - 1) / kCols); }
 
@@ -870,6 +878,7 @@ WalkArgs walk_args(const LinattnTensors& t, const LinattnShape& s) {
     g.scale = t.scale;
     g.L = s.L;
     g.H = s.heads;
+    g.batch = s.batch;
     return g;
 }
 
@@ -891,37 +900,42 @@ hipError_t bwd(const LinattnTensors& t, const LinattnShape& s, const LinattnPlan
     const LinattnWalk wq{t.dy, t.v, t.k, t.dq, t.h0, nullptr, H, Hk, Hk, dv, dk, 1, dv, false, false};
     const LinattnWalk wk{t.v, t.dy, t.q, shared ? pk : t.dk, t.dlast, nullptr, Hk, H, H, dv, dk, 1, dv, true, shared};
     const LinattnWalk wv{t.k, t.q, t.dy, shared ? pv : t.dv, t.dlast, t.dh0, Hk, H, H, dk, dv, dv, 1, true, shared};
-    auto run_walks = [&](std::initializer_list<LinattnWalk> list) {
+    const int sums = p.segments * walk_tiles(dk, true);
+    float* part = take(0);
+    auto run_walks = [&](std::initializer_list<LinattnWalk> list, bool join) {
         WalkArgs g = walk_args(t, s);
         g.roles = 0;
         for (const LinattnWalk& w : list) g.w[g.roles++] = w;
+        if (join) {
+            g.sum_part = part;
+            g.sum_out = t.dlog_decay;
+            g.sum_n = sums;
+        }
         walks<T>(g, s, p, false, runs, nullptr, st);
     };
-    if (t.dlog_decay) {
+    // Walks of one width share a launch; the slope's sums are joined by the last one.
+    const bool slope = t.dlog_decay != nullptr;
+    if (slope) {
         WalkArgs g = walk_args(t, s);
         g.w[0] = wq;
         g.roles = 1;
         g.factor = t.q;
         g.dlast = t.dlast;
-        g.part = take(0);
+        g.part = part;
         walks<T>(g, s, p, true, runs, run_slope, st);
-        hipLaunchKernelGGL(slope_sum_kernel, dim3(unsigned((H + 63) / 64)), dim3(64), 0, st, g.part, t.dlog_decay,
-                           s.batch, s.heads, p.segments * walk_tiles(dk, true));
     }
-    // walks of one width share a launch
-    if (dk == dv && t.dlog_decay) run_walks({wk, wv});
-    else if (dk == dv) run_walks({wq, wk, wv});
-    else {
-        if (t.dlog_decay) run_walks({wk});
-        else run_walks({wq, wk});
-        run_walks({wv});
+    if (dk == dv) {
+        if (slope) run_walks({wk, wv}, true);
+        else run_walks({wq, wk, wv}, false);
+    } else {
+        if (slope) run_walks({wk}, false);
+        else run_walks({wq, wk}, false);
+        run_walks({wv}, slope);
     }
     if (shared) {
-        const int64_t nk = s.batch * s.L * Hk * dk, nv = s.batch * s.L * Hk * dv;
-        hipLaunchKernelGGL((head_sum_kernel<T>), grid_of(nk), dim3(256), 0, st, pk, static_cast<T*>(t.dk), nk, s.heads,
-                           s.kv_heads, dk);
-        hipLaunchKernelGGL((head_sum_kernel<T>), grid_of(nv), dim3(256), 0, st, pv, static_cast<T*>(t.dv), nv, s.heads,
-                           s.kv_heads, dv);
+        const int64_t rows = s.batch * s.L;
+        hipLaunchKernelGGL((head_sum_kernel<T>), dim3(grid_of(rows * Hk * (dk > dv ? dk : dv)).x, 2), dim3(256), 0, st,
+                           pk, pv, static_cast<T*>(t.dk), static_cast<T*>(t.dv), rows, s.heads, s.kv_heads, dk, dv);
     }
     return hipGetLastError();
 }
@@ -932,7 +946,9 @@ hipError_t bwd(const LinattnTensors& t, const LinattnShape& s, const LinattnPlan
 // costs as much as the first, while the state pass and the carries of runs
 // cost about as much as half the outputs. So a launch that leaves CUs idle is
 // cut into as many runs as still fit one round of the 256 CUs, of 128 tokens
-// at least (measured, us at 1, 2, 4, 8, 16, 32 runs: b1 L32771, 16 heads of 128
+// at least, if that is worth the two launches more: with n stretches of 64
+// tokens, 3.5 us (bf16; fp32 6) each in the outputs and 2.2 us in the state
+// pass, S runs save 3.5 n (1 - 1 / S) and cost 2.2 n / S + 12 us (measured, us at 1, 2, 4, 8, 16, 32 runs: b1 L32771, 16 heads of 128
 // 1670 1166 597 315 200 226; b1 L2048, 16 heads 114 93 60 46 43 68; b4 L2048,
 // 32 heads 117 105 135 182; b8, 32 heads 160 201 267).
 LinattnPlan linattn_plan(const LinattnShape& s, int32_t requested, bool backward) {
@@ -944,7 +960,8 @@ LinattnPlan linattn_plan(const LinattnShape& s, int32_t requested, bool backward
         S = groups > 0 ? 256 / groups : 1;
         const int64_t most = s.L / 128;
         if (S > most) S = most;
-        if (S < 1) S = 1;
+        const int64_t n = (s.L + kRun - 1) / kRun, each = s.dtype == DType::BF16 ? 35 : 60;
+        if (S < 2 || each * n * (S - 1) < 22 * n + 120 * S) S = 1;
     }
     LinattnPlan p{1, s.L};
     if (S > 1 && s.L > 0) {
