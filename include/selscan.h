@@ -486,12 +486,14 @@ int selscan_ssd_step(float* state, const void* x, const void* delta, const float
  *   y          : [B, L, H, dv] of dtype (output)
  *   last_state : [B, H, dk, dv] fp32 output or NULL
  * dims: H a multiple of Hkv; dk, dv multiples of 8 from 8 to 256 (else
- * SELSCAN_ERR_DSTATE); L < 2^27; H * max(dk, dv) <= 2^20; B * H <= 2^20
- * (2^21 for selscan_linattn_step).
+ * SELSCAN_ERR_DSTATE); L < 2^27; H * max(dk, dv) <= 2^20; B * H <= 900000
+ * (over the runs of tokens, if segments are asked for; 2^21 for
+ * selscan_linattn_step).
  * The state is held in fp32. bfloat16 calls round only operands of the matrix
  * products, each kept as two (outputs) or three (states) bfloat16 terms, so
  * that y is rounded once and the state keeps fp32 accuracy. Tokens behind an
- * entry's length are not read. Outputs must not overlap inputs.
+ * entry's length are not read. A NaN or infinity in v may reach the outputs of
+ * up to 63 tokens before it in its head (a masked score of 0 times it). Outputs must not overlap inputs.
  * Deterministic: the same inputs and launch choices give the same bits.
  */
 typedef struct {

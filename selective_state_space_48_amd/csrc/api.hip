@@ -437,9 +437,9 @@ float linattn_scale(float scale, int64_t dk) { return scale != 0.0f ? scale : fl
 int linattn_make_plan(const selscan_linattn_dims_t& d, int32_t segments, bool backward, LinattnPlan* p) {
     if (segments < 0 || segments > 65536) return SELSCAN_ERR_CONFIG;
     *p = linattn_plan(linattn_shape(d), segments, backward);
-    // up to three walks of up to 4 column tiles per (entry, head, run), of 256
-    // threads: a grid has fewer than 2^32 threads
-    if (int64_t(p->segments) * d.batch * d.heads * 12 >= (int64_t(1) << 24)) return SELSCAN_ERR_DIMS;
+    // up to six workgroups (walks times column tiles) of up to 768 threads per
+    // (entry, head, run): a grid has fewer than 2^32 threads
+    if (int64_t(p->segments) * d.batch * d.heads * 6 * 768 >= (int64_t(1) << 32)) return SELSCAN_ERR_DIMS;
     return SELSCAN_OK;
 }
 

@@ -42,9 +42,6 @@ struct GnArgs {
 
 // ---- vectors of V values -----------------------------------------------------
 
-template <typename T, int V> struct Vec {
-    float v[V];
-};
 template <int B> struct Raw;
 template <> struct Raw<2> { using type = uint16_t; };
 template <> struct Raw<4> { using type = uint32_t; };

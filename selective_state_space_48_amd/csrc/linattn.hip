@@ -468,16 +468,27 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                 }
         };
         const int64_t run_at = (int64_t(role) * g.segments + seg) * g.run_stride + bh * K * P;  // STATE: of this run
+        // Where the last state replaces the entering one (one role then), the last
+        // run may be through before the first begins: the state pass keeps a copy
+        // behind the runs' states, and the first run reads that.
+        const bool copied = seg == 0 && w.s0 && w.s0 == w.s1 && (STATE || g.segments > 1);
+        const int64_t copy_at = int64_t(STATE ? g.segments : g.segments - 1) * g.run_stride + bh * K * P;
         {
             // the output pass has one run more than the state pass
             const int64_t from = (int64_t(role) * (g.segments - 1) + seg - 1) * g.run_stride + bh * K * P;
             const bool own = seg == 0;
             const float* src = own ? (w.s0 ? w.s0 + bh * K * P : nullptr) : STATE ? nullptr : g.run_state + from;
-            const int sn = own ? w.sn : P, sp = own ? w.sp : 1;
+            int sn = own ? w.sn : P, sp = own ? w.sp : 1;
+            if (copied && !STATE) {
+                src = g.run_state + copy_at;
+                sn = P;
+                sp = 1;
+            }
             const float* dsrc = SLOPE && !STATE && !own ? g.run_slope + from : nullptr;
             each_state([&](int kt, int r, int n, int p, bool ok) {
                 S[kt][r] = src && ok ? src[int64_t(n) * sn + int64_t(p) * sp] : 0.0f;
                 if (SLOPE) D[kt][r] = dsrc && ok ? dsrc[int64_t(n) * P + p] : 0.0f;
+                if (STATE && copied && ok) g.run_state[copy_at + int64_t(n) * P + p] = S[kt][r];
             });
         }
 
@@ -779,10 +790,10 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(float* __restrict__ s
     }
 }
 
+int col_tiles(int64_t P) { return int((P + kCols - 1) / kCols); }
+
 // Workgroups of 256 threads for n items taken in strides: a grid has fewer than 2^32 threads.
 dim3 grid_of(int64_t n) { return dim3(unsigned(n < (int64_t(1) << 29) ? (n + 255) / 256 : int64_t(1) << 21)); }
-
-int col_tiles(int64_t P) { return int((P + kCols - 1) / kCols); }
 
 // Entering states of the runs: on entry run_state (and run_slope) hold the
 // runs' own end states from zero (the first one's from the walk's entering
@@ -796,19 +807,19 @@ struct CarryArgs {
     int32_t runs, KP;
 };
 __global__ __launch_bounds__(256) void carry_kernel(CarryArgs g) {
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= g.stride) return;
-    float* x = g.state + int64_t(blockIdx.y) * g.runs * g.stride + i;
-    float* y = g.slope ? g.slope + i : nullptr;
-    const int64_t bh = i / g.KP;
-    const int64_t len = entry_length(g.lengths, bh / g.H, g.L);
-    const Decay dec(g.log_decay[bh % g.H]);
-    float s = x[0], d = y ? y[0] : 0.0f;
-    for (int r = 1; r < g.runs; ++r) {
-        const int64_t left = len - r * g.seg_len, n = left < 0 ? 0 : left < g.seg_len ? left : g.seg_len;
-        const float keep = dec.pow(n);
-        if (y) y[r * g.stride] = d = fmaf(keep, fmaf(float(n), s, d), y[r * g.stride]);
-        x[r * g.stride] = s = fmaf(keep, s, x[r * g.stride]);
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < g.stride; i += int64_t(gridDim.x) * 256) {
+        float* x = g.state + int64_t(blockIdx.y) * g.runs * g.stride + i;
+        float* y = g.slope ? g.slope + i : nullptr;
+        const int64_t bh = i / g.KP;
+        const int64_t len = entry_length(g.lengths, bh / g.H, g.L);
+        const Decay dec(g.log_decay[bh % g.H]);
+        float s = x[0], d = y ? y[0] : 0.0f;
+        for (int r = 1; r < g.runs; ++r) {
+            const int64_t left = len - r * g.seg_len, n = left < 0 ? 0 : left < g.seg_len ? left : g.seg_len;
+            const float keep = dec.pow(n);
+            if (y) y[r * g.stride] = d = fmaf(keep, fmaf(float(n), s, d), y[r * g.stride]);
+            x[r * g.stride] = s = fmaf(keep, s, x[r * g.stride]);
+        }
     }
 }
 
@@ -865,8 +876,7 @@ void walks(WalkArgs g, const LinattnShape& s, const LinattnPlan& p, bool slope, 
         launch_walk_kd<T>(g, bh, pt, true, slope, st);
         const CarryArgs c{run_state, g.run_slope, g.log_decay, g.lengths, s.L, s.heads, p.seg_len, g.run_stride,
                           p.segments - 1, int(s.dk * s.dv)};
-        hipLaunchKernelGGL(carry_kernel, dim3(unsigned((g.run_stride + 255) / 256), unsigned(g.roles)), dim3(256), 0,
-                           st, c);
+        hipLaunchKernelGGL(carry_kernel, dim3(grid_of(g.run_stride).x, unsigned(g.roles)), dim3(256), 0, st, c);
     }
     launch_walk_kd<T>(g, bh, pt, false, slope, st);
 }
@@ -971,7 +981,10 @@ LinattnPlan linattn_plan(const LinattnShape& s, int32_t requested, bool backward
     }
     return p;
 }
-size_t linattn_fwd_workspace_bytes(const LinattnShape& s, const LinattnPlan& p) { return run_bytes(s, p); }
+// (with several runs one state more: the copy of an entering state that is replaced)
+size_t linattn_fwd_workspace_bytes(const LinattnShape& s, const LinattnPlan& p) {
+    return p.segments > 1 ? up256(size_t(p.segments) * state_floats(s) * 4) : 0;
+}
 size_t linattn_bwd_workspace_bytes(const LinattnShape& s, const LinattnPlan& p, bool slope) {
     return partial_bytes(s, s.dk) + partial_bytes(s, s.dv) + (slope ? 4 : 3) * run_bytes(s, p) +
            (slope ? up256(size_t(s.batch * s.heads * p.segments * walk_tiles(s.dk, true)) * 4) : 0);

@@ -39,6 +39,11 @@ SHAPES = [
     (2, 1000, 512, 32),
     (1, 300, 2048, 1),     # one large group
     (70, 33, 96, 6),
+    (3000, 1, 24, 3),      # column sums in two stages
+    (700, 33, 40, 5),
+    (2, 20000, 16, 2),     # many slabs
+    (1, 3, 20000, 2),      # a row of a group wider than a workgroup
+    (40, 1, 2560, 1),      # rows over several waves
 ]
 
 

@@ -124,6 +124,22 @@ def test_linattn_workspace():
     assert bwd(la(), ws=P(6), ws_bytes=need) == S.ERR_ALIAS
 
 
+def test_linattn_automatic_runs():
+    """Runs where heads leave CUs idle and the sequence is long enough (workspace: a state per run)."""
+    def runs(**kw):
+        d = la(kv_heads=4, dk=128, dv=128, **kw)
+        return sizes(d)[1] // (d.batch * d.heads * 128 * 128 * 4)
+
+    assert runs(batch=64, seqlen=100000) == 0      # 256 heads: one workgroup a CU already
+    assert runs(batch=1, seqlen=300) == 0          # too short to pay for two launches
+    # 4 heads: 64 runs make one round; of 100000 / 64 = 1562.5 tokens, rounded up to 1600: 62.5 of them
+    assert runs(batch=1, seqlen=100000) == 63
+    assert runs(batch=16, seqlen=100000) == 4
+    assert runs(batch=1, seqlen=1024) == 8         # runs of 128 tokens
+    assert sizes(la(batch=1 << 18, seqlen=3))[0] == (S.ERR_DIMS, S.ERR_DIMS)  # a grid of 2^32 threads
+    assert sizes(la(batch=1 << 14, seqlen=10000), segments=100)[0] == (S.ERR_DIMS, S.ERR_DIMS)
+
+
 def gn(batch=2, spatial=3, channels=32, groups=4, dtype=S.BF16, act=0, eps=1e-5):
     return S.GroupnormDims(batch, spatial, channels, groups, dtype, act, eps)
 

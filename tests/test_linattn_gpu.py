@@ -330,6 +330,30 @@ def bwd_(p):
                                dlast_state=p["dlast"], want_dh0=True, segments=2)
 
 
+def test_two_graphs_of_one_workspace():
+    """Two captured calls that share the caller's workspace, replayed in turn."""
+    shape = (2, 300, 4, 2, 64, 64, torch.bfloat16)
+    a, b = (make(*shape, seed=s, h0=True, grads=True) for s in (26, 27))
+    case("two graphs of one workspace")
+    n = selscan.linattn_bwd_workspace_size(*shape, segments=2)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    want = [bwd(p, segments=2, workspace=ws) for p in (a, b)]
+    graphs, outs = [], []
+    for p in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(selscan.linattn_bwd(p["q"], p["k"], p["v"], p["log_decay"], dy=p["dy"], h0=p["h0"],
+                                            dlast_state=p["dlast"], want_dh0=True, segments=2, workspace=ws))
+        graphs.append(g)
+    for turn in range(3):
+        for g in graphs:
+            g.replay()
+        bwd(a, segments=2, workspace=ws)  # eager work between the replays
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(o[k], w[k]) for k in w), turn
+
+
 def test_side_stream_and_two_calls_at_once():
     p = make(2, 300, 8, 8, 64, 64, torch.bfloat16, seed=20, h0=True, grads=True)
     o = make(2, 300, 8, 8, 64, 64, torch.bfloat16, seed=21, h0=True, grads=True)
