@@ -284,6 +284,9 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
 
     if (wv >= NW) {
         // ================================ supply ================================
+        // (at a raised wave priority: what the other waves wait for is never behind
+        // their products; 2 % of a layer's forward and gradients)
+        __builtin_amdgcn_s_setprio(3);
         const int st = tid - 64 * NW;
         const int64_t ra = h / (g.H / w.ha), rb = h / (g.H / w.hb), rc = h / (g.H / w.hc);
         const T* pa = static_cast<const T*>(w.a) + (b * g.L * w.ha + ra) * K;
