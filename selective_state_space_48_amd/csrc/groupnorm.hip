@@ -274,11 +274,14 @@ constexpr int held(bool bwd, bool gate, int V) {
 template <typename T, int V, int K, bool BWD, bool GATE, int MODE>
 __global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
     __shared__ float red[16];
-    __shared__ float cols[BWD && MODE != kApply ? 1024 * V : 1];
+    extern __shared__ float cols[];  // backward: V values a thread, sized by the launch
     const int tid = threadIdx.x, rs = int(blockDim.x) / a.lanes, r0 = tid / a.lanes, v = tid % a.lanes;
-    // kFused: group g of entries n0 .. n1 - 1; else slab `slab` of instance (n0, g)
-    const int64_t slab = MODE == kFused ? 0 : blockIdx.x % a.slabs, unit = MODE == kFused ? blockIdx.x : blockIdx.x / a.slabs;
-    const int64_t g = unit % a.G, n0 = MODE == kFused ? unit / a.G * a.per : unit / a.G;
+    // kFused: group g of entries n0 .. n1 - 1; else slab `slab` of instance (n0, g).
+    // The groups of the same rows, which share cache lines where they are narrow,
+    // are neighbours and run on one XCD.
+    const int64_t idx = xcd_tile(blockIdx.x, gridDim.x), g = idx % a.G;
+    const int64_t slab = MODE == kFused ? 0 : idx / a.G % a.slabs;
+    const int64_t n0 = MODE == kFused ? idx / a.G * a.per : idx / a.G / a.slabs;
     const int64_t n1 = MODE != kFused ? n0 + 1 : n0 + a.per < a.N ? n0 + a.per : a.N;
     const int64_t s0 = MODE == kFused ? 0 : slab * a.per;
     const int64_t s1 = MODE == kFused || s0 + a.per > a.S ? a.S : s0 + a.per;
@@ -331,8 +334,8 @@ __global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
                 var = block_sum(s, red);
                 if (MODE == kStats) {
                     if (tid == 0) {
-                        a.stats[2 * int64_t(blockIdx.x)] = mean;
-                        a.stats[2 * int64_t(blockIdx.x) + 1] = var;
+                        a.stats[2 * (inst * a.slabs + slab)] = mean;
+                        a.stats[2 * (inst * a.slabs + slab) + 1] = var;
                     }
                     return;
                 }
@@ -397,8 +400,8 @@ __global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
                 m1 = block_sum(p1, red);
                 m2 = block_sum(p2, red);
                 if (MODE == kStats && tid == 0) {
-                    a.stats[2 * int64_t(blockIdx.x)] = m1;
-                    a.stats[2 * int64_t(blockIdx.x) + 1] = m2;
+                    a.stats[2 * (inst * a.slabs + slab)] = m1;
+                    a.stats[2 * (inst * a.slabs + slab) + 1] = m2;
                 }
             } else {
                 const float* st = a.stats + 2 * inst * a.slabs;
@@ -429,7 +432,7 @@ __global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
     }
     if constexpr (BWD && MODE != kApply) {
         if (a.part) {  // the column sums, the threads' rows joined in a fixed order
-            const int64_t at = MODE == kFused ? unit / a.G : n0 * a.slabs + slab;
+            const int64_t at = MODE == kFused ? idx / a.G : n0 * a.slabs + slab;
             float* out = a.part + at * 2 * a.C + g * a.D;
             for (int which = 0; which < 2; ++which) {
                 __syncthreads();
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(256) void plain_cols_kernel(GnArgs a) {
 // Column sums over runs of kJoin parts (grid z), 16 interleaved rows of them
 // joined in order; 64 columns per workgroup, du xh (y 0) and du (y 1). The
 // last stage (one run) writes dweight and dbias, the others out[run][2][C].
-constexpr int kJoin = 256;
+constexpr int kJoin = 512;
 __global__ __launch_bounds__(1024) void cols_sum_kernel(const float* __restrict__ part, int parts, int64_t C,
                                                         float* __restrict__ out, float* __restrict__ dweight,
                                                         float* __restrict__ dbias) {
@@ -636,13 +639,14 @@ template <typename T, int V, bool BWD, bool GATE>
 void launch_block(const GnArgs& a, const Plan& p, hipStream_t st) {
     constexpr int K = held(BWD, GATE, V);
     const dim3 block(unsigned(p.threads));
+    const unsigned lds = BWD ? unsigned(p.threads) * V * 4 : 0;  // at most 32 KB
     if (a.slabs == 1) {
         const dim3 grid(unsigned(ceil_div(a.N, a.per) * a.G));
-        if (p.KV == 2) hipLaunchKernelGGL((block_kernel<T, V, 2, BWD, GATE, kFused>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kFused>), grid, block, 0, st, a);
+        if (p.KV == 2) hipLaunchKernelGGL((block_kernel<T, V, 2, BWD, GATE, kFused>), grid, block, lds, st, a);
+        else hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kFused>), grid, block, lds, st, a);
     } else {
         const dim3 grid(unsigned(a.N * a.G * a.slabs));
-        hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kStats>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kStats>), grid, block, lds, st, a);
         hipLaunchKernelGGL((block_kernel<T, V, K, BWD, GATE, kApply>), grid, block, 0, st, a);
     }
 }
