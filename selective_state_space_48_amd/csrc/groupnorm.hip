@@ -8,6 +8,10 @@
 //   block (a row of the group fits a workgroup's threads): one workgroup per
 //         instance or slab, its values in registers;
 //   plain (wider groups): one workgroup per instance, several passes.
+// Measured (MI355X; bytes moved once over the time; a large copy 4.75 TB/s):
+// 16384 rows of 4096 in 32 groups, bf16, gated: 88-97 us (4.2-4.6 TB/s),
+// gradients 152 us (4.4 TB/s); 8 x 2048 x 512 fp32 in 32 groups (64-byte rows),
+// SiLU: 17 us (4.0 TB/s), gradients 30 us (3.4 TB/s).
 // Statistics in fp32 by differences: the mean first, then the squares about it
 // (slabs: their own means, joined by n_i (mean_i - mean)^2).
 #include "../../include/selscan.h"

@@ -8,6 +8,22 @@
 // tensors in other roles (launch.hpp). One workgroup walks a run of one head's
 // tokens for 64 or 128 state columns; where heads are few the sequence is cut
 // into runs: the runs' own end states, their carries, then the outputs.
+//
+// What bounds it (MI355X, b8 L2048, 32 heads of 128 x 128, bf16): the bytes, 554
+// MB read and written once, take 117 us at the rate of a large copy (4.75
+// TB/s); the kernel takes 127-134 us (4.1-4.3 TB/s; 134-151 us a call). Of its
+// cycles the LDS is busy in 54 %, the vector units in 45 %, the matrix cores in
+// 37 %: a chunk's dependent steps (stage, scores, outputs, state) come after one
+// another in a workgroup that fills its CU. Its steps (us a call): 241 with
+// every wave in every part and three barriers; 164 staged a chunk ahead (two
+// barriers); 160 with supply waves, outputs in whole rows through LDS; 151 with
+// them at a raised priority. One workgroup alone on the chip takes 3.3 us a
+// chunk. Tried without gain: 64 state columns and two workgroups a CU (196); the
+// two halves of the waves in different orders (174); products and vector
+// instructions interleaved by hand (189); one bf16 term instead of two and two
+// instead of three (147 against 163 then, but off by 2^-9 of the terms);
+// non-temporal loads and stores (equal); 128 columns for the slope (gradients
+// 290 -> 405).
 #include <initializer_list>
 
 #include "common.hpp"
@@ -18,9 +34,10 @@ namespace {
 
 constexpr int kCols = 64;   // state columns of a workgroup of the step
 constexpr int kRun = 64;    // run lengths are multiples of this
-// States of more bytes than this are read and written past the caches in a step
-// (the 256 MB of them keep a smaller one from token to token: us per step with
-// and without, 671 MB 236 and 256, 284 MB 97 and 89, 134 MB 49 and 41).
+// States of more bytes than this are read and written past the caches in a
+// step; the 256 MB cache keeps much of a smaller one from token to token (us per
+// step past the caches and through them: 671 MB 236 and 256, 284 MB 97 and 89,
+// 134 MB 49 and 41).
 constexpr int64_t kStreamBytes = int64_t(384) << 20;
 
 // ---- operands of the matrix products ---------------------------------------
@@ -130,7 +147,8 @@ __device__ __forceinline__ typename Ops<T>::Frag row_frag(const T* tile, int r0,
     return *reinterpret_cast<const typename O::Frag*>(tile + at<T, W, X>(r0 + lane % 16, k0 + O::E * (lane / 16)));
 }
 // Operand down the tile's columns: the contraction runs over rows k0 + E g ..,
-// index m is column c0 + (m / 4) step + m % 4. The LDS transpose read hands
+// index m is column c0 + (m / 4) step + m % 4 (step 8: every other four columns,
+// the rows of one of a pair of accumulators). The LDS transpose read hands
 // lane m of a 16-lane group the elements m % 4 of what lanes 4 e + m / 4 read,
 // e = 0..3 (4 rows of 16 columns, transposed).
 template <typename T, int W, bool X = false>
@@ -740,7 +758,8 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__
 }
 
 // One token: the state is read and written once (the step is bound by that
-// traffic). A workgroup takes 64 state columns of one head; thread (nq, p4) its
+// traffic: 671 MB each way take 236-245 us, 5.5-5.7 TB/s, against 4.75 TB/s of a
+// large copy). A workgroup takes 64 state columns of one head; thread (nq, p4) its
 // columns 4 p4 .. 4 p4 + 3 of rows nq + 16 i, all loaded before the first is
 // used, so that a wave moves four whole 256-byte rows per access; the outputs'
 // 16 partial sums per column meet in LDS and are added in order. STREAM: past
