@@ -492,8 +492,9 @@ int selscan_ssd_step(float* state, const void* x, const void* delta, const float
  * The state is held in fp32. bfloat16 calls round only operands of the matrix
  * products, each kept as two (outputs) or three (states) bfloat16 terms, so
  * that y is rounded once and the state keeps fp32 accuracy. Tokens behind an
- * entry's length are not read. A NaN or infinity in v may reach the outputs of
- * up to 63 tokens before it in its head (a masked score of 0 times it). Outputs must not overlap inputs.
+ * entry's length are not read. A NaN or an infinity reaches what the
+ * recurrence takes it to and no token before it; an infinity may come out as
+ * a NaN. Outputs must not overlap inputs.
  * Deterministic: the same inputs and launch choices give the same bits.
  */
 typedef struct {

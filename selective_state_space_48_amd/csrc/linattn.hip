@@ -11,7 +11,7 @@
 //
 // What bounds it (MI355X, b8 L2048, 32 heads of 128 x 128, bf16): the bytes, 554
 // MB read and written once, take 117 us at the rate of a large copy (4.75
-// TB/s); the kernel takes 127-134 us (4.1-4.3 TB/s; 134-151 us a call). Of its
+// TB/s); the kernel takes 127-134 us (4.1-4.3 TB/s; 136-151 us a call). Of its
 // cycles the LDS is busy in 54 %, the vector units in 45 %, the matrix cores in
 // 37 %: a chunk's dependent steps (stage, scores, outputs, state) come after one
 // another in a workgroup that fills its CU. Its steps (us a call): 241 with
@@ -25,6 +25,7 @@
 // non-temporal loads and stores (equal); 128 columns for the slope (gradients
 // 290 -> 405).
 #include <initializer_list>
+#include <type_traits>
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -224,6 +225,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void* p, int by
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+__device__ __forceinline__ bool not_finite(bf16_bits x) { return (x & 0x7f80u) == 0x7f80u; }
+
 // A run of a walk, chunk by chunk. KD: the width of a and b rounded up (64,
 // 128, 256); PT: state columns of the workgroup.
 // STATE: only the run's end state, into run_state. SLOPE: with the outputs,
@@ -269,6 +273,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
     constexpr int SO = PT + 8;
     __shared__ alignas(16) T Os[STATE || !VIA ? 16 : Q * SO];
     __shared__ float red[NW];
+    __shared__ int odds[2];  // number + 1 of the last (even, odd) chunk with a value that is not finite
 
     const int tid = threadIdx.x, lane = tid % 64, m = lane % 16, gq = lane / 16;
     const int wv = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -348,6 +353,16 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             }
 #pragma unroll
             for (int k = 0; k < NC; ++k) *reinterpret_cast<u32x4*>(Cs + at<T, PT, false>(ic + k * RC, cc)) = gc[k];
+        };
+        // Chunks with a NaN or an infinity among the values leave their number.
+        auto seek = [&] {
+            uint32_t found = 0;
+            constexpr uint32_t X = BF ? 0x7f807f80u : 0x7f800000u, ONE = BF ? 0x00800080u : 0x00800000u;
+#pragma unroll
+            for (int k = 0; k < NC; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) found |= (gc[k][i] & X) + ONE;
+            return (found & (BF ? 0x80008000u : 0x80000000u)) != 0;
         };
         load(0, skip0);
         // powers of lambda inside a 16 x 16 tile of scores, by row minus column, and between tiles
@@ -443,15 +458,18 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
         };
         if (nc > 0) {
             stage(0);
+            const bool found = !STATE && seek();
             load(1, 0);
             __syncthreads();
             if (!STATE) {
+                if (found) odds[0] = 1;
                 scores(0);
                 __syncthreads();
             }
         }
         for (int c = 0; c < nc; ++c) {
             stage(c + 1);  // (past the last chunk: zeros that nothing reads)
+            if (!STATE && seek()) odds[(c + 1) & 1] = c + 2;
             load(c + 2, 0);
             if (!STATE) {
                 __syncthreads();
@@ -527,6 +545,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
         float keep = dec.pow(Q);  // of the entering state over a chunk
         const int so = int(g.H) * P, po = col0 + 4 * gq;  // a lane's 4 output columns
         const int vo = po < P ? (w.rev ? 15 - m : m) * so + po : kInvalid;  // (elements)
+        if (!STATE && tid < 2) odds[tid] = 0;
         if (nc > 0) {
             __syncthreads();
             if (!STATE) __syncthreads();
@@ -548,6 +567,17 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             Frag cf[QB];
 #pragma unroll
             for (int q = 0; q < QB; ++q) cf[q] = col_frag<T, PT>(Cs, KB * q, wv * 16, 4, lane);
+            // A masked score is a 0 in the outputs' products. Times a NaN or an infinity
+            // of a later token it would not be: in a chunk with one, those values are
+            // left out there and added token by token. (The marks and branches cost 1 to 3 %;
+            // at state width 256 some registers, prompts 82 -> 95 us at 256 x 128.)
+            const bool odd = !STATE && __builtin_amdgcn_readfirstlane(odds[c & 1]) == c + 1;
+            if (odd)
+#pragma unroll
+                for (int q = 0; q < QB; ++q)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (not_finite(O::value(cf[q], e))) cf[q][e] = 0;
             if (!STATE) {
                 // ---- carry-in, transposed: o[p][t] = sum_n H[n][p] a[t][n] ----
                 f32x4 o[TT], o2[SLOPE ? TT : 1];
@@ -575,6 +605,8 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                         }
                 }
                 if (SLOPE) {
+                    // (loads taken ahead over this line spill: gradients of b4 L2048, 32 heads 324 us with, 287 without)
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int t = 0; t < TT; ++t) o2[t] = (o2[t] + o[t]) * float(16 * t + m - skip + 1);
 #pragma unroll
@@ -597,6 +629,18 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                     if (SLOPE) o2[t] *= up[t];
                     o[t] *= up[t];
                 }
+                const int64_t row0 = ((b * g.L + t_first + t_step * c) * g.H + h) * P;
+                // (asked for here, behind the next products)
+                std::conditional_t<BF, u32x2, u32x4> fac[SLOPE ? TT : 1];
+                if constexpr (SLOPE) {
+                    const auto rf = buf_rsrc(static_cast<const T*>(g.factor) + row0, ((Q - 1) * so + P) * ES);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        const int fo = vo >= 0 && 16 * t + m >= skip ? (vo + (w.rev ? TT - 1 - t : t) * 16 * so) * ES : kInvalid;
+                        if constexpr (BF) fac[t] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rf, fo, 0, 0));
+                        else fac[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rf, fo, 0, 0));
+                    }
+                }
                 // ---- scores times c ----
 #pragma unroll
                 for (int q = 0; q < QB; ++q)
@@ -609,23 +653,37 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                             if (k < TP) o[t] = O::mfma(cf[q], f, o[t]);
                             else o2[t] = O::mfma(cf[q], f, o2[t]);
                         }
+                if (odd) {
+                    int own = lane;  // (opaque: no address of this path is kept beside the other)
+                    asm volatile("" : "+v"(own));
+                    const int row = own % 16, col = wv * 16 + own / 16 * 4;
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll 1
+                        for (int s = 0; s <= 16 * t + 15; ++s) {
+                            float x = 0.0f, x2 = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < NPS; ++k)
+                                (k < TP ? x : x2) += to_f32(Ps[k][at<T, Q, false>(16 * t + row, s)]);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const T y = Cs[at<T, PT, false>(s, col + r)];
+                                if (!not_finite(y)) continue;
+                                if (s <= 16 * t + row) o[t][r] = fmaf(x, to_f32(y), o[t][r]);
+                                if (SLOPE && s < 16 * t + row) o2[t][r] = fmaf(x2, to_f32(y), o2[t][r]);
+                            }
+                        }
+                }
                 // ---- store: token 16 t + m, columns 4 gq .. 4 gq + 3 of the wave's 16 ----
-                const int64_t row0 = ((b * g.L + t_first + t_step * c) * g.H + h) * P;
                 if constexpr (SLOPE) {
-                    const auto rf = buf_rsrc(static_cast<const T*>(g.factor) + row0, ((Q - 1) * so + P) * ES);
 #pragma unroll
                     for (int t = 0; t < TT; ++t) {
-                        const bool ok = vo >= 0 && 16 * t + m >= skip;
-                        const int fo = ok ? (vo + (w.rev ? TT - 1 - t : t) * 16 * so) * ES : kInvalid;
                         f32x4 f;
-                        if constexpr (BF) {
-                            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rf, fo, 0, 0));
-                            f = f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
-                        } else {
-                            f = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rf, fo, 0, 0));
-                        }
+                        if constexpr (BF) f = f32x4{bf16_lo(fac[t][0]), bf16_hi(fac[t][0]), bf16_lo(fac[t][1]), bf16_hi(fac[t][1])};
+                        else f = __builtin_bit_cast(f32x4, fac[t]);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) total = ok ? fmaf(o2[t][r], f[r], total) : total;
+                        for (int r = 0; r < 4; ++r)
+                            total = vo >= 0 && 16 * t + m >= skip ? fmaf(o2[t][r], f[r], total) : total;
                     }
                 }
                 if (VIA && !w.o_f32) {
@@ -653,6 +711,9 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                 __syncthreads();
             }
             // ---- state: H <- lambda^n H + B^T (w c) ----
+            if (odd)
+#pragma unroll
+                for (int q = 0; q < QB; ++q) cf[q] = col_frag<T, PT>(Cs, KB * q, wv * 16, 4, lane);
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 if (SLOPE) D[kt] = (D[kt] + S[kt] * float(nv)) * keep;

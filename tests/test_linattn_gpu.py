@@ -8,6 +8,7 @@ import torch
 
 from linattn_util import DT, bwd_ref, close, fwd_ref, host, make, relative
 from oracle import linattn as ref
+from parity_util import to_np
 from selective_state_space_48_amd import selscan
 
 pytestmark = pytest.mark.gpu
@@ -204,6 +205,40 @@ def test_padding_is_not_read(dtype, segments):
     y, s = fwd(clean, segments=segments)
     assert torch.isnan(y[0, 5:, :2]).all() and torch.isfinite(y[0, :5]).all()
     assert torch.isfinite(y[0, :, 2:]).all() and torch.isfinite(y[1:]).all() and torch.isfinite(s[1:]).all()
+
+
+def check_reach(r, want, poisoned, size, c, what):
+    """What the 64-bit definition leaves finite is finite and right, the rest is not finite."""
+    for n in poisoned:
+        got, ok = to_np(r[n]), np.isfinite(poisoned[n])
+        assert np.array_equal(np.isfinite(got), ok), f"{what} {n}: {np.isfinite(got).sum()} finite, not {ok.sum()}"
+        z = np.zeros_like(got)
+        close(torch.from_numpy(np.where(ok, got, z)), np.where(ok, want[n], z), size[n], r[n].dtype, c, f"{what} {n}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(2, 150, 2, 2, 64, 64), (1, 131, 2, 1, 128, 128), (1, 70, 1, 1, 256, 40)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nan_reaches_later_tokens_alone(shape, dtype, value):
+    """A NaN or an infinity in one element reaches what the recurrence takes it to: no token before it
+    (gradients: in the walk's own direction), no other column, entry or kv head."""
+    B, L, H, Hk, dk, dv = shape
+    p = make(B, L, H, Hk, dk, dv, DT[dtype], seed=21, h0=True, grads=True)
+    p["v"] = p["v"].abs() + 0.1  # (an infinity times a sum of either sign stays one)
+    want, size = bwd_ref(p)
+    y, _, ya, _ = fwd_ref(p)
+    want["y"], size["y"] = y, ya
+    c = relative(DT[dtype], L, dk, dv)
+    for name, t, col in (("v", 37, 3), ("v", L - 1, dv - 1), ("k", 20, dk - 2), ("q", 45, 1), ("dy", 66, 5)):
+        case(f"{value} in {name} at token {t} {shape} {dtype}")
+        x = dict(p, **{name: p[name].clone()})
+        x[name][0, t, 0, col] = value
+        with np.errstate(invalid="ignore"):
+            y, _, _, _ = fwd_ref(x)
+            poisoned, _ = bwd_ref(x)
+        poisoned = {"y": y, **{n: poisoned[n] for n in ("dq", "dk", "dv")}}
+        r = {"y": fwd(x)[0], **bwd(x)}
+        check_reach(r, want, poisoned, size, c, f"{name}[{t}]")
 
 
 def test_lengths_out_of_range_are_clamped():
