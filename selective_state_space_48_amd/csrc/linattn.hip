@@ -11,9 +11,9 @@
 //
 // What bounds it (MI355X, b8 L2048, 32 heads of 128 x 128, bf16): the bytes, 554
 // MB read and written once, take 117 us at the rate of a large copy (4.75
-// TB/s); the kernel takes 127-134 us (4.1-4.3 TB/s; 136-151 us a call). Of its
-// cycles the LDS is busy in 54 %, the vector units in 45 %, the matrix cores in
-// 37 %: a chunk's dependent steps (stage, scores, outputs, state) come after one
+// TB/s); a call takes 136-151 us (3.7-4.1 TB/s; by the clock). Of its
+// cycles the LDS is busy in 50 %, the vector units in 45 %, the matrix cores in
+// 33 %: a chunk's dependent steps (stage, scores, outputs, state) come after one
 // another in a workgroup that fills its CU. Its steps (us a call): 241 with
 // every wave in every part and three barriers; 164 staged a chunk ahead (two
 // barriers); 160 with supply waves, outputs in whole rows through LDS; 151 with
