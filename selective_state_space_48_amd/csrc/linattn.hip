@@ -322,12 +322,16 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
         const int va = ca < K ? (rowa * sa + ca) * ES : kInvalid, vb = ca < K ? (rowa * sb + ca) * ES : kInvalid;
         const int vc = tile * PT + cc < P ? (rowc * sc + tile * PT + cc) * ES : kInvalid;
         u32x4 ga[STATE ? 1 : NA], gb[NA], gc[NC];
-        auto load = [&](int c, int skip) {  // (past the last chunk: nothing, zeros)
+        // Past the last chunk every lane's offset is kInvalid, which reads zeros and
+        // touches nothing. (A resource of no bytes would not do: the rows go into the
+        // scalar offset, and whether that counts against its length is not stated.)
+        auto load = [&](int c, int skip) {
             const int64_t t0 = t_first + t_step * c;
-            const int on = c < nc ? ES : 0;
-            const auto ra_ = buf_rsrc(pa + t0 * sa, ((Q - 1) * sa + K) * on);
-            const auto rb_ = buf_rsrc(pb + t0 * sb, ((Q - 1) * sb + K) * on);
-            const auto rc_ = buf_rsrc(pc + t0 * sc, ((Q - 1) * sc + P) * on);
+            const bool on = c < nc;
+            const int oa = on ? va : kInvalid, ob = on ? vb : kInvalid, oc = on ? vc : kInvalid;
+            const auto ra_ = buf_rsrc(pa + t0 * sa, ((Q - 1) * sa + K) * ES);
+            const auto rb_ = buf_rsrc(pb + t0 * sb, ((Q - 1) * sb + K) * ES);
+            const auto rc_ = buf_rsrc(pc + t0 * sc, ((Q - 1) * sc + P) * ES);
             auto get = [](__amdgpu_buffer_rsrc_t r, int v, int s) {
                 return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, v, s, 0));
             };
@@ -335,12 +339,12 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             for (int k = 0; k < NA; ++k) {
                 const int up_ = (w.rev ? NA - 1 - k : k) * RA;
                 const bool ok = ia + k * RA >= skip;
-                if (!STATE) ga[k] = get(ra_, ok ? va : kInvalid, up_ * sa * ES);
-                gb[k] = get(rb_, ok ? vb : kInvalid, up_ * sb * ES);
+                if (!STATE) ga[k] = get(ra_, ok ? oa : kInvalid, up_ * sa * ES);
+                gb[k] = get(rb_, ok ? ob : kInvalid, up_ * sb * ES);
             }
 #pragma unroll
             for (int k = 0; k < NC; ++k)
-                gc[k] = get(rc_, ic + k * RC >= skip ? vc : kInvalid, (w.rev ? NC - 1 - k : k) * RC * sc * ES);
+                gc[k] = get(rc_, ic + k * RC >= skip ? oc : kInvalid, (w.rev ? NC - 1 - k : k) * RC * sc * ES);
         };
         auto stage = [&](int c) {
             T* As = As2[STATE ? 0 : c & 1];

@@ -443,3 +443,23 @@ def test_token_offsets_past_2_31():
     y1 = selscan.linattn_step(s1, *one, dec)
     torch.cuda.synchronize()
     assert torch.equal(y[B - 1:], y1) and torch.equal(state[B - 1:], s1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segments", [1, 3])
+def test_nothing_is_read_past_the_tensors(dtype, segments):
+    """Tensors that fill their allocations (16 and 32 MB, whole pages), and the same entry among entries of
+    NaN: the loads that run ahead of a walk, forwards and backwards in time, take nothing from beside it."""
+    B, L, H, d = 3, 4096, 16, 128
+    case(f"tensors that fill their allocations {dtype} segments={segments}")
+    p = make(B, L, H, H, d, d, DT[dtype], seed=31, grads=True)
+    for n in ("q", "k", "v", "dy"):
+        p[n][0], p[n][2] = float("nan"), float("nan")
+    torch.cuda.empty_cache()
+    one = {n: None if t is None else t if n == "log_decay" else t[1:2].clone() for n, t in p.items()}
+    a, b = fwd(p, segments=segments), fwd(one, segments=segments)
+    assert all(torch.equal(x[1:2], y) and torch.isfinite(y).all() for x, y in zip(a, b))
+    kw = dict(segments=segments, want_dlog_decay=False)
+    a, b = bwd(p, **kw), bwd(one, **kw)
+    for n in b:
+        assert torch.equal(a[n][1:2], b[n]) and torch.isfinite(b[n]).all(), n
