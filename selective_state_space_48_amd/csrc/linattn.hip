@@ -180,6 +180,23 @@ struct Decay {
         const double x = g2 * double(n), w = __builtin_rint(x > 2000.0 ? 2000.0 : x);
         return x < -160.0 ? 0.0f : ldexpf(exp2_hw(float(x - w)), int(w));  // (2^-150 rounds to 0)
     }
+    // In 64 bits, for a power that is applied again and again.
+    __device__ __forceinline__ double exact(int64_t n) const { return exp2(g2 * double(n)); }
+};
+
+// The decay of a chunk, one fp32 number per chunk whose product from any chunk
+// to any other is off by a rounding or two: what a rounding takes from one is
+// given to the next. (lambda^Q rounded once and applied n times is off by n
+// roundings of the same sign: 2.6e-5 over 1024 chunks of 32 at lambda = 1 - 2^-9.)
+struct Keep {
+    float hi, lo, debt;
+    __device__ __forceinline__ explicit Keep(double r)
+        : hi(float(r)), lo(r < 3e38 ? float(r - double(float(r))) : 0.0f), debt(lo) {}
+    __device__ __forceinline__ float next() {
+        const float k = hi + debt;
+        debt = debt - (k - hi) + lo;
+        return k;
+    }
 };
 
 // ---- the walk ------------------------------------------------------------------
@@ -546,7 +563,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
 #pragma unroll
         for (int q = 0; q < QB; ++q) wq[q] = sc_upd * dec.pow(KB * (QB - 1 - q));
 
-        float keep = dec.pow(Q);  // of the entering state over a chunk
+        Keep whole(dec.exact(Q));  // of the entering state over a chunk
         const int so = int(g.H) * P, po = col0 + 4 * gq;  // a lane's 4 output columns
         const int vo = po < P ? (w.rev ? 15 - m : m) * so + po : kInvalid;  // (elements)
         if (!STATE && tid < 2) odds[tid] = 0;
@@ -559,14 +576,12 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             const T* As = As2[STATE ? 0 : c & 1];
             const T* Bs = Bs2[c & 1];
             const T* Cs = Cs2[c & 1];
-            if (c < 2 && skip0 > 0) {  // into, and out of, the partial chunk
-                keep = dec.pow(nv);
-                if (!STATE)
+            if (!STATE && c < 2 && skip0 > 0) {  // into, and out of, the partial chunk
 #pragma unroll
-                    for (int k = 0; k < TT; ++k) {
-                        const int n = 16 * k + m - skip;
-                        up[k] = sc_carry * dec.pow((n > 0 ? n : 0) + e0);
-                    }
+                for (int k = 0; k < TT; ++k) {
+                    const int n = 16 * k + m - skip;
+                    up[k] = sc_carry * dec.pow((n > 0 ? n : 0) + e0);
+                }
             }
             Frag cf[QB];
 #pragma unroll
@@ -715,6 +730,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                 __syncthreads();
             }
             // ---- state: H <- lambda^n H + B^T (w c) ----
+            const float keep = skip > 0 ? dec.pow(nv) : whole.next();
             if (odd)
 #pragma unroll
                 for (int q = 0; q < QB; ++q) cf[q] = col_frag<T, PT>(Cs, KB * q, wv * 16, 4, lane);
@@ -884,7 +900,8 @@ dim3 grid_of(int64_t n) { return dim3(unsigned(n < (int64_t(1) << 29) ? (n + 255
 
 // Entering states of the runs: on entry run_state (and run_slope) hold the
 // runs' own end states from zero (the first one's from the walk's entering
-// state); on return the states leaving them. One thread per state element.
+// state); on return the states leaving them. One thread per state element, in
+// 64 bits: there may be many runs.
 struct CarryArgs {
     float* state;
     float* slope;  // or null
@@ -900,12 +917,13 @@ __global__ __launch_bounds__(256) void carry_kernel(CarryArgs g) {
         const int64_t bh = i / g.KP;
         const int64_t len = entry_length(g.lengths, bh / g.H, g.L);
         const Decay dec(g.log_decay[bh % g.H]);
-        float s = x[0], d = y ? y[0] : 0.0f;
+        double s = x[0], d = y ? y[0] : 0.0;
+        const double whole = dec.exact(g.seg_len);
         for (int r = 1; r < g.runs; ++r) {
             const int64_t left = len - r * g.seg_len, n = left < 0 ? 0 : left < g.seg_len ? left : g.seg_len;
-            const float keep = dec.pow(n);
-            if (y) y[r * g.stride] = d = fmaf(keep, fmaf(float(n), s, d), y[r * g.stride]);
-            x[r * g.stride] = s = fmaf(keep, s, x[r * g.stride]);
+            const double keep = n == g.seg_len ? whole : dec.exact(n);
+            if (y) y[r * g.stride] = float(d = fma(keep, fma(double(n), s, d), double(y[r * g.stride])));
+            x[r * g.stride] = float(s = fma(keep, s, double(x[r * g.stride])));
         }
     }
 }

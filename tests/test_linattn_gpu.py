@@ -463,3 +463,36 @@ def test_nothing_is_read_past_the_tensors(dtype, segments):
     a, b = bwd(p, **kw), bwd(one, **kw)
     for n in b:
         assert torch.equal(a[n][1:2], b[n]) and torch.isfinite(b[n]).all(), n
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segments", [1, 5])
+@pytest.mark.parametrize("memory", [9, 12, 16])
+def test_decay_over_many_chunks(memory, segments, dtype):
+    """States that are only decayed, by (1 - 2^-memory)^16001: last_state, dh0 and dlog_decay. Counted in
+    roundings of 2^-24. The n chunks (32 or 64 tokens) round the state once each, either way alike: at most
+    1 / sqrt(3) of a rounding (standard deviation), sqrt(n / 3) for an element, sqrt(n / 3 / E) for the mean
+    of E elements. The decay itself may be off by 6 roundings in all (two powers, the product of the
+    chunks' decays, the stored result), not by n of them."""
+    L, H, d = 16001, 2, 64
+    case(f"decay over many chunks 1 - 2^-{memory} segments={segments} {dtype}")
+    decay = torch.full((H,), -(2.0 ** -memory)).log1p()
+    p = make(1, L, H, H, d, d, DT[dtype], seed=32, h0=True, grads=True, decay=decay)
+    p["h0"], p["dlast"] = p["h0"].abs() + 1, p["dlast"].abs() + 1
+    p["q"].zero_(), p["k"].zero_()
+    whole = np.exp(decay.double().numpy() * L)[None, :, None, None]
+    h0, dlast = to_np(p["h0"]), to_np(p["dlast"])
+    r = bwd(p, segments=segments, scale=1.0)
+    n, E = L / (32 if dtype == "f32" else 64) + 1, d * d
+    for what, got, want in (("last_state", fwd(p, segments=segments, scale=1.0)[1], whole * h0),
+                            ("dh0", r["dh0"], whole * dlast)):
+        off = (to_np(got) / want - 1) * 2.0 ** 24
+        mean, worst = np.abs(off.mean((2, 3))).max(), np.abs(off).max()
+        print(f"[parity] {what}: mean {mean:.2f}, largest {worst:.2f} roundings", flush=True)
+        assert mean <= 6 + 6 * (n / 3 / E) ** 0.5, what
+        assert worst <= 6 + 6 * (n / 3) ** 0.5, what
+    # T_L = L lambda^L h0 (two roundings more a chunk), summed over E elements in 16 lots a lane, a wave, 4 waves
+    want = L * (whole * h0 * dlast).sum((0, 2, 3))
+    off = np.abs(to_np(r["dlog_decay"]) / want - 1).max() * 2.0 ** 24
+    print(f"[parity] dlog_decay: {off:.2f} roundings", flush=True)
+    assert off <= 6 + 6 * (n / E) ** 0.5 + 16 + 6 + 4
