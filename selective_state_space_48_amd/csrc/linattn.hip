@@ -51,6 +51,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+__device__ __forceinline__ f32x4 fma4(const f32x4& a, float b, const f32x4& c) {
+    return __builtin_elementwise_fma(a, f32x4{b, b, b, b}, c);
+}
+
 template <typename T> struct Ops;
 
 template <> struct Ops<bf16_bits> {
@@ -514,16 +518,17 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
         // ---- state: tiles of 16 rows, one column of 16 per wave ----
         // An accumulator pair becomes one bf16 operand if its rows are dealt out as
         // n = 32 (kt / 2) + 8 (m / 4) + 4 (kt % 2) + m % 4.
-        auto row_of = [&](int kt, int r) { return BF ? 32 * (kt / 2) + 8 * gq + 4 * (kt % 2) + r : 16 * kt + 4 * gq + r; };
         f32x4 S[KT];
         f32x4 D[SLOPE ? KT : 1];
         auto each_state = [&](auto f) {
-            const int p = col0 + m;
+            int own = lane;  // (opaque: no address is kept from the entering state's loads to the leaving one's stores)
+            asm volatile("" : "+v"(own));
+            const int p = col0 + own % 16, g4 = own / 16;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int n = row_of(kt, r);
+                    const int n = BF ? 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2) + r : 16 * kt + 4 * g4 + r;
                     f(kt, r, n, p, n < K && p < P);
                 }
         };
@@ -734,25 +739,33 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             if (odd)
 #pragma unroll
                 for (int q = 0; q < QB; ++q) cf[q] = col_frag<T, PT>(Cs, KB * q, wv * 16, 4, lane);
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                if (SLOPE) D[kt] = (D[kt] + S[kt] * float(nv)) * keep;
-                S[kt] *= keep;
-            }
+            Frag cw[QB][O::TU], cd[SLOPE ? QB : 1][O::TU];
 #pragma unroll
             for (int q = 0; q < QB; ++q) {
-                Frag cw[O::TU], cd[O::TU];
                 float v[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[e] = we[e] * wq[q] * O::value(cf[q], e);
-                O::template split<O::TU, false>(v, cw);
-                if (SLOPE) {
+                O::template split<O::TU, false>(v, cw[q]);
+                if constexpr (SLOPE) {
 #pragma unroll
                     for (int e = 0; e < E; ++e) v[e] *= float(Q - 1 - (KB * q + E * gq + e) + e1);
-                    O::template split<O::TU, false>(v, cd);
+                    O::template split<O::TU, false>(v, cd[q]);
+                }
+            }
+#pragma unroll
+            for (int kt = 0; kt < KT; kt += 4) {
+                // The products are summed from zero and added to the state by the vector
+                // units, which round: a bf16 matrix product cuts off what its accumulator
+                // does not hold, and a state that takes six of them a chunk loses 1.5e-5 at
+                // lambda = 1 - 2^-16 (1.9e-6 at most this way, of either sign).
+                f32x4 u[4], ud[SLOPE ? 4 : 1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u[i] = f32x4{};
+                    if (SLOPE) ud[i] = f32x4{};
                 }
 #pragma unroll
-                for (int kt = 0; kt < KT; kt += 4) {
+                for (int q = 0; q < QB; ++q) {
                     Frag f[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -762,9 +775,14 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                     for (int k = 0; k < O::TU; ++k)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            S[kt + i] = O::mfma(f[i], cw[k], S[kt + i]);
-                            if (SLOPE) D[kt + i] = O::mfma(f[i], cd[k], D[kt + i]);
+                            u[i] = O::mfma(f[i], cw[q][k], u[i]);
+                            if (SLOPE) ud[i] = O::mfma(f[i], cd[q][k], ud[i]);
                         }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (SLOPE) D[kt + i] = fma4(fma4(S[kt + i], float(nv), D[kt + i]), keep, ud[i]);
+                    S[kt + i] = fma4(S[kt + i], keep, u[i]);
                 }
             }
             __syncthreads();

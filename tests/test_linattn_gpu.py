@@ -496,3 +496,44 @@ def test_decay_over_many_chunks(memory, segments, dtype):
     off = np.abs(to_np(r["dlog_decay"]) / want - 1).max() * 2.0 ** 24
     print(f"[parity] dlog_decay: {off:.2f} roundings", flush=True)
     assert off <= 6 + 6 * (n / E) ** 0.5 + 16 + 6 + 4
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segments", [1, 5])
+@pytest.mark.parametrize("memory", [12, 16])
+def test_sums_over_many_chunks(memory, segments, dtype):
+    """States that grow over 16001 tokens of positive keys and values: last_state, dh0 and dlog_decay against
+    their sums in 64 bits. Counted in roundings of 2^-24, and measured as the decays' errors are: a chunk
+    rounds the state once, either way alike. Off to one side may be a chunk's own sum (6 products of two
+    operands and three terms, cut off by at most 2 each), its tokens' weights (8) and the decays (6), not
+    what n chunks add up to."""
+    L, H, d = 16001, 2, 64
+    case(f"sums over many chunks 1 - 2^-{memory} segments={segments} {dtype}")
+    decay = torch.full((H,), -(2.0 ** -memory)).log1p()
+    p = make(1, L, H, H, d, d, DT[dtype], seed=33, h0=True, grads=True, decay=decay)
+    for n in ("q", "k", "v", "dy", "h0", "dlast"):
+        p[n] = p[n].abs() + 0.1
+    x = {n: to_np(p[n])[0] for n in ("q", "k", "v", "dy", "h0", "dlast")}
+    g, t = decay.double().numpy(), np.arange(L)[:, None]
+
+    def state(a, b, w, first, far):  # [H, d, d]
+        return np.stack([(a[:, h] * w[:, h:h + 1]).T @ b[:, h] for h in range(H)]) + far[:, None, None] * first
+
+    left = L - 1 - t
+    S = state(x["k"], x["v"], np.exp(g * left), x["h0"], np.exp(g * L))
+    T = state(x["k"], x["v"], np.exp(g * left) * left, x["h0"], L * np.exp(g * L))
+    M = state(x["q"], x["dy"], np.exp(g * (t + 1)), x["dlast"], np.exp(g * L))
+    n, E = L / (32 if dtype == "f32" else 64) + 1, d * d
+    one_side = 6 * 2 + 8 + 6
+    for what, got, want in (("last_state", fwd(p, segments=segments, scale=1.0)[1], S),
+                            ("dh0", bwd(p, segments=segments, scale=1.0)["dh0"], M)):
+        off = (to_np(got)[0] / want - 1) * 2.0 ** 24
+        mean, worst = np.abs(off.mean((1, 2))).max(), np.abs(off).max()
+        print(f"[parity] {what}: mean {mean:.2f}, largest {worst:.2f} roundings", flush=True)
+        assert mean <= one_side + 6 * (n / 3 / E) ** 0.5, what
+        assert worst <= one_side + 6 * (n / 3) ** 0.5, what
+    p["dy"] = torch.zeros_like(p["dy"])  # <dlast, T_L> alone, summed in 16 lots a lane, a wave, 4 waves
+    off = to_np(bwd(p, segments=segments, scale=1.0)["dlog_decay"]) / (T * x["dlast"]).sum((1, 2)) - 1
+    off = np.abs(off).max() * 2.0 ** 24
+    print(f"[parity] dlog_decay: {off:.2f} roundings", flush=True)
+    assert off <= one_side + 6 * (n / E) ** 0.5 + 16 + 6 + 4
