@@ -621,7 +621,9 @@ int selscan_linattn_bwd_workspace_size(const selscan_linattn_dims_t* dims,
  *                  else NULL
  *   weight, bias : [C] fp32 or NULL (1 and 0)
  *   mean, rstd   : [N, G] fp32 outputs or NULL (both or neither)
- * dims: C a multiple of G (> 0); eps >= 0 and finite. Statistics in fp32,
+ * dims: C a multiple of G (> 0), C <= 2^24, S < 2^31, N * G < 2^31; every
+ * N * S * C below 2^33 is taken (above it, SELSCAN_ERR_DIMS where a grid or
+ * the partial sums would not fit); eps >= 0 and finite. Statistics in fp32,
  * the variance from differences to the mean. y must not overlap any input.
  * workspace as in selscan_fwd_opts_t (selscan_groupnorm_workspace_size();
  * opts may be NULL). Deterministic.

@@ -455,57 +455,59 @@ __global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
 template <typename T, bool BWD>
 __global__ __launch_bounds__(1024) void plain_kernel(GnArgs a) {
     __shared__ float red[16];
-    const int64_t n = blockIdx.x / a.G, g = blockIdx.x % a.G, cnt = a.S * a.D;
-    const int64_t base = n * a.S * a.C + g * a.D;
-    const T* x = static_cast<const T*>(a.x) + base;
-    const T* z = static_cast<const T*>(a.z) + base;
-    const bool gate = a.act == SELSCAN_ACT_GATE;
-    auto each = [&](auto f) {
-        for (int64_t i = threadIdx.x; i < cnt; i += blockDim.x) f(i / a.D * a.C + i % a.D, g * a.D + i % a.D);
-    };
-    if (!BWD) {
-        T* y = static_cast<T*>(a.y) + base;
-        float s = 0.0f;
-        each([&](int64_t i, int64_t) { s += to_f32(x[i]); });
-        const float mean = block_sum(s, red) / float(cnt);
-        s = 0.0f;
-        each([&](int64_t i, int64_t) {
-            const float d = to_f32(x[i]) - mean;
-            s = fmaf(d, d, s);
-        });
-        const float rstd = 1.0f / sqrtf(block_sum(s, red) / float(cnt) + a.eps);
-        each([&](int64_t i, int64_t c) {
-            const float u = fmaf((to_f32(x[i]) - mean) * rstd, a.weight ? a.weight[c] : 1.0f, a.bias ? a.bias[c] : 0.0f);
-            y[i] = from_f32<T>(activate(u, a.act, gate ? to_f32(z[i]) : 0.0f));
-        });
-        if (a.mean && threadIdx.x == 0) {
-            a.mean[blockIdx.x] = mean;
-            a.rstd[blockIdx.x] = rstd;
-        }
-    } else {
-        const T* dy = static_cast<const T*>(a.dy) + base;
-        T* dx = static_cast<T*>(a.dx) + base;
-        T* dz = static_cast<T*>(a.dz) + base;
-        const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
-        float s1 = 0.0f, s2 = 0.0f;
-        auto grad = [&](int64_t i, int64_t c, float* xh, float* d) {
-            const float w = a.weight ? a.weight[c] : 1.0f;
-            *xh = (to_f32(x[i]) - mean) * rstd;
-            return w * grad_u(a.act, fmaf(*xh, w, a.bias ? a.bias[c] : 0.0f), to_f32(dy[i]), gate ? to_f32(z[i]) : 0.0f, d);
+    for (int64_t inst = blockIdx.x; inst < a.N * a.G; inst += gridDim.x) {
+        const int64_t n = inst / a.G, g = inst % a.G, cnt = a.S * a.D;
+        const int64_t base = n * a.S * a.C + g * a.D;
+        const T* x = static_cast<const T*>(a.x) + base;
+        const T* z = static_cast<const T*>(a.z) + base;
+        const bool gate = a.act == SELSCAN_ACT_GATE;
+        auto each = [&](auto f) {
+            for (int64_t i = threadIdx.x; i < cnt; i += blockDim.x) f(i / a.D * a.C + i % a.D, g * a.D + i % a.D);
         };
-        each([&](int64_t i, int64_t c) {
-            float xh, d;
-            const float e = grad(i, c, &xh, &d);
-            s1 += e;
-            s2 = fmaf(e, xh, s2);
-        });
-        const float m1 = block_sum(s1, red) / float(cnt), m2 = block_sum(s2, red) / float(cnt);
-        each([&](int64_t i, int64_t c) {
-            float xh, d;
-            const float e = grad(i, c, &xh, &d);
-            dx[i] = from_f32<T>(rstd * (e - m1 - xh * m2));
-            if (gate) dz[i] = from_f32<T>(d);
-        });
+        if (!BWD) {
+            T* y = static_cast<T*>(a.y) + base;
+            float s = 0.0f;
+            each([&](int64_t i, int64_t) { s += to_f32(x[i]); });
+            const float mean = block_sum(s, red) / float(cnt);
+            s = 0.0f;
+            each([&](int64_t i, int64_t) {
+                const float d = to_f32(x[i]) - mean;
+                s = fmaf(d, d, s);
+            });
+            const float rstd = 1.0f / sqrtf(block_sum(s, red) / float(cnt) + a.eps);
+            each([&](int64_t i, int64_t c) {
+                const float u = fmaf((to_f32(x[i]) - mean) * rstd, a.weight ? a.weight[c] : 1.0f, a.bias ? a.bias[c] : 0.0f);
+                y[i] = from_f32<T>(activate(u, a.act, gate ? to_f32(z[i]) : 0.0f));
+            });
+            if (a.mean && threadIdx.x == 0) {
+                a.mean[inst] = mean;
+                a.rstd[inst] = rstd;
+            }
+        } else {
+            const T* dy = static_cast<const T*>(a.dy) + base;
+            T* dx = static_cast<T*>(a.dx) + base;
+            T* dz = static_cast<T*>(a.dz) + base;
+            const float mean = a.mean[inst], rstd = a.rstd[inst];
+            float s1 = 0.0f, s2 = 0.0f;
+            auto grad = [&](int64_t i, int64_t c, float* xh, float* d) {
+                const float w = a.weight ? a.weight[c] : 1.0f;
+                *xh = (to_f32(x[i]) - mean) * rstd;
+                return w * grad_u(a.act, fmaf(*xh, w, a.bias ? a.bias[c] : 0.0f), to_f32(dy[i]), gate ? to_f32(z[i]) : 0.0f, d);
+            };
+            each([&](int64_t i, int64_t c) {
+                float xh, d;
+                const float e = grad(i, c, &xh, &d);
+                s1 += e;
+                s2 = fmaf(e, xh, s2);
+            });
+            const float m1 = block_sum(s1, red) / float(cnt), m2 = block_sum(s2, red) / float(cnt);
+            each([&](int64_t i, int64_t c) {
+                float xh, d;
+                const float e = grad(i, c, &xh, &d);
+                dx[i] = from_f32<T>(rstd * (e - m1 - xh * m2));
+                if (gate) dz[i] = from_f32<T>(d);
+            });
+        }
     }
 }
 
@@ -680,7 +682,9 @@ void launch_v(const GnArgs& a, const Plan& p, hipStream_t st) {
 template <typename T, bool BWD>
 void launch(const GnArgs& a, const Plan& p, hipStream_t st) {
     if (p.kind == Plan::kPlain) {
-        hipLaunchKernelGGL((plain_kernel<T, BWD>), dim3(unsigned(a.N * a.G)), dim3(unsigned(p.threads)), 0, st, a);
+        const int64_t inst = a.N * a.G, most = int64_t(1) << 21;
+        hipLaunchKernelGGL((plain_kernel<T, BWD>), dim3(unsigned(inst < most ? inst : most)), dim3(unsigned(p.threads)),
+                           0, st, a);
         if (BWD && a.part)
             hipLaunchKernelGGL((plain_cols_kernel<T>), dim3(unsigned(p.parts), unsigned(ceil_div(a.C, 256))), dim3(256),
                                0, st, a);
@@ -694,12 +698,13 @@ void launch(const GnArgs& a, const Plan& p, hipStream_t st) {
 
 }  // namespace
 
-// A grid has fewer than 2^32 threads; slabs and partial sums are counted in 32 bits.
+// A grid has fewer than 2^32 threads, and fewer than 2^16 workgroups along z (runs of partial sums).
 bool groupnorm_fits(const GroupnormShape& s, bool backward) {
     if (s.N * s.S * s.C == 0) return true;
     const Plan p = plan_of(s, backward);
-    if (p.kind == Plan::kRows) return true;
-    return p.parts <= (int64_t(1) << 22) && s.N * s.G * p.slabs * p.threads < (int64_t(1) << 32);
+    if (p.kind != Plan::kBlock) return true;
+    const int64_t grid = p.slabs == 1 ? ceil_div(s.N, p.per) * s.G : s.N * s.G * p.slabs;
+    return grid * p.threads < (int64_t(1) << 32) && (!backward || p.parts <= int64_t(65535) * kJoin);
 }
 
 size_t groupnorm_workspace_bytes(const GroupnormShape& s, bool backward) {

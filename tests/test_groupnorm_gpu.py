@@ -274,3 +274,35 @@ def test_layer_chain(dtype):
     from linattn_util import relative
     for n in gr:
         close(gr[n], want[n], size[n], gr[n].dtype, relative(DT[dtype], L + 78, d, d), f"chain {dtype} {n}")
+
+
+@pytest.mark.parametrize("shape", [(131072, 2, 512, 512), ((1 << 21) + 77, 1, 1025, 1)])
+def test_many_entries(shape):
+    """Many entries of many small groups, and more rows of wide groups than workgroups: the last entries
+    against a call on them alone, the column sums against 64 bits."""
+    N, S, C, G = shape
+    case(f"many entries {shape}")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    full = (N, C) if S == 1 else (N, S, C)
+    x, dy = (torch.empty(full, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    w = torch.ones(C, device="cuda")
+    y, mean, rstd = selscan.groupnorm(x, G, w)
+    r = selscan.groupnorm_bwd(x, G, w, dy=dy, mean=mean, rstd=rstd)
+    last = x[-70:].clone(), dy[-70:].clone()  # (a view of odd rows would not be aligned)
+    y1, m1, s1 = selscan.groupnorm(last[0], G, w)
+    r1 = selscan.groupnorm_bwd(last[0], G, w, dy=last[1], mean=m1, rstd=s1)
+    torch.cuda.synchronize()
+    assert torch.equal(y[-70:], y1) and torch.equal(mean[-70:], m1) and torch.equal(rstd[-70:], s1)
+    assert torch.equal(r["dx"][-70:], r1["dx"])
+    want = {n: torch.zeros(C, dtype=torch.float64, device="cuda") for n in ("dweight", "dbias", "sw", "sb")}
+    for a in range(0, N, 1 << 17):
+        part = slice(a, a + (1 << 17))
+        per = lambda t: t[part].double().repeat_interleave(C // G, 1)[:, None]  # noqa: E731
+        d = dy[part].double().reshape(-1, S, C)
+        t = d * (x[part].double().reshape(-1, S, C) - per(mean)) * per(rstd)
+        for n, v in (("dweight", t), ("dbias", d), ("sw", t.abs()), ("sb", d.abs())):
+            want[n] += v.sum((0, 1))
+    # at most N S / 64 + 64 additions each and 8 roundings of a term, either way alike: six times their root
+    c = 6 * (N * S / 64 + 72) ** 0.5 * 2.0 ** -24
+    close(r["dweight"], to_np(want["dweight"]), to_np(want["sw"]), torch.float32, c, f"many entries {shape} dweight")
+    close(r["dbias"], to_np(want["dbias"]), to_np(want["sb"]), torch.float32, c, f"many entries {shape} dbias")

@@ -1,5 +1,6 @@
 """Refusals of the linear-attention and group-norm calls, before any HIP call (CPU; fake pointers)."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -201,6 +202,37 @@ def test_groupnorm_pointers():
     assert gbwd(d, ws=P(20), ws_bytes=n.value - 1) == S.ERR_CONFIG
     assert gbwd(d, ws=ctypes.c_void_p(P(20).value + 8), ws_bytes=n.value) == S.ERR_CONFIG
     assert gbwd(d, ws=P(7), ws_bytes=n.value) == S.ERR_ALIAS
+
+
+def gn_size(N, S, C, G, dtype=S.BF16, act=0):
+    d, n = gn(N, S, C, G, dtype, act), [ctypes.c_uint64(0), ctypes.c_uint64(0)]
+    return [lib.selscan_groupnorm_workspace_size(ctypes.byref(d), i, ctypes.byref(n[i])) for i in (0, 1)]
+
+
+def test_groupnorm_sizes():
+    """Every size that the header allows is taken, forwards and backwards: 2^32 threads of a workgroup for
+    each entry and group are no limit where a workgroup takes many of them."""
+    both = [S.OK, S.OK]
+    for N in (131071, 131072, 1 << 20):
+        assert gn_size(N, 2, 512, 512) == both, N   # small maps of many narrow groups
+    assert gn_size(5_000_000, 1, 1025, 1, S.F32) == both  # rows wider than a workgroup's vectors
+    assert gn_size(1 << 20, 3, 4097, 1) == both
+    assert gn_size(1 << 16, 1 << 10, 128, 4) == both
+    rng = random.Random(5)
+    for _ in range(3000):
+        log = lambda hi: int(2 ** rng.uniform(0, hi))  # noqa: E731
+        G = log(10)
+        C = G * log(14)
+        rows = (1 << 33) // C
+        N = max(1, min(log(33), rows - 1, (1 << 31) // G - 1))
+        size = N, max(1, min(log(30), (rows - 1) // N)), C, G
+        for dtype in (S.F32, S.BF16):
+            for act in (0, 2):
+                assert gn_size(*size, dtype, act) == both, (size, dtype, act)
+    refused = [S.ERR_DIMS, S.ERR_DIMS]
+    assert gn_size(1 << 30, 1, 8, 2) == refused
+    assert gn_size(1, 1 << 31, 8, 2) == refused
+    assert gn_size(1 << 24, 1 << 15, 64, 1) == refused  # 2^45 values
 
 
 def test_binding_refusals():
