@@ -451,6 +451,10 @@ __global__ __launch_bounds__(1024) void block_kernel(GnArgs a) {
 }
 
 // ---- plain: groups wider than a workgroup's vectors -------------------------------
+//
+// A thread's own sums are as long as the instance is large, so they are kept in 64
+// bits (in 32, what is small beside the sum is lost: 7e-6 of the variance of
+// 65536 values a thread, always to the same side).
 
 template <typename T, bool BWD>
 __global__ __launch_bounds__(1024) void plain_kernel(GnArgs a) {
@@ -466,15 +470,15 @@ __global__ __launch_bounds__(1024) void plain_kernel(GnArgs a) {
         };
         if (!BWD) {
             T* y = static_cast<T*>(a.y) + base;
-            float s = 0.0f;
+            double s = 0.0;
             each([&](int64_t i, int64_t) { s += to_f32(x[i]); });
-            const float mean = block_sum(s, red) / float(cnt);
-            s = 0.0f;
+            const float mean = block_sum(float(s), red) / float(cnt);
+            s = 0.0;
             each([&](int64_t i, int64_t) {
                 const float d = to_f32(x[i]) - mean;
-                s = fmaf(d, d, s);
+                s += d * d;
             });
-            const float rstd = 1.0f / sqrtf(block_sum(s, red) / float(cnt) + a.eps);
+            const float rstd = 1.0f / sqrtf(block_sum(float(s), red) / float(cnt) + a.eps);
             each([&](int64_t i, int64_t c) {
                 const float u = fmaf((to_f32(x[i]) - mean) * rstd, a.weight ? a.weight[c] : 1.0f, a.bias ? a.bias[c] : 0.0f);
                 y[i] = from_f32<T>(activate(u, a.act, gate ? to_f32(z[i]) : 0.0f));
@@ -488,7 +492,7 @@ __global__ __launch_bounds__(1024) void plain_kernel(GnArgs a) {
             T* dx = static_cast<T*>(a.dx) + base;
             T* dz = static_cast<T*>(a.dz) + base;
             const float mean = a.mean[inst], rstd = a.rstd[inst];
-            float s1 = 0.0f, s2 = 0.0f;
+            double s1 = 0.0, s2 = 0.0;
             auto grad = [&](int64_t i, int64_t c, float* xh, float* d) {
                 const float w = a.weight ? a.weight[c] : 1.0f;
                 *xh = (to_f32(x[i]) - mean) * rstd;
@@ -498,9 +502,9 @@ __global__ __launch_bounds__(1024) void plain_kernel(GnArgs a) {
                 float xh, d;
                 const float e = grad(i, c, &xh, &d);
                 s1 += e;
-                s2 = fmaf(e, xh, s2);
+                s2 += e * xh;
             });
-            const float m1 = block_sum(s1, red) / float(cnt), m2 = block_sum(s2, red) / float(cnt);
+            const float m1 = block_sum(float(s1), red) / float(cnt), m2 = block_sum(float(s2), red) / float(cnt);
             each([&](int64_t i, int64_t c) {
                 float xh, d;
                 const float e = grad(i, c, &xh, &d);
@@ -518,18 +522,18 @@ __global__ __launch_bounds__(256) void plain_cols_kernel(GnArgs a) {
     if (c >= a.C) return;
     const int64_t g = c / a.D, r0 = int64_t(blockIdx.x) * a.per, r1 = r0 + a.per < rows ? r0 + a.per : rows;
     const float w = a.weight ? a.weight[c] : 1.0f, b = a.bias ? a.bias[c] : 0.0f;
-    float sw = 0.0f, sb = 0.0f;
+    double sw = 0.0, sb = 0.0;
     for (int64_t r = r0; r < r1; ++r) {
         const int64_t n = r / a.S, j = r * a.C + c;
         const float xh = (to_f32(static_cast<const T*>(a.x)[j]) - a.mean[n * a.G + g]) * a.rstd[n * a.G + g];
         float dz;
         const float du = grad_u(a.act, fmaf(xh, w, b), to_f32(static_cast<const T*>(a.dy)[j]),
                                 a.act == SELSCAN_ACT_GATE ? to_f32(static_cast<const T*>(a.z)[j]) : 0.0f, &dz);
-        sw = fmaf(du, xh, sw);
+        sw += du * xh;
         sb += du;
     }
-    a.part[(int64_t(blockIdx.x) * 2 + 0) * a.C + c] = sw;
-    a.part[(int64_t(blockIdx.x) * 2 + 1) * a.C + c] = sb;
+    a.part[(int64_t(blockIdx.x) * 2 + 0) * a.C + c] = float(sw);
+    a.part[(int64_t(blockIdx.x) * 2 + 1) * a.C + c] = float(sb);
 }
 
 // Column sums over runs of kJoin parts (grid z), 16 interleaved rows of them

@@ -306,3 +306,31 @@ def test_many_entries(shape):
     c = 6 * (N * S / 64 + 72) ** 0.5 * 2.0 ** -24
     close(r["dweight"], to_np(want["dweight"]), to_np(want["sw"]), torch.float32, c, f"many entries {shape} dweight")
     close(r["dbias"], to_np(want["dbias"]), to_np(want["sb"]), torch.float32, c, f"many entries {shape} dbias")
+
+
+def test_wide_groups_over_many_positions():
+    """80000 values a thread, with an offset: the statistics and the averages of the gradients. In roundings
+    of 2^-24: a workgroup's sum of its threads' is 6 + 16 additions, and 8 more for an average, a root, a
+    quotient and the difference that a term is; not what the threads' own sums pass through."""
+    N, S, C = 1, 40000, 2051
+    case(f"wide groups over many positions {N, S, C}")
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x = torch.randn((N, S, C), device="cuda", generator=g).add_(3.0)
+    dy = torch.randn((N, S, C), device="cuda", generator=g).add_(x, alpha=0.5)
+    y, mean, rstd = selscan.groupnorm(x, 1)
+    r = selscan.groupnorm_bwd(x, 1, dy=dy, mean=mean, rstd=rstd)
+    torch.cuda.synchronize()
+    c = 30 * 2.0 ** -24
+    xd = x.double()
+    m, v = xd.mean(), xd.var(correction=0) + 1e-5
+    for what, got, want in (("mean", mean, m), ("rstd", rstd, v.rsqrt())):
+        off = abs(got.double().item() / want.item() - 1)
+        print(f"[parity] wide groups {what}: {off * 2 ** 24:.2f} roundings", flush=True)
+        assert off <= c, what
+    xh, e = xd.sub_(mean.double()).mul_(rstd.double()), dy.double()
+    m1, m2 = e.mean(), (e * xh).mean()
+    want = (e - m1 - xh * m2) * rstd.double()
+    room = (e.abs() + m1.abs() + xh.abs() * m2.abs()) * rstd.double() * c
+    worst = ((r["dx"].double() - want).abs() / room).max().item()
+    print(f"[parity] wide groups dx: {worst:.3f} of the tolerance", flush=True)
+    assert worst <= 1
