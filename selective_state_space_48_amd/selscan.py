@@ -556,8 +556,8 @@ def _scale(scale: Optional[float]) -> float:
     """The C calls' scale: 0 stands for 1 / sqrt(dk)."""
     if scale is None:
         return 0.0
-    if scale == 0:
-        raise ValueError("scale must not be 0 (None: 1 / sqrt(dk))")
+    if ctypes.c_float(scale).value == 0:  # (a double that fp32 has no number for, too)
+        raise ValueError("scale must not be 0 in fp32 (None: 1 / sqrt(dk))")
     return float(scale)
 
 

@@ -266,3 +266,11 @@ def test_binding_refusals():
         S.groupnorm(z(2, 2, 2, 8), 2)
     with pytest.raises(ValueError):
         S.groupnorm_bwd(x, 2, dy=x, mean=z(6, 3), rstd=z(6, 2))
+
+
+def test_binding_scale():
+    """A scale that is 0 in fp32 is refused: the C calls would take it for the default."""
+    for bad in (0, 0.0, -0.0, 1e-46, -1e-300):
+        with pytest.raises(ValueError):
+            S._scale(bad)
+    assert S._scale(None) == 0 and S._scale(-0.5) == -0.5 and S._scale(1e-40) == 1e-40
