@@ -482,7 +482,10 @@ int selscan_ssd_step(float* state, const void* x, const void* delta, const float
  *   k, v       : [B, L, Hkv, dk], [B, L, Hkv, dv] of dtype; head h reads kv
  *                head h / (H / Hkv)
  *   log_decay  : [H] fp32, the natural logarithm of each head's decay per
- *                token (0: nothing is forgotten; -inf: only the token itself)
+ *                token (0: nothing is forgotten; -inf: only the token itself;
+ *                above 0 the state grows, and what passes the range of fp32
+ *                comes out as an infinity or a NaN, with |scale| > 1 also
+ *                where lambda^64 |scale| does)
  *   y          : [B, L, H, dv] of dtype (output)
  *   last_state : [B, H, dk, dv] fp32 output or NULL
  * dims: H a multiple of Hkv; dk, dv multiples of 8 from 8 to 256 (else

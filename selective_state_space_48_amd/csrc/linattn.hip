@@ -207,6 +207,7 @@ struct Keep {
 
 constexpr int kInvalid = int(0x80000000u);  // a buffer offset past every resource
 
+
 struct WalkArgs {
     LinattnWalk w[3];
     int32_t roles, tiles, segments;  // segments of this launch
@@ -295,6 +296,14 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
     __shared__ alignas(16) T Os[STATE || !VIA ? 16 : Q * SO];
     __shared__ float red[NW];
     __shared__ int odds[2];  // number + 1 of the last (even, odd) chunk with a value that is not finite
+
+    // Weights inside a chunk are cut at the largest number, so that where a state
+    // grows an empty slot's weight times its zeros stays 0. Where a token's own
+    // weight is cut, the decay of its chunk or the factor of the entering state is
+    // an infinity, and what comes out is not finite (a scale above 1 is in the
+    // first alone, so those calls are left uncut).
+    const float most = fabsf(g.scale) <= 1.0f ? 3.4028235e38f : __builtin_inff();
+    auto cut = [&](float x) { return __builtin_amdgcn_fmed3f(x, -most, most); };
 
     const int tid = threadIdx.x, lane = tid % 64, m = lane % 16, gq = lane / 16;
     const int wv = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -396,7 +405,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int d = m - 4 * gq - r;
-                diag[r] = d >= 0 ? g.scale * dec.pow(d) : 0.0f;
+                diag[r] = d >= 0 ? cut(g.scale * dec.pow(d)) : 0.0f;
                 base[r] = g.scale * dec.pow(16 + d);
             }
             pw16 = dec.pow(16);
@@ -440,7 +449,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     // (a masked score may be infinite or NaN: selected, not multiplied away)
-                    v[r] = gap == 0 ? (m >= 4 * gq + r ? acc[i][r] * diag[r] : 0.0f) : acc[i][r] * (base[r] * far);
+                    v[r] = gap == 0 ? (m >= 4 * gq + r ? acc[i][r] * diag[r] : 0.0f) : acc[i][r] * cut(base[r] * far);
                     v2[r] = v[r] * float(t - s - r);
                 }
                 auto put = [&](int first_tile, int terms, const float (&x)[4]) {
@@ -744,7 +753,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             for (int q = 0; q < QB; ++q) {
                 float v[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = we[e] * wq[q] * O::value(cf[q], e);
+                for (int e = 0; e < E; ++e) v[e] = cut(we[e] * wq[q]) * O::value(cf[q], e);
                 O::template split<O::TU, false>(v, cw[q]);
                 if constexpr (SLOPE) {
 #pragma unroll

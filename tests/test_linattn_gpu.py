@@ -537,3 +537,22 @@ def test_sums_over_many_chunks(memory, segments, dtype):
     off = np.abs(off).max() * 2.0 ** 24
     print(f"[parity] dlog_decay: {off:.2f} roundings", flush=True)
     assert off <= one_side + 6 * (n / E) ** 0.5 + 16 + 6 + 4
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("L,decay", [(1, [8.0, 80.0, 0.0]), (5, [6.0, 12.0, 1.5]), (30, [2.0, 1.5, 0.4])])
+def test_states_that_grow(L, decay, dtype):
+    """Short prompts of heads that grow fast: lambda to the length of a chunk may be past fp32 where lambda to
+    the length of the prompt is not."""
+    case(f"states that grow {decay} L={L} {dtype}")
+    p = make(2, L, 3, 3, 32, 40, DT[dtype], seed=34, h0=True, grads=True, decay=torch.tensor(decay),
+             lengths=[L, L // 2])
+    for scale in (None, -1.0):
+        check_fwd(p, f"grow {decay} {dtype} {scale}", scale=scale)
+        check_bwd(p, f"grow {decay} {dtype} {scale}", scale=scale)
+    p = make(1, 130, 2, 2, 32, 40, DT[dtype], seed=35, grads=True, decay=torch.tensor([1.5, -0.5]))
+    y, s = fwd(p, scale=1.0)  # sums past fp32: not finite, and not finite numbers in their place
+    want = fwd_ref(p, 1.0)
+    past = np.abs(want[0]) > 3e38
+    assert past.any() and not np.isfinite(to_np(y)[past]).any() and not torch.isfinite(s[:, 0]).any()
+    assert torch.isfinite(y[:, :, 1]).all() and torch.isfinite(s[:, 1]).all()
