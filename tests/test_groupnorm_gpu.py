@@ -334,3 +334,24 @@ def test_wide_groups_over_many_positions():
     worst = ((r["dx"].double() - want).abs() / room).max().item()
     print(f"[parity] wide groups dx: {worst:.3f} of the tolerance", flush=True)
     assert worst <= 1
+
+
+@pytest.mark.parametrize("shape,dtype,act", [((8300, 1, 4096, 32), "bf16", "gate"), ((8300, 1, 4096, 4), "bf16", "silu"),
+                                             ((4200, 1, 4096, 32), "f32", "none"), ((4200, 1, 4096, 4), "f32", "gate")])
+def test_outputs_past_the_caches(shape, dtype, act):
+    """Rows whose output is above 64 MB, which is stored past the caches, against the definition, with the
+    sums over so many rows."""
+    N, S, C, G = shape
+    case(f"outputs past the caches {shape} {dtype} {act}")
+    assert N * C * (2 if dtype == "bf16" else 4) > 64 << 20
+    check(inputs(N, S, C, act, DT[dtype], seed=14), N, S, C, G, act, f"{shape} {dtype} {act}")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(2, 700, 2055, 1), (3, 5, 16400, 2), (1, 40, 33000, 2)])
+def test_wide_groups(shape, dtype, act):
+    """Groups wider than a workgroup's vectors, over few and many positions."""
+    N, S, C, G = shape
+    case(f"wide groups {shape} {dtype} {act}")
+    check(inputs(N, S, C, act, DT[dtype], seed=15, mean=2.0), N, S, C, G, act, f"{shape} {dtype} {act}")

@@ -556,3 +556,80 @@ def test_states_that_grow(L, decay, dtype):
     past = np.abs(want[0]) > 3e38
     assert past.any() and not np.isfinite(to_np(y)[past]).any() and not torch.isfinite(s[:, 0]).any()
     assert torch.isfinite(y[:, :, 1]).all() and torch.isfinite(s[:, 1]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segments", [1, 2, 3])
+def test_state_replaced_in_place(segments, dtype):
+    """The leaving state in the entering one's buffer, over several runs, with entries that end in the first
+    run, before it and at a run's end: the bits of the call with buffers of its own."""
+    case(f"state in place segments={segments} {dtype}")
+    for shape in ((4, 300, 4, 2, 64, 96), (4, 300, 2, 1, 256, 40)):
+        p = make(*shape, DT[dtype], seed=36, h0=True, lengths=[300, 50, 0, 128])
+        y, s = fwd(p, segments=segments)
+        state = p["h0"].clone()
+        q = dict(p, h0=state)
+        y2, s2 = fwd(q, segments=segments, last_state=state)
+        assert s2 is state and torch.equal(y, y2) and torch.equal(s, state)
+        check_fwd(p, f"{shape} {segments} {dtype}", segments=segments)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("widths", [(256, 256), (256, 40), (40, 256), (128, 128)])
+def test_runs_of_wide_heads(widths, dtype):
+    """The runs' own end states (and their derivatives by log_decay) at every width of the state."""
+    case(f"runs of wide heads {widths} {dtype}")
+    p = make(2, 300, 2, 1, *widths, DT[dtype], seed=37, h0=True, lengths=[300, 129], grads=True)
+    for segments in (2, 4):
+        check_fwd(p, f"{widths} {segments} {dtype}", segments=segments)
+        check_bwd(p, f"{widths} {segments} {dtype}", segments=segments)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nan_reaches_later_runs_alone(value, dtype):
+    """As one run, so several: an element that is not finite reaches what the recurrence takes it to."""
+    B, L, H, Hk, dk, dv = 2, 260, 2, 1, 64, 40
+    p = make(B, L, H, Hk, dk, dv, DT[dtype], seed=38, h0=True, grads=True)
+    p["v"] = p["v"].abs() + 0.1  # (an infinity times a sum of either sign stays one)
+    want, size = bwd_ref(p)
+    y, _, ya, _ = fwd_ref(p)
+    want["y"], size["y"] = y, ya
+    c = relative(DT[dtype], L, dk, dv)
+    for name, t, col in (("v", 37, 3), ("k", 150, dk - 2), ("q", 70, 1), ("dy", 140, 5)):
+        case(f"{value} in {name} at token {t} over runs {dtype}")
+        x = dict(p, **{name: p[name].clone()})
+        x[name][0, t, 0, col] = value
+        with np.errstate(invalid="ignore"):
+            y, _, _, _ = fwd_ref(x)
+            poisoned, _ = bwd_ref(x)
+        poisoned = {"y": y, **{n: poisoned[n] for n in ("dq", "dk", "dv")}}
+        r = {"y": fwd(x, segments=3)[0], **bwd(x, segments=3)}
+        check_reach(r, want, poisoned, size, c, f"{name}[{t}] runs")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(110, 32, 8, 256, 128), (210, 32, 32, 128, 128), (400, 32, 16, 64, 128)])
+def test_token_of_a_large_state(shape, dtype):
+    """States above 384 MB, which a step takes past the caches, against the definition (in 64 bits on the GPU)."""
+    B, H, Hk, dk, dv = shape
+    case(f"token of a large state {shape} {dtype}")
+    assert B * H * dk * dv * 4 > 384 << 20
+    g = torch.Generator(device="cuda").manual_seed(39)
+    rn = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    state, q, k, v = rn(B, H, dk, dv), rn(B, H, dk).to(DT[dtype]), rn(B, Hk, dk).to(DT[dtype]), rn(B, Hk, dv).to(DT[dtype])
+    dec = torch.full((H,), -0.03, device="cuda") * torch.arange(H, device="cuda")
+    was = state.double()
+    y = selscan.linattn_step(state, q, k, v, dec)
+    lam = dec.double().exp()[:, None, None]
+    kv = k.double().repeat_interleave(H // Hk, 1)[..., None] * v.double().repeat_interleave(H // Hk, 1)[:, :, None]
+    want, size = lam * was + kv, lam * was.abs() + kv.abs()
+    scale, qd = dk ** -0.5, q.double()[..., None]
+    ry, ya = scale * (qd * want).sum(2), scale * (qd.abs() * size).sum(2)
+    c = relative(torch.float32, 1, dk, dv)
+    assert ((state.double() - want).abs() <= c * size + 2.0 ** -24 * (want.abs() + c * size)).all()
+    close(y, to_np64(ry), to_np64(ya), y.dtype, c, f"token of a large state {shape} {dtype}")
+
+
+def to_np64(t):
+    return t.cpu().numpy()
