@@ -7,13 +7,19 @@
 //         instance, sums by shuffles, weights kept in registers over many rows;
 //   block (a row of the group fits a workgroup's threads): one workgroup per
 //         instance or slab, its values in registers;
-//   plain (wider groups): one workgroup per instance, several passes.
+//   plain (groups of more than 1024 vectors): one workgroup per instance, three
+//         passes, scalar accesses.
 // Measured (MI355X; bytes moved once over the time; a large copy 4.75 TB/s):
 // 16384 rows of 4096 in 32 groups, bf16, gated: 88-97 us (4.2-4.6 TB/s),
 // gradients 152 us (4.4 TB/s); 8 x 2048 x 512 fp32 in 32 groups (64-byte rows),
-// SiLU: 17 us (4.0 TB/s), gradients 30 us (3.4 TB/s).
-// Statistics in fp32 by differences: the mean first, then the squares about it
-// (slabs: their own means, joined by n_i (mean_i - mean)^2).
+// SiLU: 17 us (4.0 TB/s), gradients 30 us (3.4 TB/s). Far from the copy rate:
+// slabs (8 x 16384 x 512 bf16 in 32 groups: 97 us, 2.8 TB/s, gradients 266 us, 1.5
+// TB/s), plain (4096 x 16384 fp32: 450 us, 1.2 TB/s, gradients 542 us, 1.5 TB/s),
+// and maps of few positions, whose workgroups hold one instance however small
+// (131072 x 2 x 512 bf16 in 64 groups: 2.8 ms, 0.2 TB/s, gradients 5.2 ms).
+// Statistics in fp32: the mean, a sum of the values (off by its roundings: some
+// 2^-24 of the average magnitude), then the squares about it (slabs: their own
+// means, joined by n_i (mean_i - mean)^2).
 #include "../../include/selscan.h"
 #include "common.hpp"
 #include "launch.hpp"

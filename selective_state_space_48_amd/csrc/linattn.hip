@@ -11,10 +11,13 @@
 //
 // What bounds it (MI355X, b8 L2048, 32 heads of 128 x 128, bf16): the bytes, 554
 // MB read and written once, take 117 us at the rate of a large copy (4.75
-// TB/s); a call takes 136-151 us (3.7-4.1 TB/s; by the clock). Of its
-// cycles the LDS is busy in 50 %, the vector units in 45 %, the matrix cores in
-// 33 %: a chunk's dependent steps (stage, scores, outputs, state) come after one
-// another in a workgroup that fills its CU. Its steps (us a call): 241 with
+// TB/s); a call takes 135-157 us (3.5-4.1 TB/s; by the clock). Of its
+// cycles the LDS is busy in 54 %, the vector units in 47 %, the matrix cores in
+// 36 %: a chunk's dependent steps (stage, scores, outputs, state) come after one
+// another in a workgroup that fills its CU. fp32 (b4, 1001 tokens at most, 12 heads of
+// 64 x 128: 54-57 us against 14): of the outputs' walk, 34 us, the matrix cores of
+// the 192 CUs that have a workgroup are busy in 35 %, the waves wait on LDS in 2 %.
+// Its steps (us a call): 241 with
 // every wave in every part and three barriers; 164 staged a chunk ahead (two
 // barriers); 160 with supply waves, outputs in whole rows through LDS; 151 with
 // them at a raised priority. One workgroup alone on the chip takes 3.3 us a
@@ -602,8 +605,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
             for (int q = 0; q < QB; ++q) cf[q] = col_frag<T, PT>(Cs, KB * q, wv * 16, 4, lane);
             // A masked score is a 0 in the outputs' products. Times a NaN or an infinity
             // of a later token it would not be: in a chunk with one, those values are
-            // left out there and added token by token. (The marks and branches cost 1 to 3 %;
-            // at state width 256 some registers, prompts 82 -> 95 us at 256 x 128.)
+            // left out there and added token by token. (The marks and branches cost up to 2 %.)
             const bool odd = !STATE && __builtin_amdgcn_readfirstlane(odds[c & 1]) == c + 1;
             if (odd)
 #pragma unroll
@@ -638,7 +640,7 @@ __global__ __launch_bounds__(PT * 4 + kSupply * 64, (PT / 16 + kSupply) / 4) voi
                         }
                 }
                 if (SLOPE) {
-                    // (loads taken ahead over this line spill: gradients of b4 L2048, 32 heads 324 us with, 287 without)
+                    // (loads taken ahead over this line spill: gradients of b4 L2048, 32 heads 309 us with, 278 without)
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int t = 0; t < TT; ++t) o2[t] = (o2[t] + o[t]) * float(16 * t + m - skip + 1);
