@@ -680,6 +680,292 @@ int selscan_groupnorm_workspace_size(const selscan_groupnorm_dims_t* dims, int32
                                      uint64_t* bytes);
 
 /*
+ * selscan_gated_fwd — a gated linear recurrence: a scan with one state per
+ * channel whose decay is a gate of the token, over whole sequences,
+ * token-major.
+ *
+ * Defined by: the linear recurrence of "State Space Models and Mamba"
+ * (multigrid.ai), section "It is a linear recurrence", with a state of one
+ * number per channel and, as its section "Selective state: the change that
+ * made it work on text" asks, a decay and an input term that are functions of
+ * the token (SELSCAN_GATED_MIX is the recurrence of Theorem 1 of "Mamba:
+ * Linear-Time Sequence Modeling with Selective State Spaces" (azimuth.plus):
+ * N = 1, A = -1); the SiLU gate branch of section "What a Mamba block actually
+ * contains". Per batch entry b and channel d, from h = h0[b,d] (or 0), for
+ * t < len = lengths[b] (or L):
+ *   SELSCAN_GATED_MIX    u = sigmoid(g[b,t,d]);  h = (1 - u) h + u x[b,t,d]
+ *   SELSCAN_GATED_DECAY  a = exp(A[d] sigmoid(r[b,t,d]));
+ *                        h = a h + sqrt(1 - a^2) sigmoid(g[b,t,d]) x[b,t,d]
+ *   y[b,t,d] = h, or h silu(z[b,t,d]) with z;  0 for len <= t < L
+ *   last_state[b,d] = h after token len-1
+ *
+ * Arguments (device pointers):
+ *   x, g, r, z, y : [B, L, D] of dtype (D contiguous), as a projection writes
+ *                   them; r with SELSCAN_GATED_DECAY only (else NULL); z NULL
+ *                   means no gate
+ *   A             : [D] fp32 with SELSCAN_GATED_DECAY (else NULL), at most 0:
+ *                   the logarithm of the channel's smallest decay per token.
+ *                   Above 0, where 1 - a^2 < 0, the state is a NaN
+ *   last_state    : [B, D] fp32 output or NULL
+ * dims: L < 2^27; D <= 2^24; B * ceil(D / 8) * segments <= 4194304 (else
+ * SELSCAN_ERR_DIMS). Fully fp32 arithmetic on values that are rounded once;
+ * 1 - a and sqrt(1 - a^2) are formed without cancellation, and the state that
+ * passes from tile to tile of tokens is held in 64 bits. Tokens behind an
+ * entry's length are not read. A NaN or an infinity reaches no token or
+ * channel that the recurrence does not take it to; an infinity may come out as
+ * a NaN. Outputs must not overlap inputs or each other. Deterministic: the
+ * same inputs and launch choices give the same bits.
+ */
+#define SELSCAN_GATED_MIX 0
+#define SELSCAN_GATED_DECAY 1
+typedef struct {
+    int64_t batch;
+    int64_t seqlen;
+    int64_t dim;
+    int32_t dtype;
+    int32_t kind; /* SELSCAN_GATED_* */
+} selscan_gated_dims_t;
+
+/* Tokens between the checkpoints of selscan_gated_fwd. */
+#define SELSCAN_GATED_CKPT 64
+
+/*
+ * Options of selscan_gated_fwd (NULL: all defaults). Zero-initialise, then set
+ * what is wanted.
+ *   h0        : [B, D] fp32, the state entering token 0 (NULL: zeros). It may
+ *               be last_state itself; it must not overlap y or ckpt.
+ *   lengths   : [B] int32, tokens of each entry (NULL: all have L); a value
+ *               below 0 counts as 0, above L as L. Must not overlap an output.
+ *   ckpt      : NULL, or a [ceil(L/64), B, D] fp32 output: the states entering
+ *               tokens 0, 64, 128, ..., for selscan_gated_bwd over the same
+ *               inputs (behind an entry's length: its last state).
+ *   segments  : runs of tokens scanned in parallel (1 = one walk per channel;
+ *               > 1 = the runs' own decays and states, their carries, then the
+ *               outputs); 0 = automatic. At most 65536; the run length is
+ *               rounded up to whole tiles. Results agree to rounding.
+ *   workspace : caller-owned device memory of workspace_bytes bytes, 256-byte
+ *               aligned, at least selscan_gated_fwd_workspace_size(); NULL
+ *               means the library takes and returns its own on the stream. It
+ *               must not overlap any input or output.
+ */
+typedef struct {
+    const float* h0;
+    const int32_t* lengths;
+    float* ckpt;
+    int32_t segments;
+    void* workspace;
+    uint64_t workspace_bytes;
+} selscan_gated_opts_t;
+
+int selscan_gated_fwd(const void* x, const void* g, const void* r, const float* A, const void* z,
+                      void* y, float* last_state, const selscan_gated_dims_t* dims,
+                      const selscan_gated_opts_t* opts, void* stream);
+
+/* Bytes of workspace selscan_gated_fwd needs (only opts->segments matters; opts
+ * may be NULL). Host only. */
+int selscan_gated_fwd_workspace_size(const selscan_gated_dims_t* dims,
+                                     const selscan_gated_opts_t* opts, uint64_t* bytes);
+
+/*
+ * selscan_gated_step — one token of the recurrence, the state updated in place:
+ * state [B, D] fp32; x, g, r, z, y [B, D] of dtype; A [D] fp32, as
+ * selscan_gated_fwd's. dims->seqlen is ignored. y and state must not overlap
+ * any input or each other.
+ */
+int selscan_gated_step(float* state, const void* x, const void* g, const void* r, const float* A,
+                       const void* z, void* y, const selscan_gated_dims_t* dims, void* stream);
+
+/*
+ * selscan_gated_bwd — gradients of selscan_gated_fwd for an output gradient dy
+ * (and, with dlast_state, for the last state).
+ *
+ * Defined by: the chain rule through the recurrence. With d_t = dy_t (dy_t
+ * silu(z_t) with z), from C = dlast_state (or 0) behind an entry's last token:
+ *   G_t = d_t + C;  C = a_t G_t   (a = 1 - u for SELSCAN_GATED_MIX);  dh0 = C at the end
+ *   SELSCAN_GATED_MIX    dx = G u;  dg = G (x - h_{t-1}) u (1 - u)
+ *   SELSCAN_GATED_DECAY  with v = sigmoid(g), s = sigmoid(r), w = sqrt(1 - a^2):
+ *     dx = G w v;  dg = G w x v (1 - v);  dl = G a (h_{t-1} - (a / w) v x);
+ *     dr = dl A s (1 - s);  dA[d] = sum over b, t of dl s
+ *   dz = dy_t h_t silu'(z_t)
+ * Where a rounds to 1 (w = 0) the derivative of w is taken as 0. The states are
+ * recomputed from the checkpoints, or from the inputs ("Mamba: Linear-Time
+ * Sequence Modeling with Selective State Spaces" (azimuth.plus), hardware-aware
+ * algorithm).
+ *
+ * Arguments: inputs as selscan_gated_fwd; dy [B, L, D] of dtype; outputs dx,
+ * dg, dr, dz [B, L, D] of dtype (dr with SELSCAN_GATED_DECAY, dz with z, else
+ * NULL; zero behind an entry's length), dA [D] fp32 or NULL (not wanted).
+ * Options: h0, lengths as the forward's; dlast_state [B, D] fp32 (NULL:
+ * zeros); dh0 [B, D] fp32 output or NULL; ckpt, the forward's checkpoints over
+ * the same inputs (h0 is then not read), or NULL; segments and workspace as the
+ * forward's (selscan_gated_bwd_workspace_size()). Outputs must not overlap
+ * inputs or each other. Deterministic.
+ */
+typedef struct {
+    const float* h0;
+    const int32_t* lengths;
+    const float* dlast_state;
+    float* dh0;
+    const float* ckpt;
+    int32_t segments;
+    void* workspace;
+    uint64_t workspace_bytes;
+} selscan_gated_bwd_opts_t;
+
+int selscan_gated_bwd(const void* x, const void* g, const void* r, const float* A, const void* z,
+                      const void* dy, void* dx, void* dg, void* dr, float* dA, void* dz,
+                      const selscan_gated_dims_t* dims, const selscan_gated_bwd_opts_t* opts,
+                      void* stream);
+
+/* Bytes of workspace selscan_gated_bwd needs (only opts->segments and whether
+ * opts->ckpt is set matter; opts may be NULL). Host only. */
+int selscan_gated_bwd_workspace_size(const selscan_gated_dims_t* dims,
+                                     const selscan_gated_bwd_opts_t* opts, uint64_t* bytes);
+
+/*
+ * selscan_addnorm — what stands around a block in a residual network: the norm
+ * behind the block, its gate and scale, the sum into the residual stream, and
+ * the norm before the next block, in one pass over the rows.
+ *
+ * Defined by the formulas. For every row i, with j = i / (R / gate_rows):
+ *   u = post(x[i,:]);  s = res_scale res[i,:] + scale gate[j,:] u
+ *   res_out[i,:] = s;  y[i,:] = pre(s)
+ * where post and pre are
+ *   SELSCAN_NORM_NONE   the value itself (pre: y is not written)
+ *   SELSCAN_NORM_RMS    v / sqrt(average of v^2 + eps) * weight + bias
+ *   SELSCAN_NORM_LAYER  (v - mean) / sqrt(average of (v - mean)^2 + eps) * weight + bias
+ * y is formed from s before it is rounded.
+ *
+ * Arguments (device pointers):
+ *   x, y         : [R, C] of dtype (C contiguous); y NULL with pre SELSCAN_NORM_NONE
+ *   res, res_out : [R, C] of res_dtype; res NULL means zeros, res_out NULL not
+ *                  wanted; res_out may be res itself
+ *   stats        : [R, 4] fp32 output or NULL: post's mean and 1 / sqrt, pre's
+ *                  mean and 1 / sqrt (0 and 1 where there is no such norm; a
+ *                  SELSCAN_NORM_RMS has mean 0), for selscan_addnorm_bwd
+ * Options: post_weight, post_bias, pre_weight, pre_bias [C] fp32 or NULL (1 and
+ * 0), only with their norm; gate [gate_rows, C] fp32 or NULL (1).
+ * dims: R < 2^31; C <= 16384; R a multiple of gate_rows (with a gate);
+ * res_dtype the dtype or SELSCAN_F32; eps >= 0, scale and res_scale finite.
+ * Statistics in fp32, the variance from differences to the mean. Other outputs
+ * must not overlap inputs or each other. A row's result does not depend on the
+ * other rows. Deterministic.
+ */
+#define SELSCAN_NORM_NONE 0
+#define SELSCAN_NORM_RMS 1
+#define SELSCAN_NORM_LAYER 2
+typedef struct {
+    int64_t rows;      /* R */
+    int64_t channels;  /* C */
+    int64_t gate_rows; /* ignored without a gate */
+    int32_t dtype;
+    int32_t res_dtype;
+    int32_t post;
+    int32_t pre;
+    float eps; /* ignored by selscan_addnorm_bwd */
+    float scale;
+    float res_scale;
+} selscan_addnorm_dims_t;
+
+typedef struct {
+    const float* post_weight;
+    const float* post_bias;
+    const float* pre_weight;
+    const float* pre_bias;
+    const float* gate;
+    void* workspace; /* selscan_addnorm_bwd: as selscan_fwd_opts_t's */
+    uint64_t workspace_bytes;
+} selscan_addnorm_opts_t;
+
+int selscan_addnorm(const void* x, const void* res, void* res_out, void* y, float* stats,
+                    const selscan_addnorm_dims_t* dims, const selscan_addnorm_opts_t* opts,
+                    void* stream);
+
+/*
+ * selscan_addnorm_bwd — gradients of selscan_addnorm for the output gradients
+ * dy and dres_out, from the sum (res_out) and the stats that the forward gave:
+ * the chain rule through its definition. With xh2 = (s - mean2) rstd2, xh1 =
+ * (x - mean1) rstd1 (x itself without a post norm) and averages over the row:
+ *   e = dy pre_weight;  ds = dres_out + rstd2 (e - average(e) - xh2 average(e xh2))
+ *   dres = res_scale ds;  du = scale gate ds
+ *   f = du post_weight;  dx = rstd1 (f - average(f) - xh1 average(f xh1)), or du
+ *   dpre_weight = sum dy xh2;  dpre_bias = sum dy;  dpost_weight = sum du xh1;
+ *   dpost_bias = sum du;  dgate = sum scale u ds      (over the rows they serve)
+ * without the average(e) and average(f) for SELSCAN_NORM_RMS.
+ *
+ * Arguments: x [R, C] as the forward's (NULL if there is no post norm and no
+ * dgate is wanted); sum [R, C] of res_dtype and dy [R, C] of dtype (NULL
+ * without a pre norm); stats [R, 4]; dres_out [R, C] of res_dtype or NULL
+ * (zeros); outputs dx [R, C] of dtype, dres [R, C] of res_dtype, either NULL if
+ * not wanted; grads' fields fp32, each NULL if not wanted: the four of [C], and
+ * dgate [gate_rows, C] (only with a gate). grads itself may be NULL. dres may be
+ * dres_out itself; other outputs must not overlap inputs or each other. Sums
+ * over rows in a fixed order: deterministic.
+ */
+typedef struct {
+    float* dpost_weight;
+    float* dpost_bias;
+    float* dpre_weight;
+    float* dpre_bias;
+    float* dgate;
+} selscan_addnorm_grads_t;
+
+int selscan_addnorm_bwd(const void* x, const void* sum, const float* stats, const void* dy,
+                        const void* dres_out, void* dx, void* dres,
+                        const selscan_addnorm_grads_t* grads, const selscan_addnorm_dims_t* dims,
+                        const selscan_addnorm_opts_t* opts, void* stream);
+
+/* Bytes of workspace selscan_addnorm_bwd needs for these dims, opts (whether
+ * there is a gate) and grads (which are wanted). Host only. */
+int selscan_addnorm_bwd_workspace_size(const selscan_addnorm_dims_t* dims,
+                                       const selscan_addnorm_opts_t* opts,
+                                       const selscan_addnorm_grads_t* grads, uint64_t* bytes);
+
+/*
+ * selscan_rotary — rotary positions for the queries and keys of an attention
+ * layer (selscan_linattn_fwd and its token step and gradients): pairs of a
+ * head's values are turned by an angle proportional to the token's position,
+ * so that products of queries and keys depend on the distance of their tokens.
+ *
+ * Defined by the formulas. For every token (b, t) with the position p =
+ * offset + positions[b,t] (or offset + t without positions), every head and
+ * i < rot / 2, theta = p inv_freq[i], the pair (a, b) at (i, i + rot / 2) with
+ * SELSCAN_ROTARY_HALF, (2 i, 2 i + 1) with SELSCAN_ROTARY_INTERLEAVED:
+ *   (a, b) -> scale (a cos theta - b sin theta, a sin theta + b cos theta)
+ * and with -theta if inverse is set, which is the gradient: dq of the call
+ * turned back. Values from rot on are passed on as they are.
+ *
+ * Arguments (device pointers):
+ *   q, q_out  : [B, L, H, W] of dtype; k, k_out: [B, L, Hkv, W] (NULL with Hkv 0)
+ *   inv_freq  : [rot / 2] fp32, the angle per position, scaled for a longer
+ *               context where that is wanted
+ *   positions : [B, L] int32 or NULL
+ * dims: 0 < rot <= W <= 4096, rot even (else SELSCAN_ERR_DSTATE); L < 2^27; B L
+ * (H + Hkv) < 2^38; -2^31 < offset < 2^31; scale finite, 0 means 1. The angle
+ * is formed in 64 bits and its whole turns taken off, so that far positions
+ * keep fp32 accuracy. q_out may be q itself and k_out k; otherwise outputs must
+ * not overlap inputs or each other. No workspace. Deterministic.
+ */
+#define SELSCAN_ROTARY_HALF 0
+#define SELSCAN_ROTARY_INTERLEAVED 1
+typedef struct {
+    int64_t batch;
+    int64_t seqlen;
+    int64_t heads;
+    int64_t kv_heads;
+    int64_t width; /* W */
+    int64_t rot;
+    int64_t offset;
+    int32_t dtype;
+    int32_t layout; /* SELSCAN_ROTARY_* */
+    int32_t inverse;
+    float scale;
+} selscan_rotary_dims_t;
+
+int selscan_rotary(const void* q, const void* k, const float* inv_freq, const int32_t* positions,
+                   void* q_out, void* k_out, const selscan_rotary_dims_t* dims, void* stream);
+
+/*
  * selscan_conv1d — the short causal convolution in front of the scan: a
  * depthwise conv1d of width SELSCAN_CONV_WIDTH (4), then SiLU.
  *

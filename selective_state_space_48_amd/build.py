@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libselscan.so")
 SOURCES = ["api.hip", "fwd.hip", "step.hip", "conv.hip", "bwd.hip", "ssd.hip", "linattn.hip",
-           "groupnorm.hip"]
+           "groupnorm.hip", "api_block.hip", "gated.hip", "addnorm.hip", "rotary.hip"]
 # Counter-calibration copies (measurement only), a library of their own.
 CALIB_LIB = os.path.join(PKG, "libselscan_calib.so")
 CALIB_SOURCES = ["calib.hip"]

@@ -268,6 +268,94 @@ hipError_t launch_groupnorm(const GroupnormTensors& t, const GroupnormShape& s, 
 hipError_t launch_groupnorm_bwd(const GroupnormTensors& t, const GroupnormShape& s, void* workspace,
                                 hipStream_t stream);
 
+// Gated linear recurrence. x, g, r, z, y and their gradients: [batch, L, dim];
+// A, dA: [dim]; states: [batch, dim]; ckpt: [ceil(L/64), batch, dim].
+struct GatedShape {
+    int64_t batch, L, dim;
+    DType dtype;
+    int32_t kind;  // SELSCAN_GATED_*
+};
+struct GatedPlan {
+    int32_t segments;  // runs of seg_len tokens (a multiple of the tile when segments > 1)
+    int64_t seg_len;
+};
+struct GatedTensors {
+    const void* x;
+    const void* g;
+    const void* r;   // decay only
+    const float* A;  // decay only
+    const void* z;   // null: no gate
+    const int32_t* lengths;
+    const float* h0;  // null: zeros
+    // forward
+    void* y;
+    float* last_state;
+    float* ckpt;  // output of the forward (null: none), input of the backward (null: recomputed)
+    // backward
+    const void* dy;
+    const float* dlast;  // null: zeros
+    void* dx;
+    void* dg;
+    void* dr;
+    float* dA;  // null: not wanted
+    void* dz;
+    float* dh0;  // null: not wanted
+};
+// The runs of a call (requested 0: automatic); false where the grid would not fit.
+bool gated_plan(const GatedShape& s, int32_t requested, bool backward, GatedPlan* p);
+size_t gated_fwd_workspace_bytes(const GatedShape& s, const GatedPlan& p);
+size_t gated_bwd_workspace_bytes(const GatedShape& s, const GatedPlan& p, bool ckpt_given);
+hipError_t launch_gated_fwd(const GatedTensors& t, const GatedShape& s, const GatedPlan& p, void* workspace,
+                            hipStream_t stream);
+hipError_t launch_gated_bwd(const GatedTensors& t, const GatedShape& s, const GatedPlan& p, void* workspace,
+                            hipStream_t stream);
+hipError_t launch_gated_step(float* state, const GatedTensors& t, const GatedShape& s, hipStream_t stream);
+
+// Norms around a block with the residual sum: x, y [R, C] of dtype; res, sum [R, C] of res_dtype.
+struct AddnormShape {
+    int64_t R, C, G;  // G: rows of the gate (0 without one)
+    DType dtype, res_dtype;
+    int32_t post, pre;  // SELSCAN_NORM_*
+    float eps, scale, res_scale;
+};
+struct AddnormTensors {
+    const void* x;
+    const void* res;  // null: zeros
+    void* sum;        // output of the forward (null: not wanted), input of the backward
+    void* y;
+    float* stats;  // [R, 4], output of the forward (null: not wanted), input of the backward
+    const float* post_w;
+    const float* post_b;
+    const float* pre_w;
+    const float* pre_b;
+    const float* gate;
+    // backward
+    const void* dy;
+    const void* dsum;  // null: zeros
+    void* dx;
+    void* dres;
+    // sums over rows, null: not wanted
+    float* dpost_w;
+    float* dpost_b;
+    float* dpre_w;
+    float* dpre_b;
+    float* dgate;
+};
+size_t addnorm_bwd_workspace_bytes(const AddnormShape& s, const AddnormTensors& wanted);
+hipError_t launch_addnorm(const AddnormTensors& t, const AddnormShape& s, hipStream_t stream);
+hipError_t launch_addnorm_bwd(const AddnormTensors& t, const AddnormShape& s, void* workspace, hipStream_t stream);
+
+// Rotary positions: q [batch, L, heads, W], k [batch, L, kv_heads, W].
+struct RotaryShape {
+    int64_t batch, L, heads, kv_heads, W, rot, offset;
+    DType dtype;
+    int32_t layout;  // SELSCAN_ROTARY_*
+    bool inverse;
+    float scale;
+};
+hipError_t launch_rotary(const void* q, const void* k, const float* inv_freq, const int32_t* positions, void* q_out,
+                         void* k_out, const RotaryShape& s, hipStream_t stream);
+
 // Causal depthwise conv (width 4) + SiLU. x/out: [rows, L]; w: [dim, 4];
 // bias: [dim] or null; x_prev/x_last: [rows, 3] fp32 or null.
 struct ConvTensors {

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -88,6 +89,47 @@ class GroupnormOpts(ctypes.Structure):
     _fields_ = [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
 
 
+class GatedDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32)]
+
+
+class GatedOpts(ctypes.Structure):
+    _fields_ = [("h0", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("ckpt", ctypes.c_void_p),
+                ("segments", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class GatedBwdOpts(ctypes.Structure):
+    _fields_ = [("h0", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("dlast_state", ctypes.c_void_p),
+                ("dh0", ctypes.c_void_p), ("ckpt", ctypes.c_void_p), ("segments", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class AddnormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("pre", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("res_scale", ctypes.c_float)]
+
+
+class AddnormOpts(ctypes.Structure):
+    _fields_ = [("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("pre_bias", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class AddnormGrads(ctypes.Structure):
+    _fields_ = [("dpost_weight", ctypes.c_void_p), ("dpost_bias", ctypes.c_void_p), ("dpre_weight", ctypes.c_void_p),
+                ("dpre_bias", ctypes.c_void_p), ("dgate", ctypes.c_void_p)]
+
+
+class RotaryDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("width", ctypes.c_int64), ("rot", ctypes.c_int64),
+                ("offset", ctypes.c_int64), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class SelscanError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"libselscan error {code}: {msg}")
@@ -147,6 +189,20 @@ def _load() -> ctypes.CDLL:
               lib.selscan_linattn_bwd, lib.selscan_linattn_bwd_workspace_size, lib.selscan_groupnorm,
               lib.selscan_groupnorm_bwd, lib.selscan_groupnorm_workspace_size):
         f.restype = ctypes.c_int
+    ga_p, ga_o, ga_bo = (ctypes.POINTER(t) for t in (GatedDims, GatedOpts, GatedBwdOpts))
+    an_p, an_o, an_g = (ctypes.POINTER(t) for t in (AddnormDims, AddnormOpts, AddnormGrads))
+    lib.selscan_gated_fwd.argtypes = [vp, vp, vp, fp, vp, vp, fp, ga_p, ga_o, vp]
+    lib.selscan_gated_fwd_workspace_size.argtypes = [ga_p, ga_o, u64_p]
+    lib.selscan_gated_step.argtypes = [fp, vp, vp, vp, fp, vp, vp, ga_p, vp]
+    lib.selscan_gated_bwd.argtypes = [vp, vp, vp, fp, vp, vp, vp, vp, vp, fp, vp, ga_p, ga_bo, vp]
+    lib.selscan_gated_bwd_workspace_size.argtypes = [ga_p, ga_bo, u64_p]
+    lib.selscan_addnorm.argtypes = [vp, vp, vp, vp, fp, an_p, an_o, vp]
+    lib.selscan_addnorm_bwd.argtypes = [vp, vp, fp, vp, vp, vp, vp, an_g, an_p, an_o, vp]
+    lib.selscan_addnorm_bwd_workspace_size.argtypes = [an_p, an_o, an_g, u64_p]
+    lib.selscan_rotary.argtypes = [vp, vp, fp, vp, vp, vp, ctypes.POINTER(RotaryDims), vp]
+    for name in ("gated_fwd", "gated_fwd_workspace_size", "gated_step", "gated_bwd", "gated_bwd_workspace_size",
+                 "addnorm", "addnorm_bwd", "addnorm_bwd_workspace_size", "rotary"):
+        getattr(lib, "selscan_" + name).restype = ctypes.c_int
     lib.selscan_conv1d.argtypes = [vp, fp, fp, fp, vp, fp, dims_p, vp]
     lib.selscan_conv1d.restype = ctypes.c_int
     lib.selscan_conv1d_step.argtypes = [fp, vp, fp, fp, vp, dims_p, vp]
@@ -789,6 +845,371 @@ def groupnorm_bwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] =
                                          _ptr(out.get("dbias")), _ptr(out.get("dz")), ctypes.byref(dims),
                                          ctypes.byref(opts), _stream(dev)))
     return out
+
+
+GATED_MIX, GATED_DECAY = 0, 1
+# Tokens between the checkpoints of gated_fwd
+GATED_CKPT = 64
+
+
+def gated_ckpt_shape(batch: int, L: int, dim: int) -> Tuple[int, int, int]:
+    """Shape of the checkpoints ``gated_fwd`` writes and ``gated_bwd`` reads."""
+    return ((L + GATED_CKPT - 1) // GATED_CKPT, batch, dim)
+
+
+def _gated_args(x, g, r, A, z, shape, **others) -> "GatedDims":
+    """The inputs of the three gated calls, checked; ``others`` are further tensors of x's type and shape."""
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if (r is None) != (A is None):
+        raise ValueError("r and A belong together")
+    dev = x.device
+    _req(x, "x", x.dtype, shape, dev)
+    for name, t in dict(g=g, r=r, z=z, **others).items():
+        _req(t, name, x.dtype, shape, dev)
+    _req(A, "A", torch.float32, (shape[-1],), dev)
+    L = shape[1] if len(shape) == 3 else 1
+    return GatedDims(shape[0], L, shape[-1], _DTYPES[x.dtype], GATED_MIX if r is None else GATED_DECAY)
+
+
+def gated_workspace_size(batch: int, L: int, dim: int, dtype: torch.dtype, *, decay: bool = True,
+                         segments: int = 0) -> int:
+    """Bytes of workspace ``gated_fwd`` needs for this shape and number of segments."""
+    dims = GatedDims(batch, L, dim, _DTYPES[dtype], int(decay))
+    n = ctypes.c_uint64(0)
+    _check(lib.selscan_gated_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(GatedOpts(segments=int(segments))),
+                                                ctypes.byref(n)))
+    return int(n.value)
+
+
+def gated_bwd_workspace_size(batch: int, L: int, dim: int, dtype: torch.dtype, *, decay: bool = True,
+                             ckpt_given: bool = False, segments: int = 0) -> int:
+    """Bytes of workspace ``gated_bwd`` needs for this shape and these choices."""
+    dims = GatedDims(batch, L, dim, _DTYPES[dtype], int(decay))
+    opts = GatedBwdOpts(ckpt=16 if ckpt_given else None, segments=int(segments))
+    n = ctypes.c_uint64(0)
+    _check(lib.selscan_gated_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(n)))
+    return int(n.value)
+
+
+def gated_fwd(x: torch.Tensor, g: torch.Tensor, r: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
+              z: Optional[torch.Tensor] = None, *, h0: Optional[torch.Tensor] = None,
+              lengths: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+              last_state: Optional[torch.Tensor] = None, return_last_state: bool = True,
+              ckpt: Optional[torch.Tensor] = None, segments: int = 0, workspace: Optional[torch.Tensor] = None
+              ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gated linear recurrence (selscan_gated_fwd). Returns (y, last_state).
+
+    ``x``, ``g``, ``r``, ``z`` [batch, L, dim] (float32 or bfloat16). Without
+    ``r``: h = (1 - u) h + u x, u = sigmoid(g). With ``r`` and ``A`` [dim] fp32
+    (at most 0): a = exp(A sigmoid(r)), h = a h + sqrt(1 - a^2) sigmoid(g) x.
+    y = h, or h silu(z). ``h0`` [batch, dim] fp32 is the state entering token 0
+    (it may be ``last_state`` itself); ``lengths`` [batch] int32 the tokens of
+    each entry (y is 0 behind them). ``ckpt`` (``gated_ckpt_shape``) fp32
+    receives states for ``gated_bwd``. ``segments`` and ``workspace`` as for
+    ``fwd`` (``gated_workspace_size``).
+    """
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, L, dim]")
+    batch, L, dim = x.shape
+    dev, dt = x.device, x.dtype
+    dims = _gated_args(x, g, r, A, z, x.shape)
+    _req(h0, "h0", torch.float32, (batch, dim), dev)
+    _req(lengths, "lengths", torch.int32, (batch,), dev)
+    _req(ckpt, "ckpt", torch.float32, gated_ckpt_shape(batch, L, dim), dev)
+    with _device(dev):
+        if y is None:
+            y = torch.empty((batch, L, dim), dtype=dt, device=dev)
+        _req(y, "y", dt, (batch, L, dim), dev)
+        if last_state is None and return_last_state:
+            last_state = torch.empty((batch, dim), dtype=torch.float32, device=dev)
+        _req(last_state, "last_state", torch.float32, (batch, dim), dev)
+        opts = GatedOpts(_ptr(h0), _ptr(lengths), _ptr(ckpt), int(segments), None, 0)
+        need = ctypes.c_uint64(0)
+        _check(lib.selscan_gated_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(need)))
+        workspace = _scratch(workspace, int(need.value), dev)
+        if workspace is not None:
+            opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _check(lib.selscan_gated_fwd(_ptr(x), _ptr(g), _ptr(r), _ptr(A), _ptr(z), _ptr(y), _ptr(last_state),
+                                     ctypes.byref(dims), ctypes.byref(opts), _stream(dev)))
+    return y, last_state
+
+
+def gated_step(state: torch.Tensor, x: torch.Tensor, g: torch.Tensor, r: Optional[torch.Tensor] = None,
+               A: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None, *,
+               y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the recurrence (selscan_gated_step): updates ``state``
+    [batch, dim] fp32 in place and returns y [batch, dim]; ``x``, ``g``, ``r``,
+    ``z`` [batch, dim] and ``A`` [dim] as for ``gated_fwd``."""
+    if state.dim() != 2:
+        raise ValueError("state must be [batch, dim]")
+    dev, dt = x.device, x.dtype
+    dims = _gated_args(x, g, r, A, z, state.shape)
+    _req(state, "state", torch.float32, state.shape, dev)
+    with _device(dev):
+        if y is None:
+            y = torch.empty(state.shape, dtype=dt, device=dev)
+        _req(y, "y", dt, state.shape, dev)
+        _check(lib.selscan_gated_step(_ptr(state), _ptr(x), _ptr(g), _ptr(r), _ptr(A), _ptr(z), _ptr(y),
+                                      ctypes.byref(dims), _stream(dev)))
+    return y
+
+
+def gated_bwd(x: torch.Tensor, g: torch.Tensor, r: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
+              z: Optional[torch.Tensor] = None, *, dy: torch.Tensor, h0: Optional[torch.Tensor] = None,
+              lengths: Optional[torch.Tensor] = None, dlast_state: Optional[torch.Tensor] = None,
+              ckpt: Optional[torch.Tensor] = None, want_dA: bool = True, want_dh0: bool = False, segments: int = 0,
+              workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``gated_fwd`` (selscan_gated_bwd) for ``dy`` [batch, L, dim]
+    and, when given, ``dlast_state`` (the gradient into last_state).
+
+    Returns a dict with dx, dg and, where there are such inputs, dr, dz (like
+    x; 0 behind an entry's length) and dA [dim] fp32, and dh0 [batch, dim] fp32
+    when wanted. ``ckpt``: the forward's checkpoints over the same inputs (then
+    h0 is not read); without them the states are recomputed. ``workspace``: at
+    least ``gated_bwd_workspace_size(...)`` bytes.
+    """
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, L, dim]")
+    batch, L, dim = x.shape
+    dev = x.device
+    dims = _gated_args(x, g, r, A, z, x.shape, dy=dy)
+    _req(h0, "h0", torch.float32, (batch, dim), dev)
+    _req(dlast_state, "dlast_state", torch.float32, (batch, dim), dev)
+    _req(lengths, "lengths", torch.int32, (batch,), dev)
+    _req(ckpt, "ckpt", torch.float32, gated_ckpt_shape(batch, L, dim), dev)
+    with _device(dev):
+        out = {"dx": torch.empty_like(x), "dg": torch.empty_like(x)}
+        if r is not None:
+            out["dr"] = torch.empty_like(x)
+            if want_dA:
+                out["dA"] = torch.empty_like(A)
+        if z is not None:
+            out["dz"] = torch.empty_like(x)
+        if want_dh0:
+            out["dh0"] = torch.empty((batch, dim), dtype=torch.float32, device=dev)
+        opts = GatedBwdOpts(_ptr(h0), _ptr(lengths), _ptr(dlast_state), _ptr(out.get("dh0")), _ptr(ckpt),
+                            int(segments), None, 0)
+        need = ctypes.c_uint64(0)
+        _check(lib.selscan_gated_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(need)))
+        workspace = _scratch(workspace, int(need.value), dev)
+        if workspace is not None:
+            opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _check(lib.selscan_gated_bwd(_ptr(x), _ptr(g), _ptr(r), _ptr(A), _ptr(z), _ptr(dy), _ptr(out["dx"]),
+                                     _ptr(out["dg"]), _ptr(out.get("dr")), _ptr(out.get("dA")), _ptr(out.get("dz")),
+                                     ctypes.byref(dims), ctypes.byref(opts), _stream(dev)))
+    return out
+
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _addnorm_dims(rows, C, dt, res_dt, pre, post, gate, eps, scale, res_scale) -> "AddnormDims":
+    if dt not in _DTYPES or res_dt not in _DTYPES:
+        raise TypeError(f"unsupported dtypes {dt}, {res_dt}")
+    if pre not in NORMS or post not in NORMS:
+        raise ValueError(f"pre and post must be one of {sorted(NORMS)}")
+    return AddnormDims(rows, C, 0 if gate is None else gate.shape[0], _DTYPES[dt], _DTYPES[res_dt], NORMS[post],
+                       NORMS[pre], float(eps), float(scale), float(res_scale))
+
+
+def _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate) -> "AddnormOpts":
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
+                    ("pre_bias", pre_bias)):
+        _req(t, name, torch.float32, (C,), dev)
+    if gate is not None:
+        if gate.dim() != 2:
+            raise ValueError("gate must be [gate_rows, channels]")
+        _req(gate, "gate", torch.float32, (gate.shape[0], C), dev)
+    return AddnormOpts(_ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), _ptr(gate), None, 0)
+
+
+def addnorm(x: torch.Tensor, res: Optional[torch.Tensor] = None, *, pre: str = "rms",
+            pre_weight: Optional[torch.Tensor] = None, pre_bias: Optional[torch.Tensor] = None, post: str = "none",
+            post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None,
+            gate: Optional[torch.Tensor] = None, scale: float = 1.0, res_scale: float = 1.0, eps: float = 1e-5,
+            res_dtype: Optional[torch.dtype] = None, y: Optional[torch.Tensor] = None,
+            res_out: Optional[torch.Tensor] = None, return_res: bool = True, return_stats: bool = True
+            ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """The norms around a block with the residual sum (selscan_addnorm). Returns (y, res_out, stats).
+
+    res_out = res_scale res + scale gate post(x) and y = pre(res_out), rounded
+    once each; ``post`` and ``pre`` are "none", "rms" or "layer" over the last
+    axis, with weights and biases [channels] fp32. ``x`` [..., channels]
+    float32 or bfloat16; ``res`` (None: zeros) the same shape, of x's type or
+    float32 (``res_dtype`` where there is no res); ``gate`` [gate_rows,
+    channels] fp32, each row of it for rows / gate_rows rows of x in turn (None:
+    1). ``res_out`` may be ``res`` itself; with ``return_res=False`` it is not
+    written. ``stats`` [rows, 4] fp32 is what ``addnorm_bwd`` needs (None with
+    ``return_stats=False``). With pre "none" y is None.
+    """
+    if x.dim() < 1:
+        raise ValueError("x must be [..., channels]")
+    shape, C, dev, dt = x.shape, x.shape[-1], x.device, x.dtype
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    rt = res.dtype if res is not None else res_out.dtype if res_out is not None else res_dtype or dt
+    dims = _addnorm_dims(rows, C, dt, rt, pre, post, gate, eps, scale, res_scale)
+    _req(x, "x", dt, None, dev)
+    _req(res, "res", rt, shape, dev)
+    opts = _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate)
+    with _device(dev):
+        if y is None and pre != "none":
+            y = torch.empty(shape, dtype=dt, device=dev)
+        _req(y, "y", dt, shape, dev)
+        if res_out is None and return_res:
+            res_out = torch.empty(shape, dtype=rt, device=dev)
+        _req(res_out, "res_out", rt, shape, dev)
+        stats = torch.empty((rows, 4), dtype=torch.float32, device=dev) if return_stats else None
+        _check(lib.selscan_addnorm(_ptr(x), _ptr(res), _ptr(res_out), _ptr(y), _ptr(stats), ctypes.byref(dims),
+                                   ctypes.byref(opts), _stream(dev)))
+    return y, res_out, stats
+
+
+def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, dy: Optional[torch.Tensor],
+                dres_out: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor], pre: str = "rms",
+                pre_weight: Optional[torch.Tensor] = None, pre_bias: Optional[torch.Tensor] = None,
+                post: str = "none", post_weight: Optional[torch.Tensor] = None,
+                post_bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                res_scale: float = 1.0, want_dx: bool = True, want_dres: bool = True, want_dparams: bool = True,
+                dres: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``addnorm`` (selscan_addnorm_bwd) for ``dy`` (None with pre
+    "none") and ``dres_out`` (the gradient into res_out; None: zeros), from the
+    ``res_out`` and ``stats`` that it returned.
+
+    Returns a dict with dx, dres (``dres`` may be ``dres_out`` itself) and, with
+    ``want_dparams``, dpost_weight, dpost_bias, dpre_weight, dpre_bias [channels]
+    and dgate (like gate), all fp32, of the parameters that are given. ``x`` may
+    be None where there is neither a post norm nor a gate whose gradient is
+    wanted, ``res_out`` with pre "none".
+    """
+    like = next((t for t in (dy, x, res_out, dres_out) if t is not None), None)
+    if like is None or like.dim() < 1:
+        raise ValueError("dy, x, res_out or dres_out must be given, as [..., channels]")
+    shape, C, dev = like.shape, like.shape[-1], like.device
+    dt = dy.dtype if dy is not None else x.dtype if x is not None else like.dtype
+    rt = next((t.dtype for t in (res_out, dres_out, dres) if t is not None), dt)
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    dims = _addnorm_dims(rows, C, dt, rt, pre, post, gate, 0.0, scale, res_scale)
+    for t, name, tt in ((x, "x", dt), (dy, "dy", dt), (res_out, "res_out", rt), (dres_out, "dres_out", rt)):
+        _req(t, name, tt, shape, dev)
+    _req(stats, "stats", torch.float32, (rows, 4), dev)
+    opts = _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate)
+    params = dict(post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight, pre_bias=pre_bias, gate=gate)
+    with _device(dev):
+        out = {}
+        if want_dx:
+            out["dx"] = torch.empty(shape, dtype=dt, device=dev)
+        if want_dres:
+            out["dres"] = torch.empty(shape, dtype=rt, device=dev) if dres is None else dres
+            _req(out["dres"], "dres", rt, shape, dev)
+        if want_dparams:
+            out.update({"d" + n: torch.empty_like(p) for n, p in params.items() if p is not None})
+        grads = AddnormGrads(*(_ptr(out.get("d" + n)) for n in ("post_weight", "post_bias", "pre_weight", "pre_bias",
+                                                                "gate")))
+        need = ctypes.c_uint64(0)
+        _check(lib.selscan_addnorm_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(grads),
+                                                      ctypes.byref(need)))
+        workspace = _scratch(workspace, int(need.value), dev)
+        if workspace is not None:
+            opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _check(lib.selscan_addnorm_bwd(_ptr(x), _ptr(res_out), _ptr(stats), _ptr(dy), _ptr(dres_out),
+                                       _ptr(out.get("dx")), _ptr(out.get("dres")), ctypes.byref(grads),
+                                       ctypes.byref(dims), ctypes.byref(opts), _stream(dev)))
+    return out
+
+
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original: int = 0, fast: float = 32.0, slow: float = 1.0,
+                       device: Optional[torch.device] = None) -> torch.Tensor:
+    """The ``inv_freq`` [rot / 2] fp32 of ``rotary``: base^(-2 i / rot), for a
+    context ``factor`` times as long as the one of training where wanted.
+
+    ``scaling``: "none"; "linear", every frequency divided by ``factor``;
+    "base", the base multiplied by factor^(rot / (rot - 2)), which leaves the
+    fastest frequency and divides the slowest by ``factor``; "parts", those
+    that turn more than ``fast`` times over ``original`` tokens left, those
+    that turn less than ``slow`` times divided by ``factor``, and linear in the
+    index between these two (the magnitude is ``rotary``'s ``scale``).
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and positive")
+    if not (base > 1 and factor > 0):
+        raise ValueError("base must be above 1 and factor above 0")
+    i = torch.arange(0, rot, 2, dtype=torch.float64) / rot
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError('scaling "base" needs two frequencies')
+        base = base * factor ** (rot / (rot - 2))
+    freq = float(base) ** -i
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "parts":
+        if original <= 0 or not fast > slow > 0:
+            raise ValueError('scaling "parts" needs original > 0 and fast > slow > 0')
+        # the index whose frequency turns n times over the original context
+        where = [rot * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow)]
+        lo, hi = max(math.floor(where[0]), 0), min(math.ceil(where[1]), rot - 1)
+        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - ramp) + freq / factor * ramp
+    elif scaling not in ("none", "base"):
+        raise ValueError('scaling must be "none", "linear", "base" or "parts"')
+    return freq.float().to(device) if device is not None else freq.float()
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor, *,
+           positions: Optional[torch.Tensor] = None, offset: int = 0, layout: str = "half",
+           scale: Optional[float] = None, inverse: bool = False, q_out: Optional[torch.Tensor] = None,
+           k_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotary positions (selscan_rotary). Returns (q_out, k_out).
+
+    ``q`` [batch, L, heads, width], ``k`` [batch, L, kv_heads, width] or None
+    (float32 or bfloat16): the first 2 len(inv_freq) values of each head are
+    turned by (offset + position) inv_freq, in pairs (i, i + half) or (2 i, 2 i
+    + 1) for ``layout`` "half" or "interleaved", and multiplied by ``scale``
+    (None: 1). ``positions`` [batch, L] int32 (None: 0, 1, ... along L);
+    ``inv_freq`` fp32 (``rotary_frequencies``). ``inverse`` turns back: the
+    gradients of q and k are their outputs' gradients turned back. ``q_out``
+    and ``k_out`` may be q and k themselves.
+    """
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be [batch, L, heads, width]")
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUTS)}")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    if scale is not None and ctypes.c_float(scale).value == 0:
+        raise ValueError("scale must not be 0 in fp32 (None: 1)")
+    batch, L, H, W = q.shape
+    dev, dt = q.device, q.dtype
+    Hk = 0 if k is None else k.shape[2]
+    _req(q, "q", dt, None, dev)
+    _req(k, "k", dt, (batch, L, Hk, W), dev)
+    _req(inv_freq, "inv_freq", torch.float32, None, dev)
+    _req(positions, "positions", torch.int32, (batch, L), dev)
+    dims = RotaryDims(batch, L, H, Hk, W, 2 * inv_freq.shape[0], int(offset), _DTYPES[dt], ROTARY_LAYOUTS[layout],
+                      int(inverse), 0.0 if scale is None else float(scale))
+    if k is None and k_out is not None:
+        raise ValueError("k_out belongs to k")
+    with _device(dev):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        _req(q_out, "q_out", dt, q.shape, dev)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty_like(k)
+            _req(k_out, "k_out", dt, k.shape, dev)
+        _check(lib.selscan_rotary(_ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(q_out), _ptr(k_out),
+                                  ctypes.byref(dims), _stream(dev)))
+    return q_out, k_out
 
 
 CONV_WIDTH = 4
