@@ -707,7 +707,7 @@ int selscan_groupnorm_workspace_size(const selscan_groupnorm_dims_t* dims, int32
  *                   the logarithm of the channel's smallest decay per token.
  *                   Above 0, where 1 - a^2 < 0, the state is a NaN
  *   last_state    : [B, D] fp32 output or NULL
- * dims: L < 2^27; D <= 2^24; B * ceil(D / 8) * segments <= 4194304 (else
+ * dims: L < 2^27; D <= 2^20; B * ceil(D / 8) * segments <= 4194304 (else
  * SELSCAN_ERR_DIMS). Fully fp32 arithmetic on values that are rounded once;
  * 1 - a and sqrt(1 - a^2) are formed without cancellation, and the state that
  * passes from tile to tile of tokens is held in 64 bits. Tokens behind an

@@ -31,7 +31,7 @@ int done(hipError_t e) { return e == hipSuccess ? SELSCAN_OK : SELSCAN_ERR_LAUNC
 int check_gated(const selscan_gated_dims_t* d, bool step, GatedShape* s) {
     if (!d) return SELSCAN_ERR_NULL;
     const int64_t L = step ? 1 : d->seqlen;
-    if (d->batch < 0 || d->dim < 0 || L < 0 || L >= (int64_t(1) << 27) || d->dim > (int64_t(1) << 24))
+    if (d->batch < 0 || d->dim < 0 || L < 0 || L >= (int64_t(1) << 27) || d->dim > (int64_t(1) << 20))
         return SELSCAN_ERR_DIMS;
     if (!known_dtype(d->dtype)) return SELSCAN_ERR_DTYPE;
     if (d->kind != SELSCAN_GATED_MIX && d->kind != SELSCAN_GATED_DECAY) return SELSCAN_ERR_CONFIG;

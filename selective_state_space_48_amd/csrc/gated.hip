@@ -1,9 +1,12 @@
 // Gated linear recurrence, its token step and its gradients.
 //
-// A token's decay a is held as a or as a - 1, whichever is smaller: formed without
-// cancellation (a sigmoid, or the exponential's series), it keeps full relative
-// accuracy of what is remembered where a is near 0, and of 1 - a, and with it of
-// what the state settles to, where a is near 1.
+// Bound by memory where the vector units keep up: a bfloat16 value leaves them some
+// 80 slots at the rate of a large copy (five tensors), of which the sigmoids, the
+// exponential, the root and the gate take half.
+//
+// What a long memory settles to hangs on 1 - a, which a itself, near 1, does not
+// hold: 1 - a is formed without cancellation, and what a group of tokens leaves of
+// the state is held as the product of its decays or, near 1, as that less 1.
 #include "../../include/selscan.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -38,61 +41,43 @@ struct GaArgs {
     const double* enter;   // the states (gradients) entering the runs; null: h0 (dlast)
 };
 
-// sigmoid(v) and 1 - sigmoid(v), each to full relative accuracy.
-struct Sig { float s, c; };
-__device__ __forceinline__ Sig sigmoid2(float v) {
-    const float t = exp2_hw(-fabsf(v) * kLog2e);
-    const float w = rcp_hw(1.0f + t), m = t * w;
-    return v >= 0.0f ? Sig{w, m} : Sig{m, w};
+// sigmoid(v) to full relative accuracy, and sigmoid'(v).
+__device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw(-v * kLog2e)); }
+struct Sig { float s, slope; };
+__device__ __forceinline__ Sig sigmoid_slope(float v) {
+    const float t = exp2_hw(-fabsf(v) * kLog2e), w = rcp_hw(1.0f + t), m = t * w;
+    return {v >= 0.0f ? w : m, m * w};
 }
 
-// A decay a in [0, 1], held so that it has full relative accuracy near 0 and 1 - a
-// near 1: q is a itself (sign bit clear) or a - 1 (sign bit set), and p what is to
-// be added, 0 or 1.
-__device__ __forceinline__ float whole_of(float q) {
-    return __int_as_float((__float_as_int(q) >> 31) & 0x3f800000);
+// A token of one channel: its decay a, e = a - 1 and its input's weight f: h = a h + f x.
+struct Token { float a, e, f; };
+
+// mix: a = 1 - sigmoid(g), f = sigmoid(g), each to full relative accuracy. (slope: sigmoid'(g))
+__device__ __forceinline__ Token mix_of(float g, float* slope) {
+    const float t = exp2_hw(-fabsf(g) * kLog2e), w = rcp_hw(1.0f + t), m = t * w;
+    const bool up = g >= 0.0f;
+    const float u = up ? w : m;
+    *slope = m * w;
+    return {up ? m : w, -u, u};
 }
 
-// e^l for l <= 0 in that form. From -1/2 on, where a - 1 would cancel, a - 1 is the
-// Taylor series up to l^8 / 8! (its rest is below 2^-26 of the sum).
-__device__ __forceinline__ float decay_of(float l) {
-    float s = 1.0f / 40320;
-    s = fmaf(s, l, 1.0f / 5040);
-    s = fmaf(s, l, 1.0f / 720);
-    s = fmaf(s, l, 1.0f / 120);
-    s = fmaf(s, l, 1.0f / 24);
-    s = fmaf(s, l, 1.0f / 6);
-    s = fmaf(s, l, 0.5f);
-    return l < -0.5f ? exp2_hw(l * kLog2e) : -fabsf(fmaf(l * l, s, l));
-}
-
-// h after a token: a h + b.
-__device__ __forceinline__ float step_of(float q, float p, float h, float b) {
-    return fmaf(p, h, fmaf(q, h, b));
-}
-
-// A token of one channel: its decay, its input's weight f (b = f x), and what the gradients use.
-struct Token {
-    float q, p, f;
-    Sig v, s;  // of g and r
-    float w;   // sqrt(1 - a^2)
-};
-template <bool DECAY>
-__device__ __forceinline__ Token token_of(float g, float r, float A) {
-    Token k{};
-    k.v = sigmoid2(g);
-    if constexpr (!DECAY) {
-        k.q = g > 0.0f ? k.v.c : -k.v.s;
-        k.p = whole_of(k.q);
-        k.f = k.v.s;
-    } else {
-        k.s = sigmoid2(r);
-        k.q = decay_of(A * k.s.s);
-        k.p = whole_of(k.q);
-        k.w = __builtin_amdgcn_sqrtf(((1.0f - k.p) - k.q) * ((1.0f + k.p) + k.q));
-        k.f = k.w * k.v.s;
+// decay: a = exp(l), l = A sigmoid(r) <= 0. From -0.35 on, where a - 1 would cancel,
+// a - 1 = l + l^2 p(l), p the best cubic for (e^l - 1 - l) / l^2 there (the sum's
+// relative error with its roundings is below 1.4 of 2^-24). f = sqrt(1 - a^2) times
+// the input gate, 1 - a^2 = -e (2 + e). ANY false: no channel of the wave has such l.
+constexpr float kNear = -0.35f;
+template <bool ANY> __device__ __forceinline__ Token decay_of(float l) {
+    float p = 0.007231935393065214f;
+    p = fmaf(p, l, 0.0413486510515213f);
+    p = fmaf(p, l, 0.1666298657655716f);
+    p = fmaf(p, l, 0.49999865889549255f);
+    float e = fmaf(l * l, p, l), a = 1.0f + e;
+    if constexpr (ANY) {
+        const float far = exp2_hw(l * kLog2e);
+        a = l < kNear ? far : a;
+        e = l < kNear ? far - 1.0f : e;
     }
-    return k;
+    return {a, e, __builtin_amdgcn_sqrtf(-e * (2.0f + e))};
 }
 
 // The channel's A, a NaN where it is above 0 (which has no sqrt(1 - a^2)).
@@ -119,11 +104,11 @@ template <typename T> __device__ __forceinline__ void put(void* p, int64_t i, fl
 // A workgroup walks CL * V channels of an entry through tiles of tokens. A lane
 // holds V channels (4 bytes of a row) of N tokens in a row; 64 / CL lanes of a
 // wave, and the waves, hold the groups of N tokens after one another. A group
-// steps its tokens from 0, which gives its state S and, as the product of its
-// decays in 64 bits, what it leaves of the state that enters it: P. Groups are
-// joined by h = P h + S in 64 bits, inside a wave by shuffles and over the waves
-// through LDS, so that a tile costs one barrier (the LDS entries alternate) and
-// every value is read once. The next tile's loads are in flight meanwhile.
+// steps its tokens from 0, which gives its state S, and what it leaves of the
+// state that enters it, P. Groups are joined by h = P h + S in 64 bits, inside a
+// wave by shuffles and over the waves through LDS, so that a tile costs one
+// barrier (the LDS entries alternate) and every value is read once. The next
+// tile's loads are in flight meanwhile.
 constexpr int kWaves = 8;
 
 template <int B> struct RawOf;
@@ -153,21 +138,41 @@ __device__ __forceinline__ Stretch after(const Stretch& first, const Stretch& th
     return {then.P * first.P, then.P * first.S + then.S};
 }
 
-// Where a thread stands: lane column c, group `first` of N tokens in the tile.
-template <int V, int CL, int N> struct Place {
-    static constexpr int kTile = kWaves * (64 / CL) * N, kChan = CL * V;
-    int lane, wave, c, tg;
-    int64_t d, b;     // first channel, entry
+// The product of a group's decays: as it is, and less 1, which keeps what the first
+// loses near 1 (as the first keeps what the second loses near 0).
+struct Product {
+    float D = 1.0f, E = 0.0f;
+    __device__ __forceinline__ void step(float a, float e) {
+        D *= a;
+        E += fmaf(E, e, e);
+    }
+    __device__ __forceinline__ double value() const { return D < 0.5f ? double(D) : 1.0 + double(E); }
+};
+
+// Where a thread stands: lane column c of its workgroup's channels, group tg of its wave.
+template <typename T, int V, int CL, int N> struct Place {
+    static constexpr int kGroups = 64 / CL, kWaveTokens = kGroups * N, kTile = kWaves * kWaveTokens, kChan = CL * V;
+    int wave, c, tg;
+    int64_t d0, d, b;  // the workgroup's first channel, the lane's, the entry
     bool live;
+    uint32_t off;      // bytes from the wave's first value in a tile to the lane's
     __device__ __forceinline__ Place(int64_t block, int64_t D) {
-        lane = threadIdx.x % 64; wave = threadIdx.x / 64;
-        c = lane % CL; tg = lane / CL;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        c = threadIdx.x % CL;
+        tg = threadIdx.x % 64 / CL;
         const int64_t blocks = (D + kChan - 1) / kChan;
-        d = block % blocks * kChan + c * V;
+        d0 = block % blocks * kChan;
+        d = d0 + c * V;
         b = block / blocks;
         live = d < D;
+        // (a lane without channels reads the first ones)
+        off = uint32_t((int64_t(tg) * N * D + (live ? c * V : 0)) * int64_t(sizeof(T)));
     }
-    __device__ __forceinline__ int64_t token(int64_t t0) const { return t0 + (wave * (64 / CL) + tg) * N; }
+    // The wave's first value in the tile at t0, and the lane's first token.
+    __device__ __forceinline__ int64_t base(const GaArgs& a, int64_t t0) const {
+        return (b * a.L + t0 + wave * kWaveTokens) * a.D + d0;
+    }
+    __device__ __forceinline__ int64_t token(int64_t t0) const { return t0 + wave * kWaveTokens + tg * N; }
 };
 
 // The group's stretch before this one in its wave (P 1, S 0 for the first), and the wave's own whole stretch in
@@ -178,7 +183,6 @@ template <int CL> __device__ __forceinline__ Stretch before_in_wave(Stretch& own
         const Stretch prev = {__shfl_up(own.P, s * CL, 64), __shfl_up(own.S, s * CL, 64)};
         if (tg >= s) own = after(prev, own);
     }
-    if constexpr (CL == 64) return {1.0, 0.0};
     const Stretch prev = {__shfl_up(own.P, CL, 64), __shfl_up(own.S, CL, 64)};
     return tg ? prev : Stretch{1.0, 0.0};
 }
@@ -190,21 +194,72 @@ template <int CL> __device__ __forceinline__ Stretch after_in_wave(Stretch& own,
         const Stretch next = {__shfl_down(own.P, s * CL, 64), __shfl_down(own.S, s * CL, 64)};
         if (tg + s < n) own = after(next, own);
     }
-    if constexpr (CL == 64) return {1.0, 0.0};
     const Stretch next = {__shfl_down(own.P, CL, 64), __shfl_down(own.S, CL, 64)};
     return tg + 1 < n ? next : Stretch{1.0, 0.0};
 }
 
-// Loads of N tokens of one tensor at `at` (element of the group's first token), tokens from `last` on taken from it.
+// A pointer that the whole wave shares, kept in scalar registers: rows then cost no vector additions (the compiler
+// adds the lane's offset first, and then to every row in 64 bits).
+template <typename P> __device__ __forceinline__ P* uniform(P* p) {
+    asm("" : "+s"(p));
+    return p;
+}
+
+// The lane's N tokens of one tensor, `base` the wave's first value; tokens past `left` (the last that exists)
+// taken from it. `row`: bytes of a row.
 template <typename T, int V, int N>
-__device__ __forceinline__ void fetch(const void* p, int64_t at, int64_t D, int last, raw_t<T, V> (&r)[N]) {
-    const T* q = static_cast<const T*>(p) + at;
-    if (last >= N - 1) {
+__device__ __forceinline__ void fetch(const void* p, int64_t base, uint32_t off, int64_t row, raw_t<T, V> (&r)[N]) {
+    const char* q = reinterpret_cast<const char*>(static_cast<const T*>(p) + base);
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const raw_t<T, V>*>(q + i * D);
-    } else {
+    for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const raw_t<T, V>*>(uniform(q + i * row) + off);
+}
+template <typename T, int V, int N>
+__device__ __forceinline__ void fetch_some(const void* p, int64_t base, uint32_t off, int64_t row, int left,
+                                           raw_t<T, V> (&r)[N]) {
+    const char* q = reinterpret_cast<const char*>(static_cast<const T*>(p) + base);
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const raw_t<T, V>*>(q + (i < last ? i : last) * D);
+    for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const raw_t<T, V>*>(q + (off + uint32_t(i < left ? i : left) * uint32_t(row)));
+}
+template <typename T, int V, int N>
+__device__ __forceinline__ void store_rows(void* p, int64_t base, uint32_t off, int64_t row, int i, const float (&o)[V]) {
+    char* q = uniform(reinterpret_cast<char*>(static_cast<T*>(p) + base) + i * row);
+    *reinterpret_cast<raw_t<T, V>*>(q + off) = pack<T, V>(o);
+}
+
+// The state after the first `n` waves' stretches (against time: after those behind wave n), from h: their entries
+// are read two waves at a time, ahead of the products that wait for them.
+template <int V, int C>
+__device__ __forceinline__ void join(const Stretch (&whole)[kWaves][C], int c, int n, double (&h)[V]) {
+#pragma unroll
+    for (int j = 0; j < kWaves - 1; j += 2) {
+        if (j >= n) break;
+        Stretch s[2][V];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[u][v] = whole[j + u][c + v];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (j + u < n)
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = s[u][v].P * h[v] + s[u][v].S;
+    }
+}
+template <int V, int C>
+__device__ __forceinline__ void join_back(const Stretch (&whole)[kWaves][C], int c, int n, double (&h)[V]) {
+#pragma unroll
+    for (int j = kWaves - 1; j > 0; j -= 2) {
+        if (j <= n) break;
+        Stretch s[2][V];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[u][v] = whole[j - u][c + v];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (j - u > n)
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = s[u][v].P * h[v] + s[u][v].S;
     }
 }
 
@@ -212,107 +267,113 @@ __device__ __forceinline__ void fetch(const void* p, int64_t at, int64_t D, int 
 enum { kOut = 0, kKeep = 1, kRun = 2 };
 
 template <typename T, bool DECAY, bool GATE, int V, int CL, int N, int MODE>
-__global__ __launch_bounds__(kWaves * 64) void fwd_kernel(GaArgs a) {
-    using W = Place<V, CL, N>;
+__global__ __launch_bounds__(kWaves * 64, N == 8 ? 4 : 2) void fwd_kernel(GaArgs a) {
+    using W = Place<T, V, CL, N>;
     using R = raw_t<T, V>;
     __shared__ Stretch whole[2][kWaves][W::kChan];
     __shared__ double carry[2][W::kChan];
     const int64_t per = (a.D + W::kChan - 1) / W::kChan * a.B, idx = xcd_tile(blockIdx.x, gridDim.x);
     const int64_t run = idx / per;
     const W w(idx % per, a.D);
-    const int64_t n = entry_length(a.lengths, w.b, a.L), row = w.b * a.D + w.d, rows = a.B * a.D;
+    const int64_t n = entry_length(a.lengths, w.b, a.L), lane = w.b * a.D + w.d, lanes = a.B * a.D;
     const int64_t begin = run * a.seg_len, end = begin + a.seg_len < a.L ? begin + a.seg_len : a.L;
-    const bool last_wave = w.wave == kWaves - 1 && w.tg == 64 / CL - 1;
+    const int64_t stop = end < n ? end : n, row = a.D * int64_t(sizeof(T));
+    const bool last_group = w.wave == kWaves - 1 && w.tg == W::kGroups - 1;
     float A[V];
-    Stretch all[V];
+    double allP[V];
+    bool any = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        A[v] = DECAY && w.live ? rate_of(a.A, w.d + v) : 0.0f;
-        all[v] = {1.0, 0.0};
-    }
-    if (w.wave == 0 && w.tg == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
+        A[v] = DECAY ? rate_of(a.A, w.live ? w.d + v : w.d0) : 0.0f;
+        any |= A[v] < kNear;
+        allP[v] = 1.0;
+        if (w.wave == 0 && w.tg == 0)
             carry[0][w.c * V + v] = MODE == kRun || !w.live ? 0.0
-                                    : a.enter               ? a.enter[run * rows + row + v]
-                                    : a.h0                  ? double(a.h0[row + v])
+                                    : a.enter               ? a.enter[run * lanes + lane + v]
+                                    : a.h0                  ? double(a.h0[lane + v])
                                                             : 0.0;
     }
+    any = __any(any);
     R nx[N], ng[N], nr[DECAY ? N : 1], nz[GATE ? N : 1];
     auto load = [&](int64_t t0) {
-        const int64_t t = w.token(t0);
-        if (!w.live || t >= n) return;
-        const int64_t at = (w.b * a.L + t) * a.D + w.d;
-        const int left = int(n - t < N ? n - t : N) - 1;
-        fetch<T, V, N>(a.x, at, a.D, left, nx);
-        fetch<T, V, N>(a.g, at, a.D, left, ng);
-        if constexpr (DECAY) fetch<T, V, N>(a.r, at, a.D, left, nr);
-        if constexpr (GATE) fetch<T, V, N>(a.z, at, a.D, left, nz);
+        const int64_t at = w.base(a, t0);
+        fetch<T, V, N>(a.x, at, w.off, row, nx);
+        fetch<T, V, N>(a.g, at, w.off, row, ng);
+        if constexpr (DECAY) fetch<T, V, N>(a.r, at, w.off, row, nr);
+        if constexpr (GATE) fetch<T, V, N>(a.z, at, w.off, row, nz);
     };
-    load(begin);
+    auto load_some = [&](int64_t t0, int left) {
+        const int64_t at = w.base(a, t0);
+        fetch_some<T, V, N>(a.x, at, w.off, row, left, nx);
+        fetch_some<T, V, N>(a.g, at, w.off, row, left, ng);
+        if constexpr (DECAY) fetch_some<T, V, N>(a.r, at, w.off, row, left, nr);
+        if constexpr (GATE) fetch_some<T, V, N>(a.z, at, w.off, row, left, nz);
+    };
+    // One tile; all its tokens exist if `whole_tile`, and the next one's loads are sent off if `more`.
     int buf = 0;
-    for (int64_t t0 = begin; t0 < end; t0 += W::kTile, buf ^= 1) {
+    auto tile = [&](int64_t t0, auto whole_tile, bool more) {
+        constexpr bool FULL = decltype(whole_tile)::value;
         const int64_t t = w.token(t0);
-        const int have = n - t < 0 ? 0 : n - t < N ? int(n - t) : N;
-        float q[N][V], b[N][V];
+        const int have = FULL ? N : n - t < 0 ? 0 : n - t < N ? int(n - t) : N;
+        float dec[N][V], b[N][V];
         R z[GATE ? N : 1];
+        Product prod[V];
+        auto tokens = [&](auto far) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float x[V], g[V], r[V];
-            unpack<T, V>(nx[i], x);
-            unpack<T, V>(ng[i], g);
-            if constexpr (DECAY) unpack<T, V>(nr[i], r);
-            if constexpr (GATE) z[i] = nz[i];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Token k = token_of<DECAY>(g[v], DECAY ? r[v] : 0.0f, A[v]);
-                q[i][v] = k.q;
-                b[i][v] = k.f * x[v];
-            }
-        }
-        if (have < N) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i) {
+                float x[V], g[V], r[V];
+                unpack<T, V>(nx[i], x);
+                unpack<T, V>(ng[i], g);
+                if constexpr (DECAY) unpack<T, V>(nr[i], r);
+                if constexpr (GATE) z[i] = nz[i];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    q[i][v] = i < have ? q[i][v] : -0.0f;
-                    b[i][v] = i < have ? b[i][v] : 0.0f;
+                    Token k;
+                    float slope;
+                    if constexpr (DECAY) {
+                        k = decay_of<decltype(far)::value>(A[v] * sigmoid(r[v]));
+                        k.f *= sigmoid(g[v]);
+                    } else {
+                        k = mix_of(g[v], &slope);
+                    }
+                    dec[i][v] = k.a;
+                    b[i][v] = k.f * x[v];
+                    if constexpr (!FULL) {
+                        const bool in = i < have;
+                        k.e = in ? k.e : 0.0f;
+                        dec[i][v] = in ? k.a : 1.0f;
+                        b[i][v] = in ? b[i][v] : 0.0f;
+                    }
+                    prod[v].step(dec[i][v], k.e);
                 }
-        }
-        if (t0 + W::kTile < end) load(t0 + W::kTile);
+            }
+        };
+        if (DECAY && !any) tokens(std::false_type{});
+        else tokens(std::true_type{});
+        if (more) load(t0 + W::kTile);
         Stretch own[V], before[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            double P = 1.0;
             float S = 0.0f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float p = whole_of(q[i][v]);
-                P *= double(p) + double(q[i][v]);
-                S = step_of(q[i][v], p, S, b[i][v]);
-            }
-            own[v] = {P, double(S)};
+            for (int i = 0; i < N; ++i) S = fmaf(dec[i][v], S, b[i][v]);
+            own[v] = {prod[v].value(), double(S)};
             before[v] = before_in_wave<CL>(own[v], w.tg);
-            if (w.tg == 64 / CL - 1) whole[buf][w.wave][w.c * V + v] = own[v];
+            if (w.tg == W::kGroups - 1) whole[buf][w.wave][w.c * V + v] = own[v];
         }
         __syncthreads();
         double h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = carry[buf][w.c * V + v];
-        for (int j = 0; j < w.wave; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Stretch s = whole[buf][j][w.c * V + v];
-                h[v] = s.P * h[v] + s.S;
-            }
-        if (last_wave) {
+        join<V>(whole[buf], w.c * V, w.wave, h);
+        if (last_group) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 carry[buf ^ 1][w.c * V + v] = own[v].P * h[v] + own[v].S;
                 if constexpr (MODE == kRun) {
-                    Stretch tile = own[v];
-                    for (int j = kWaves - 2; j >= 0; --j) tile = after(whole[buf][j][w.c * V + v], tile);
-                    all[v].P *= tile.P;
+                    double P = own[v].P;
+                    for (int j = 0; j < kWaves - 1; ++j) P *= whole[buf][j][w.c * V + v].P;
+                    allP[v] *= P;
                 }
             }
         }
@@ -322,39 +383,72 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_kernel(GaArgs a) {
             for (int v = 0; v < V; ++v) hf[v] = float(before[v].P * h[v] + before[v].S);
             if (a.ckpt && w.live && t % SELSCAN_GATED_CKPT == 0 && t < a.L)
 #pragma unroll
-                for (int v = 0; v < V; ++v) a.ckpt[t / SELSCAN_GATED_CKPT * rows + row + v] = hf[v];
+                for (int v = 0; v < V; ++v) a.ckpt[t / SELSCAN_GATED_CKPT * lanes + lane + v] = hf[v];
             if constexpr (MODE == kOut) {
-                T* y = static_cast<T*>(a.y) + (w.b * a.L + t) * a.D + w.d;
+                const int64_t at = w.base(a, t0);
+                if (w.live) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    float o[V];
+                    for (int i = 0; i < N; ++i) {
+                        float o[V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        hf[v] = step_of(q[i][v], whole_of(q[i][v]), hf[v], b[i][v]);
-                        o[v] = hf[v];
+                        for (int v = 0; v < V; ++v) {
+                            hf[v] = fmaf(dec[i][v], hf[v], b[i][v]);
+                            o[v] = hf[v];
+                        }
+                        if constexpr (GATE) {
+                            float f[V];
+                            unpack<T, V>(z[i], f);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) o[v] *= silu(f[v]);
+                        }
+                        if constexpr (!FULL) {
+                            if (t + i >= a.L) continue;
+#pragma unroll
+                            for (int v = 0; v < V; ++v) o[v] = i < have ? o[v] : 0.0f;
+                        }
+                        store_rows<T, V, N>(a.y, at, w.off, row, i, o);
                     }
-                    if constexpr (GATE) {
-                        float f[V];
-                        unpack<T, V>(z[i], f);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] *= silu(f[v]);
-                    }
-                    if (i >= have)
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] = 0.0f;
-                    if (w.live && t + i < a.L) *reinterpret_cast<R*>(y + i * a.D) = pack<T, V>(o);
                 }
             }
         }
+        buf ^= 1;
+    };
+    int64_t t0 = begin;
+    const int64_t whole_end = begin + (stop > begin ? (stop - begin) / W::kTile * W::kTile : 0);
+    if (t0 < whole_end) load(t0);
+    for (; t0 < whole_end; t0 += W::kTile) tile(t0, std::true_type{}, t0 + W::kTile < whole_end);
+    if (t0 < stop) {
+        if (w.token(t0) < n) {
+            const int64_t left = n - w.token(t0);
+            load_some(t0, int(left < N ? left : N) - 1);
+        }
+        tile(t0, std::false_type{}, false);
+        t0 += W::kTile;
     }
     if constexpr (MODE == kRun) {
-        if (last_wave && w.live)
+        if (last_group && w.live)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.runs[run * lanes + lane + v] = {allP[v], carry[buf][w.c * V + v]};
+        return;
+    }
+    __syncthreads();
+    // tiles behind the entry's length
+    for (; t0 < end; t0 += W::kTile) {
+        const int64_t t = w.token(t0);
+        if (!w.live || t >= a.L) continue;
+        if (a.ckpt && t % SELSCAN_GATED_CKPT == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                a.runs[run * rows + row + v] = {all[v].P, carry[buf][w.c * V + v]};
-    } else if (last_wave && w.live && a.last && end == a.L) {
+                a.ckpt[t / SELSCAN_GATED_CKPT * lanes + lane + v] = float(carry[buf][w.c * V + v]);
+        if constexpr (MODE == kOut) {
+            const float zero[V] = {};
+            for (int i = 0; i < N && t + i < a.L; ++i)
+                store_rows<T, V, N>(a.y, w.base(a, t0), w.off, row, i, zero);
+        }
+    }
+    if (last_group && w.live && a.last && end == a.L) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.last[row + v] = float(carry[buf][w.c * V + v]);
+        for (int v = 0; v < V; ++v) a.last[lane + v] = float(carry[buf][w.c * V + v]);
     }
 }
 
@@ -362,129 +456,171 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_kernel(GaArgs a) {
 // C = a (d + C), the same decays against time.
 template <typename T, bool DECAY, bool GATE, int V, int CL, int N, int MODE>
 __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
-    using W = Place<V, CL, N>;
+    using W = Place<T, V, CL, N>;
     using R = raw_t<T, V>;
-    __shared__ Stretch fwd[2][MODE == kOut ? kWaves : 1][W::kChan], bwd[2][kWaves][W::kChan];
+    constexpr bool OUT = MODE == kOut;
+    __shared__ Stretch fwd[2][OUT ? kWaves : 1][W::kChan], bwd[2][kWaves][W::kChan];
     __shared__ double carry[2][W::kChan];
     const int64_t per = (a.D + W::kChan - 1) / W::kChan * a.B, idx = xcd_tile(blockIdx.x, gridDim.x);
     const int64_t run = idx / per;
     const W w(idx % per, a.D);
-    const int64_t n = entry_length(a.lengths, w.b, a.L), row = w.b * a.D + w.d, rows = a.B * a.D;
+    const int64_t n = entry_length(a.lengths, w.b, a.L), lane = w.b * a.D + w.d, lanes = a.B * a.D;
     const int64_t begin = run * a.seg_len, end = begin + a.seg_len < a.L ? begin + a.seg_len : a.L;
-    const int64_t tiles = (end - begin + W::kTile - 1) / W::kTile;
+    const int64_t stop = end < n ? end : n, row = a.D * int64_t(sizeof(T));
+    const int64_t tiles = stop > begin ? (stop - begin + W::kTile - 1) / W::kTile : 0;
     const bool first_group = w.wave == 0 && w.tg == 0;
     float A[V], dA[V];
     double allP[V];
+    bool any = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        A[v] = DECAY && w.live ? rate_of(a.A, w.d + v) : 0.0f;
+        A[v] = DECAY ? rate_of(a.A, w.live ? w.d + v : w.d0) : 0.0f;
+        any |= A[v] < kNear;
         dA[v] = 0.0f;
         allP[v] = 1.0;
         if (first_group)
             carry[0][w.c * V + v] = MODE == kRun || !w.live ? 0.0
-                                    : a.enter               ? a.enter[run * rows + row + v]
-                                    : a.dlast               ? double(a.dlast[row + v])
+                                    : a.enter               ? a.enter[run * lanes + lane + v]
+                                    : a.dlast               ? double(a.dlast[lane + v])
                                                             : 0.0;
     }
-    constexpr bool OUT = MODE == kOut;
+    any = __any(any);
     R nx[OUT ? N : 1], ng[N], nr[DECAY ? N : 1], nz[GATE ? N : 1], nd[N];
     float nh[V];
-    auto load = [&](int64_t t0) {
-        const int64_t t = w.token(t0);
-        if (!w.live || t >= n) return;
-        const int64_t at = (w.b * a.L + t) * a.D + w.d;
-        const int left = int(n - t < N ? n - t : N) - 1;
-        if constexpr (OUT) fetch<T, V, N>(a.x, at, a.D, left, nx);
-        if constexpr (OUT || !DECAY) fetch<T, V, N>(a.g, at, a.D, left, ng);
-        if constexpr (DECAY) fetch<T, V, N>(a.r, at, a.D, left, nr);
-        if constexpr (GATE) fetch<T, V, N>(a.z, at, a.D, left, nz);
-        fetch<T, V, N>(a.dy, at, a.D, left, nd);
+    auto enter_tile = [&](int64_t t0) {
         if constexpr (OUT)
 #pragma unroll
-            for (int v = 0; v < V; ++v) nh[v] = a.ckpt[t0 / SELSCAN_GATED_CKPT * rows + row + v];
+            for (int v = 0; v < V; ++v)
+                nh[v] = a.ckpt[t0 / SELSCAN_GATED_CKPT * lanes + (w.live ? lane + v : w.b * a.D + w.d0)];
     };
-    load(begin + (tiles - 1) * W::kTile);
+    auto load = [&](int64_t t0) {
+        const int64_t at = w.base(a, t0);
+        if constexpr (OUT) fetch<T, V, N>(a.x, at, w.off, row, nx);
+        if constexpr (OUT || !DECAY) fetch<T, V, N>(a.g, at, w.off, row, ng);
+        if constexpr (DECAY) fetch<T, V, N>(a.r, at, w.off, row, nr);
+        if constexpr (GATE) fetch<T, V, N>(a.z, at, w.off, row, nz);
+        fetch<T, V, N>(a.dy, at, w.off, row, nd);
+        enter_tile(t0);
+    };
+    auto load_some = [&](int64_t t0, int left) {
+        const int64_t at = w.base(a, t0);
+        if constexpr (OUT) fetch_some<T, V, N>(a.x, at, w.off, row, left, nx);
+        if constexpr (OUT || !DECAY) fetch_some<T, V, N>(a.g, at, w.off, row, left, ng);
+        if constexpr (DECAY) fetch_some<T, V, N>(a.r, at, w.off, row, left, nr);
+        if constexpr (GATE) fetch_some<T, V, N>(a.z, at, w.off, row, left, nz);
+        fetch_some<T, V, N>(a.dy, at, w.off, row, left, nd);
+        enter_tile(t0);
+    };
+    if constexpr (OUT) {  // tiles behind the entry's length
+        for (int64_t t0 = begin + tiles * W::kTile; t0 < end; t0 += W::kTile) {
+            const int64_t t = w.token(t0), at = w.base(a, t0);
+            const float zero[V] = {};
+            for (int i = 0; w.live && i < N && t + i < a.L; ++i) {
+                store_rows<T, V, N>(a.dx, at, w.off, row, i, zero);
+                store_rows<T, V, N>(a.dg, at, w.off, row, i, zero);
+                if constexpr (DECAY) store_rows<T, V, N>(a.dr, at, w.off, row, i, zero);
+                if constexpr (GATE) store_rows<T, V, N>(a.dz, at, w.off, row, i, zero);
+            }
+        }
+    }
     int buf = 0;
-    for (int64_t k = tiles - 1; k >= 0; --k, buf ^= 1) {
-        const int64_t t0 = begin + k * W::kTile, t = w.token(t0);
-        const int have = n - t < 0 ? 0 : n - t < N ? int(n - t) : N;
-        Token tok[N][V];
-        float x[OUT ? N : 1][V], d[N][V], dy[OUT && GATE ? N : 1][V], h0[V];
-        R z[OUT && GATE ? N : 1];
+    auto tile = [&](int64_t t0, auto whole_tile, bool more) {
+        constexpr bool FULL = decltype(whole_tile)::value;
+        const int64_t t = w.token(t0);
+        const int have = FULL ? N : n - t < 0 ? 0 : n - t < N ? int(n - t) : N;
+        // of each token: a; d, dy silu(z); and (OUT) b, then the state before it; f; and
+        //   mix:   u', x
+        //   decay: f' = w x v', dl = G (a h - rest), A s', s
+        // with the gate dy silu'(z)
+        constexpr int M = OUT ? N : 1, MD = OUT && DECAY ? N : 1, MG = OUT && GATE ? N : 1;
+        float dec[N][V], d[N][V], hb[M][V], f[M][V], fs[M][V], rest[M][V], rs[MD][V], sr[MD][V], dz[MG][V], h0[V];
+        Product prod[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) h0[v] = OUT ? nh[v] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float g[V], r[V], f[V];
-            if constexpr (OUT) unpack<T, V>(nx[i], x[i]);
-            if constexpr (OUT || !DECAY) unpack<T, V>(ng[i], g);
-            if constexpr (DECAY) unpack<T, V>(nr[i], r);
-            unpack<T, V>(nd[i], d[i]);
-            if constexpr (GATE) unpack<T, V>(nz[i], f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                tok[i][v] = token_of<DECAY>(OUT || !DECAY ? g[v] : 0.0f, DECAY ? r[v] : 0.0f, A[v]);
-                if constexpr (GATE) {
-                    if constexpr (OUT) dy[i][v] = d[i][v];
-                    d[i][v] *= silu(f[v]);
-                }
-            }
-            if constexpr (OUT && GATE) z[i] = nz[i];
-        }
-        if (have < N) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (i < have) continue;
-                    tok[i][v].q = -0.0f;
-                    tok[i][v].p = 1.0f;
-                    tok[i][v].f = 0.0f;
-                    d[i][v] = 0.0f;
-                    if constexpr (OUT) x[i][v] = 0.0f;
-                }
-        }
-        if (k > 0) load(t0 - W::kTile);
-        Stretch ownb[V], later[V], before[OUT ? V : 1];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            double P = 1.0;
-            float S = 0.0f, C = 0.0f;
+        auto tokens = [&](auto far) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const Token& m = tok[i][v];
-                P *= double(m.p) + double(m.q);
-                if constexpr (OUT) S = step_of(m.q, m.p, S, m.f * x[i][v]);
-            }
+                float x[V], g[V], r[V], z[V];
+                if constexpr (OUT) unpack<T, V>(nx[i], x);
+                if constexpr (OUT || !DECAY) unpack<T, V>(ng[i], g);
+                if constexpr (DECAY) unpack<T, V>(nr[i], r);
+                if constexpr (GATE) unpack<T, V>(nz[i], z);
+                unpack<T, V>(nd[i], d[i]);
 #pragma unroll
-            for (int i = N - 1; i >= 0; --i) C = step_of(tok[i][v].q, tok[i][v].p, d[i][v] + C, 0.0f);
-            ownb[v] = {P, double(C)};
-            later[v] = after_in_wave<CL>(ownb[v], w.tg);
-            if (w.tg == 0) bwd[buf][w.wave][w.c * V + v] = ownb[v];
+                for (int v = 0; v < V; ++v) {
+                    const bool in = FULL || i < have;
+                    Token k;
+                    if constexpr (DECAY) {
+                        const Sig s = sigmoid_slope(r[v]);
+                        k = decay_of<decltype(far)::value>(A[v] * s.s);
+                        if constexpr (OUT) {
+                            const Sig u = sigmoid_slope(g[v]);
+                            const float ux = u.s * x[v];
+                            hb[i][v] = k.f * ux;
+                            fs[i][v] = k.f * x[v] * u.slope;
+                            // a^2 / w of w's derivative by l (0 where a rounds to 1)
+                            rest[i][v] = k.f > 0.0f ? k.a * k.a * rcp_hw(k.f) * ux : 0.0f;
+                            f[i][v] = k.f * u.s;
+                            rs[i][v] = A[v] * s.slope;
+                            sr[i][v] = in ? s.s : 0.0f;
+                        }
+                    } else {
+                        float slope;
+                        k = mix_of(g[v], &slope);
+                        if constexpr (OUT) {
+                            hb[i][v] = k.f * x[v];
+                            f[i][v] = k.f;
+                            fs[i][v] = slope;
+                            rest[i][v] = x[v];
+                        }
+                    }
+                    if constexpr (GATE) {
+                        const float s = rcp_hw(1.0f + exp2_hw(-z[v] * kLog2e));
+                        if constexpr (OUT) dz[i][v] = d[i][v] * (s * fmaf(z[v], 1.0f - s, 1.0f));
+                        d[i][v] *= z[v] * s;
+                    }
+                    dec[i][v] = in ? k.a : 1.0f;
+                    d[i][v] = in ? d[i][v] : 0.0f;
+                    if constexpr (OUT) hb[i][v] = in ? hb[i][v] : 0.0f;
+                    prod[v].step(dec[i][v], in ? k.e : 0.0f);
+                }
+            }
+        };
+        if (DECAY && !any) tokens(std::false_type{});
+        else tokens(std::true_type{});
+        if (more) load(t0 - W::kTile);
+        Stretch own[V], later[V], before[OUT ? V : 1];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float S = 0.0f, C = 0.0f;
+            if constexpr (OUT)
+#pragma unroll
+                for (int i = 0; i < N; ++i) S = fmaf(dec[i][v], S, hb[i][v]);
+#pragma unroll
+            for (int i = N - 1; i >= 0; --i) C = dec[i][v] * (d[i][v] + C);
+            const double P = prod[v].value();
+            own[v] = {P, double(C)};
+            later[v] = after_in_wave<CL>(own[v], w.tg);
+            if (w.tg == 0) bwd[buf][w.wave][w.c * V + v] = own[v];
             if constexpr (OUT) {
-                Stretch own = {P, double(S)};
-                before[v] = before_in_wave<CL>(own, w.tg);
-                if (w.tg == 64 / CL - 1) fwd[buf][w.wave][w.c * V + v] = own;
+                Stretch s = {P, double(S)};
+                before[v] = before_in_wave<CL>(s, w.tg);
+                if (w.tg == W::kGroups - 1) fwd[buf][w.wave][w.c * V + v] = s;
             }
         }
         __syncthreads();
         double C[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) C[v] = carry[buf][w.c * V + v];
-        for (int j = kWaves - 1; j > w.wave; --j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Stretch s = bwd[buf][j][w.c * V + v];
-                C[v] = s.P * C[v] + s.S;
-            }
+        join_back<V>(bwd[buf], w.c * V, w.wave, C);
         if (first_group) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                carry[buf ^ 1][w.c * V + v] = ownb[v].P * C[v] + ownb[v].S;
+                carry[buf ^ 1][w.c * V + v] = own[v].P * C[v] + own[v].S;
                 if constexpr (!OUT) {
-                    Stretch tile = ownb[v];
-                    for (int j = 1; j < kWaves; ++j) tile = after(bwd[buf][j][w.c * V + v], tile);
-                    allP[v] *= tile.P;
+                    double P = own[v].P;
+                    for (int j = 1; j < kWaves; ++j) P *= bwd[buf][j][w.c * V + v].P;
+                    allP[v] *= P;
                 }
             }
         }
@@ -492,85 +628,84 @@ __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
             double h[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = h0[v];
-            for (int j = 0; j < w.wave; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const Stretch s = fwd[buf][j][w.c * V + v];
-                    h[v] = s.P * h[v] + s.S;
-                }
-            const int64_t at = (w.b * a.L + t) * a.D + w.d;
-            float hb[N][V];
+            join<V>(fwd[buf], w.c * V, w.wave, h);
+            const int64_t at = w.base(a, t0);
+            float Cf[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                Cf[v] = float(later[v].P * C[v] + later[v].S);
                 float hf = float(before[v].P * h[v] + before[v].S);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
+                    const float b = hb[i][v];
                     hb[i][v] = hf;
-                    hf = step_of(tok[i][v].q, tok[i][v].p, hf, tok[i][v].f * x[i][v]);
-                    if constexpr (GATE) dy[i][v] *= hf;  // (times silu' below)
+                    hf = fmaf(dec[i][v], hf, b);
+                    if constexpr (GATE) dz[i][v] *= hf;
                 }
             }
-            float Cf[V];
+            if (w.live) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) Cf[v] = float(later[v].P * C[v] + later[v].S);
+                for (int i = N - 1; i >= 0; --i) {
+                    float ox[V], og[V], orr[V], oz[V];
+                    const bool in = FULL || i < have;
 #pragma unroll
-            for (int i = N - 1; i >= 0; --i) {
-                float ox[V], og[V], orr[V], oz[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const Token& m = tok[i][v];
-                    const float G = d[i][v] + Cf[v];
-                    Cf[v] = step_of(m.q, m.p, G, 0.0f);
-                    ox[v] = G * m.f;
-                    if constexpr (!DECAY) {
-                        og[v] = G * (x[i][v] - hb[i][v]) * (m.v.s * m.v.c);
-                    } else {
-                        og[v] = G * m.w * x[i][v] * (m.v.s * m.v.c);
-                        const float dec = m.p + m.q, ratio = m.w > 0.0f ? dec * rcp_hw(m.w) : 0.0f;
-                        const float dl = G * dec * (hb[i][v] - ratio * (m.v.s * x[i][v]));
-                        orr[v] = dl * A[v] * (m.s.s * m.s.c);
-                        dA[v] += i < have ? dl * m.s.s : 0.0f;
+                    for (int v = 0; v < V; ++v) {
+                        const float G = d[i][v] + Cf[v];
+                        Cf[v] = dec[i][v] * G;
+                        ox[v] = in ? G * f[i][v] : 0.0f;
+                        if constexpr (!DECAY) {
+                            og[v] = in ? G * (rest[i][v] - hb[i][v]) * fs[i][v] : 0.0f;
+                        } else {
+                            og[v] = in ? G * fs[i][v] : 0.0f;
+                            const float dl = in ? G * fmaf(dec[i][v], hb[i][v], -rest[i][v]) : 0.0f;
+                            dA[v] = fmaf(dl, sr[i][v], dA[v]);
+                            orr[v] = in ? dl * rs[i][v] : 0.0f;
+                        }
+                        if constexpr (GATE) oz[v] = in ? dz[i][v] : 0.0f;
                     }
-                    if constexpr (GATE) {
-                        float f[V];
-                        unpack<T, V>(z[i], f);
-                        oz[v] = dy[i][v] * silu_grad(f[v]);
-                    }
-                    if (i >= have) ox[v] = og[v] = orr[v] = oz[v] = 0.0f;
-                }
-                if (w.live && t + i < a.L) {
-                    auto out = [&](void* p, const float (&o)[V]) {
-                        *reinterpret_cast<R*>(static_cast<T*>(p) + at + i * a.D) = pack<T, V>(o);
-                    };
-                    out(a.dx, ox);
-                    out(a.dg, og);
-                    if constexpr (DECAY) out(a.dr, orr);
-                    if constexpr (GATE) out(a.dz, oz);
+                    if (!FULL && t + i >= a.L) continue;
+                    store_rows<T, V, N>(a.dx, at, w.off, row, i, ox);
+                    store_rows<T, V, N>(a.dg, at, w.off, row, i, og);
+                    if constexpr (DECAY) store_rows<T, V, N>(a.dr, at, w.off, row, i, orr);
+                    if constexpr (GATE) store_rows<T, V, N>(a.dz, at, w.off, row, i, oz);
                 }
             }
         }
+        buf ^= 1;
+    };
+    int64_t k = tiles - 1;
+    if (tiles && begin + tiles * W::kTile > n) {  // the last tile's tokens do not all exist
+        const int64_t t0 = begin + k * W::kTile;
+        if (w.token(t0) < n) {
+            const int64_t left = n - w.token(t0);
+            load_some(t0, int(left < N ? left : N) - 1);
+        }
+        tile(t0, std::false_type{}, false);
+        --k;
     }
+    if (k >= 0) load(begin + k * W::kTile);
+    for (; k >= 0; --k) tile(begin + k * W::kTile, std::true_type{}, k > 0);
     if constexpr (!OUT) {
         if (first_group && w.live)
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.runs[run * rows + row + v] = {allP[v], carry[buf][w.c * V + v]};
+            for (int v = 0; v < V; ++v) a.runs[run * lanes + lane + v] = {allP[v], carry[buf][w.c * V + v]};
         return;
     }
     if (first_group && w.live && a.dh0 && begin == 0) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.dh0[row + v] = float(carry[buf][w.c * V + v]);
+        for (int v = 0; v < V; ++v) a.dh0[lane + v] = float(carry[buf][w.c * V + v]);
     }
     if constexpr (DECAY) {
         if (a.dA_part) {  // the groups' sums in order
-            __shared__ float sums[kWaves * (64 / CL)][W::kChan];
+            __shared__ float sums[kWaves * W::kGroups][W::kChan];
 #pragma unroll
-            for (int v = 0; v < V; ++v) sums[w.wave * (64 / CL) + w.tg][w.c * V + v] = dA[v];
+            for (int v = 0; v < V; ++v) sums[w.wave * W::kGroups + w.tg][w.c * V + v] = dA[v];
             __syncthreads();
             if (first_group && w.live)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     float s = 0.0f;
-                    for (int j = 0; j < kWaves * (64 / CL); ++j) s += sums[j][w.c * V + v];
+                    for (int j = 0; j < kWaves * W::kGroups; ++j) s += sums[j][w.c * V + v];
                     a.dA_part[(run * a.B + w.b) * a.D + w.d + v] = s;
                 }
         }
@@ -605,8 +740,17 @@ template <typename T, bool DECAY>
 __global__ __launch_bounds__(256) void step_kernel(float* state, GaArgs a) {
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (i >= a.B * a.D) return;
-    const Token k = token_of<DECAY>(at<T>(a.g, i), DECAY ? at<T>(a.r, i) : 0.0f, DECAY ? rate_of(a.A, i % a.D) : 0.0f);
-    const float h = state[i], hn = step_of(k.q, k.p, h, k.f * at<T>(a.x, i));
+    Token k;
+    float slope;
+    if constexpr (DECAY) {
+        k = decay_of<true>(rate_of(a.A, i % a.D) * sigmoid(at<T>(a.r, i)));
+        k.f *= sigmoid(at<T>(a.g, i));
+    } else {
+        k = mix_of(at<T>(a.g, i), &slope);
+    }
+    // near 1 from a - 1, as a token loop has no other way to keep what its state settles to
+    const float h = state[i], b = k.f * at<T>(a.x, i);
+    const float hn = k.a < 0.5f ? fmaf(k.a, h, b) : h + fmaf(k.e, h, b);
     state[i] = hn;
     put<T>(a.y, i, a.z ? hn * silu(at<T>(a.z, i)) : hn);
 }
@@ -626,14 +770,27 @@ GaArgs args_of(const GatedTensors& t, const GatedShape& s, const GatedPlan& p) {
 // Channels of a lane: 4 bytes of a row, where rows of an odd number of bfloat16 values allow it.
 int lane_channels(const GatedShape& s) { return s.dtype == DType::BF16 && s.dim % 2 == 0 ? 2 : 1; }
 
-constexpr int kCL = 32;               // lanes across channels
-constexpr int kNF = 8, kNB = 8;       // tokens of a thread, forward and backward
-constexpr int kTileF = kWaves * (64 / kCL) * kNF, kTileB = kWaves * (64 / kCL) * kNB;
-static_assert(kTileF % SELSCAN_GATED_CKPT == 0 && kTileB % SELSCAN_GATED_CKPT == 0 && kNF <= SELSCAN_GATED_CKPT &&
-                  SELSCAN_GATED_CKPT % kNF == 0,
+// Lanes across channels, and tokens of a thread, of the wide and the narrow split.
+// Wide: 128-byte rows. Narrow: half of that, twice the workgroups, where the wide
+// ones would leave CUs idle or take a round more (the work of a workgroup is bound
+// by its CU; us, wide and narrow: bf16 4 x 2048 x 2048 74 and 40, 4 x 4096 x 5120
+// 214 and 194; but 4 x 2048 x 4096 62 and 60, 3 x 4096 x 5120 132 and 155, 8 x 2048
+// x 4096 with a gate 175 and 219, as two workgroups then read each line). Tokens of
+// a thread are what the registers take: 4 backward, where 8 spill (331 against 858).
+constexpr int kWide = 32, kNarrow = 16;
+constexpr int kNF = 8, kNFNarrow = 16, kNB = 4;
+constexpr int tile_of(int lanes, int tokens) { return kWaves * (64 / lanes) * tokens; }
+constexpr int kTile = tile_of(kWide, kNF);  // runs are of whole tiles
+static_assert(kTile % tile_of(kWide, kNB) == 0 && tile_of(kWide, kNB) % SELSCAN_GATED_CKPT == 0 &&
+                  tile_of(kNarrow, kNFNarrow) % SELSCAN_GATED_CKPT == 0 && tile_of(kNarrow, kNB) % SELSCAN_GATED_CKPT == 0 &&
+                  SELSCAN_GATED_CKPT % kNFNarrow == 0 && SELSCAN_GATED_CKPT % kNF == 0,
               "a checkpoint is the state entering a group of tokens, and every tile's first");
 
-int64_t blocks_of(const GatedShape& s) { return ceil_div(s.dim, kCL * lane_channels(s)) * s.batch; }
+int64_t blocks_of(const GatedShape& s, int lanes) { return ceil_div(s.dim, lanes * lane_channels(s)) * s.batch; }
+bool narrow(const GatedShape& s) {
+    const int64_t wide = ceil_div(blocks_of(s, kWide), 256), half = ceil_div(blocks_of(s, kNarrow), 256);
+    return half * 23 < wide * 40;  // half the work each, at 1.15 of its cost
+}
 
 // f(type, decay, gate, channels of a lane) with the call's choices as constants.
 template <typename F> void dispatch(const GatedShape& s, bool gate, F f) {
@@ -657,16 +814,32 @@ template <typename F> void dispatch(const GatedShape& s, bool gate, F f) {
 
 template <int MODE> void run_fwd(const GaArgs& a, const GatedShape& s, int segments, hipStream_t st) {
     dispatch(s, MODE == kOut && a.z, [&](auto T, auto decay, auto gate, auto V) {
-        hipLaunchKernelGGL((fwd_kernel<decltype(T), decltype(decay)::value, MODE == kOut && decltype(gate)::value,
-                                       decltype(V)::value, kCL, kNF, MODE>),
-                           dim3(unsigned(blocks_of(s) * segments)), dim3(kWaves * 64), 0, st, a);
+        using E = decltype(T);
+        constexpr bool D = decltype(decay)::value, G = MODE == kOut && decltype(gate)::value;
+        constexpr int C = decltype(V)::value;
+        if constexpr (MODE != kRun)
+            if (segments == 1 && narrow(s)) {
+                hipLaunchKernelGGL((fwd_kernel<E, D, G, C, kNarrow, kNFNarrow, MODE>), dim3(unsigned(blocks_of(s, kNarrow))),
+                                   dim3(kWaves * 64), 0, st, a);
+                return;
+            }
+        hipLaunchKernelGGL((fwd_kernel<E, D, G, C, kWide, kNF, MODE>), dim3(unsigned(blocks_of(s, kWide) * segments)),
+                           dim3(kWaves * 64), 0, st, a);
     });
 }
 template <int MODE> void run_bwd(const GaArgs& a, const GatedShape& s, int segments, hipStream_t st) {
     dispatch(s, a.z, [&](auto T, auto decay, auto gate, auto V) {
-        hipLaunchKernelGGL((bwd_kernel<decltype(T), decltype(decay)::value, decltype(gate)::value, decltype(V)::value,
-                                       kCL, kNB, MODE>),
-                           dim3(unsigned(blocks_of(s) * segments)), dim3(kWaves * 64), 0, st, a);
+        using E = decltype(T);
+        constexpr bool D = decltype(decay)::value, G = decltype(gate)::value;
+        constexpr int C = decltype(V)::value;
+        if constexpr (MODE != kRun)
+            if (segments == 1 && narrow(s)) {
+                hipLaunchKernelGGL((bwd_kernel<E, D, G, C, kNarrow, kNB, MODE>), dim3(unsigned(blocks_of(s, kNarrow))),
+                                   dim3(kWaves * 64), 0, st, a);
+                return;
+            }
+        hipLaunchKernelGGL((bwd_kernel<E, D, G, C, kWide, kNB, MODE>), dim3(unsigned(blocks_of(s, kWide) * segments)),
+                           dim3(kWaves * 64), 0, st, a);
     });
 }
 void run_carry(Stretch* runs, double* enter, const float* first, int64_t rows, int segments, bool against,
@@ -699,22 +872,24 @@ Layout layout_of(const GatedShape& s, const GatedPlan& p, bool backward, bool ck
 }  // namespace
 
 bool gated_plan(const GatedShape& s, int32_t requested, bool backward, GatedPlan* p) {
+    (void)backward;
     *p = GatedPlan{1, s.L};
-    const int64_t tile = backward ? (kTileF > kTileB ? kTileF : kTileB) : kTileF;
-    const int64_t blocks = blocks_of(s);
+    const int64_t blocks = blocks_of(s, kWide);
     int64_t want = requested;
     if (!requested) {
-        // runs where workgroups leave CUs idle, of eight tiles at least
-        want = blocks > 0 ? 512 / blocks : 1;
-        const int64_t most = s.L / (8 * tile);
+        // Runs, which read what the decays hang on twice, where even narrow workgroups
+        // leave CUs idle, of eight tiles at least (bf16 1 x 8192, us with and without:
+        // 2560 channels 89 and 101, gradients 160 and 265; 5120 140 and 139).
+        want = blocks > 0 && blocks < 96 ? 512 / blocks : 1;
+        const int64_t most = s.L / (8 * kTile);
         want = want < most ? want : most;
     }
-    if (want > 1 && s.L > tile) {
-        p->seg_len = ceil_div(ceil_div(s.L, want), tile) * tile;
+    if (want > 1 && s.L > kTile) {
+        p->seg_len = ceil_div(ceil_div(s.L, want), kTile) * kTile;
         p->segments = int32_t(ceil_div(s.L, p->seg_len));
     }
     // a grid has fewer than 2^32 threads
-    return blocks * p->segments <= (int64_t(1) << 22);
+    return blocks_of(s, kNarrow) <= (int64_t(1) << 22) && blocks * p->segments <= (int64_t(1) << 22);
 }
 
 size_t gated_fwd_workspace_bytes(const GatedShape& s, const GatedPlan& p) { return layout_of(s, p, false, false).bytes; }

@@ -29,6 +29,8 @@ SHAPES = [
     (1, 1000, 62),
     (5, 513, 31),
     (1, 2051, 16),
+    (1, 70, 16384),  # channels enough for wide workgroups
+    (1, 200, 8200),
 ]
 
 
