@@ -1,4 +1,15 @@
 // Norms around a block with the residual sum between them, and the gradients.
+//
+// Bound by memory: a row is held in registers, read once and written once. A
+// thread holds vectors of 8 values of a row, `lanes` threads a row: a power of two
+// of a wave's lanes for narrow rows (sums by shuffles, several rows a workgroup),
+// whole waves for wide ones (sums through LDS, one barrier each, as the entries
+// alternate). Workgroups go over their rows with the weights kept in registers and
+// the next row's loads in flight.
+//
+// Statistics in fp32: a mean, then the squares about it. Backward, a workgroup adds
+// what its rows give to the gradients of weights, biases and gate in registers and
+// writes them once; join_kernel adds the workgroups' parts in order.
 #include "../../include/selscan.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -8,151 +19,571 @@ namespace {
 
 struct AnArgs {
     AddnormTensors t;
-    int64_t R, C, per_gate;  // rows of a gate row
+    int64_t R, C, per_gate;  // rows of a gate row (R without a gate)
     int32_t post, pre;
     float eps, scale, res_scale;
+    int32_t lanes;  // threads of a row
+    // backward: workgroups of a gate row (0: a workgroup takes whole gate rows), rows of a workgroup
+    int64_t runs, per;
+    float* part;       // [workgroup][kind of sum][C]
+    float* gate_part;  // [workgroup][C], or dgate itself where a workgroup takes whole gate rows
+    float* averages;   // [R][2], rows of more than 512 threads: what cols_kernel needs of a row
 };
 
-template <typename T> __device__ __forceinline__ float at(const void* p, int64_t i) {
-    return to_f32(static_cast<const T*>(p)[i]);
-}
-template <typename T> __device__ __forceinline__ void put(void* p, int64_t i, float v) {
-    static_cast<T*>(p)[i] = from_f32<T>(v);
-}
+constexpr int kV = 8;  // values of a vector
 
-// Sum over the workgroup's 256 threads, in a fixed order; every thread gets it.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes at any element: rows of a width that is no multiple of 8 begin anywhere
+struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
+
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    u32x4 a, b;
+    __device__ __forceinline__ void get(float (&f)[kV]) const {
 #pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
-    __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
-}
-
-template <typename T, typename S>
-__global__ __launch_bounds__(256) void fwd_kernel(AnArgs a) {
-    __shared__ float red[4];
-    extern __shared__ float row[];
-    const AddnormTensors& t = a.t;
-    for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-        float st[4] = {0.0f, 1.0f, 0.0f, 1.0f};
-        auto stats = [&](int kind, float* mean, float* rstd) {
-            if (kind == SELSCAN_NORM_NONE) return;
-            float s = 0.0f;
-            if (kind == SELSCAN_NORM_LAYER) {
-                for (int64_t c = threadIdx.x; c < a.C; c += 256) s += row[c];
-                *mean = block_sum(s, red) / float(a.C > 0 ? a.C : 1);
-                s = 0.0f;
-            }
-            for (int64_t c = threadIdx.x; c < a.C; c += 256) s += (row[c] - *mean) * (row[c] - *mean);
-            *rstd = 1.0f / sqrtf(block_sum(s, red) / float(a.C > 0 ? a.C : 1) + a.eps);
-        };
-        for (int64_t c = threadIdx.x; c < a.C; c += 256) row[c] = at<T>(t.x, r * a.C + c);
-        stats(a.post, &st[0], &st[1]);
-        for (int64_t c = threadIdx.x; c < a.C; c += 256) {
-            float u = (row[c] - st[0]) * st[1];
-            if (t.post_w) u *= t.post_w[c];
-            if (t.post_b) u += t.post_b[c];
-            u *= a.scale;
-            if (t.gate) u *= t.gate[r / a.per_gate * a.C + c];
-            if (t.res) u = fmaf(a.res_scale, at<S>(t.res, r * a.C + c), u);
-            row[c] = u;
-            if (t.sum) put<S>(t.sum, r * a.C + c, u);
+        for (int i = 0; i < 4; ++i) {
+            f[i] = __uint_as_float(a[i]);
+            f[4 + i] = __uint_as_float(b[i]);
         }
-        stats(a.pre, &st[2], &st[3]);
-        if (t.y)
-            for (int64_t c = threadIdx.x; c < a.C; c += 256) {
-                float u = (row[c] - st[2]) * st[3];
-                if (t.pre_w) u *= t.pre_w[c];
-                if (t.pre_b) u += t.pre_b[c];
-                put<T>(t.y, r * a.C + c, u);
+    }
+};
+template <> struct Vec<bf16_bits> {
+    u32x4 a;
+    __device__ __forceinline__ void get(float (&f)[kV]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(a[i]);
+            f[2 * i + 1] = bf16_hi(a[i]);
+        }
+    }
+};
+
+// n values from p (8, fewer at a row's end, or none); the others are 0.
+template <typename T> __device__ __forceinline__ Vec<T> load(const void* base, int64_t at, int n) {
+    const T* p = static_cast<const T*>(base) + at;
+    Vec<T> v{};
+    if (n == kV) {
+        v.a = reinterpret_cast<const Any16*>(p)->v;
+        if constexpr (sizeof(T) == 4) v.b = reinterpret_cast<const Any16*>(p + 4)->v;
+    } else if (n > 0) {
+        struct Values { T t[kV]; } s{};
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            if (i < n) s.t[i] = p[i];
+        v = __builtin_bit_cast(Vec<T>, s);
+    }
+    return v;
+}
+template <typename T> __device__ __forceinline__ void store(void* base, int64_t at, int n, const float (&f)[kV]) {
+    T* p = static_cast<T*>(base) + at;
+    if (n == kV) {
+        if constexpr (sizeof(T) == 4) {
+            u32x4 a, b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = __float_as_uint(f[i]);
+                b[i] = __float_as_uint(f[4 + i]);
             }
-        if (t.stats && threadIdx.x < 4) t.stats[r * 4 + threadIdx.x] = st[threadIdx.x];
+            reinterpret_cast<Any16*>(p)->v = a;
+            reinterpret_cast<Any16*>(p + 4)->v = b;
+        } else {
+            u32x4 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+            reinterpret_cast<Any16*>(p)->v = a;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            if (i < n) p[i] = from_f32<T>(f[i]);
+    }
+}
+// Weights (n values, the others 0), `dflt` without them.
+__device__ __forceinline__ void weights(const float* w, int64_t at, int n, float dflt, float (&f)[kV]) {
+    if (w) {
+        load<float>(w, at, n).get(f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) f[i] = i < n ? dflt : 0.0f;
     }
 }
 
-template <typename T, typename S>
-__global__ __launch_bounds__(256) void bwd_kernel(AnArgs a, float* ds_out) {
-    __shared__ float red[4];
-    extern __shared__ float row[];
+// A thread's place, and sums over a row: in the lanes of a wave (WIDE false), or over the workgroup.
+template <bool WIDE> struct Row {
+    int l, ri, step, lanes;
+    float (*red)[2][16];
+    int slot = 0;
+    __device__ __forceinline__ Row(int lanes_, float (*red_)[2][16]) : lanes(lanes_), red(red_) {
+        l = WIDE ? threadIdx.x : threadIdx.x % lanes;
+        ri = WIDE ? 0 : threadIdx.x / lanes;
+        step = WIDE ? 1 : 256 / lanes;
+    }
+    __device__ __forceinline__ void sums(float& a, float& b) {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int m = 32; m; m >>= 1) {
+                a += __shfl_xor(a, m, 64);
+                b += __shfl_xor(b, m, 64);
+            }
+            const int waves = blockDim.x / 64;
+            if (threadIdx.x % 64 == 0) {
+                red[slot][0][threadIdx.x / 64] = a;
+                red[slot][1][threadIdx.x / 64] = b;
+            }
+            __syncthreads();
+            a = red[slot][0][0];
+            b = red[slot][1][0];
+            for (int i = 1; i < waves; ++i) {
+                a += red[slot][0][i];
+                b += red[slot][1][i];
+            }
+            // an entry is written again only behind a barrier that follows every read of it
+            slot ^= 1;
+        } else {
+            for (int m = lanes / 2; m; m >>= 1) {
+                a += __shfl_xor(a, m, 64);
+                b += __shfl_xor(b, m, 64);
+            }
+        }
+    }
+    __device__ __forceinline__ float sum(float a) {
+        float b = 0.0f;
+        sums(a, b);
+        return a;
+    }
+};
+
+// mean and 1 / sqrt of a row's values (0 past its end).
+template <int K, bool WIDE>
+__device__ __forceinline__ void statistics(int kind, const float (&v)[K][kV], const int (&n)[K], float inv, float eps,
+                                           Row<WIDE>& row, float* mean, float* rstd) {
+    *mean = 0.0f;
+    float s = 0.0f;
+    if (kind == SELSCAN_NORM_LAYER) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < kV; ++i) s += v[k][i];
+        *mean = row.sum(s) * inv;
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const float d = i < n[k] ? v[k][i] - *mean : 0.0f;
+                s = fmaf(d, d, s);
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < kV; ++i) s = fmaf(v[k][i], v[k][i], s);
+    }
+    *rstd = 1.0f / sqrtf(row.sum(s) * inv + eps);
+}
+
+// KEEP: weights and the next row's loads stay in registers, which takes at most 512 threads a row.
+template <typename T, typename S, int K, bool WIDE, bool KEEP>
+__global__ __launch_bounds__(!WIDE ? 256 : KEEP ? 512 : 1024) void fwd_kernel(AnArgs a) {
+    __shared__ float red[2][2][16];
+    Row<WIDE> row(a.lanes, red);
     const AddnormTensors& t = a.t;
-    for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-        const float* st = t.stats + r * 4;
-        const int64_t o = r * a.C;
-        float m1 = 0.0f, m2 = 0.0f;
-        auto e_of = [&](int64_t c) { return at<T>(t.dy, o + c) * (t.pre_w ? t.pre_w[c] : 1.0f); };
-        auto xh_of = [&](int64_t c) { return (at<S>(t.sum, o + c) - st[2]) * st[3]; };
-        if (a.pre != SELSCAN_NORM_NONE) {
-            for (int64_t c = threadIdx.x; c < a.C; c += 256) {
-                m1 += e_of(c);
-                m2 += e_of(c) * xh_of(c);
+    const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
+    int n[K];
+    float w1[KEEP ? K : 1][kV], w2[KEEP ? K : 1][kV];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t c = int64_t(row.l + a.lanes * k) * kV, left = a.C - c;
+        n[k] = left < 0 ? 0 : left < kV ? int(left) : kV;
+        if constexpr (KEEP) {
+            weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w1[k]);
+            weights(pre ? t.pre_w : nullptr, c, n[k], 1.0f, w2[k]);
+        }
+    }
+    const float inv = 1.0f / float(a.C > 0 ? a.C : 1);
+    Vec<T> nx[K];
+    Vec<S> ns[K];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
+            nx[k] = load<T>(t.x, at, n[k]);
+            if (t.res) ns[k] = load<S>(t.res, at, n[k]);
+        }
+    };
+    const int64_t stride = int64_t(gridDim.x) * row.step;
+    int64_t r = int64_t(blockIdx.x) * row.step + row.ri;
+    if (KEEP && r < a.R) fetch(r);
+    for (; r < a.R; r += stride) {
+        float v[K][kV], s[K][kV];
+        if (!KEEP) fetch(r);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            nx[k].get(v[k]);
+#pragma unroll
+            for (int i = 0; i < kV; ++i) s[k][i] = 0.0f;
+            if (t.res) {
+                ns[k].get(s[k]);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) s[k][i] *= a.res_scale;
             }
-            m1 = a.pre == SELSCAN_NORM_LAYER ? block_sum(m1, red) / float(a.C) : 0.0f;
-            m2 = block_sum(m2, red) / float(a.C);
         }
-        for (int64_t c = threadIdx.x; c < a.C; c += 256) {
-            float ds = t.dsum ? at<S>(t.dsum, o + c) : 0.0f;
-            if (a.pre != SELSCAN_NORM_NONE) ds += st[3] * (e_of(c) - m1 - xh_of(c) * m2);
-            row[c] = ds;
-        }
-        m1 = m2 = 0.0f;
-        auto f_of = [&](int64_t c) {
-            return row[c] * a.scale * (t.gate ? t.gate[r / a.per_gate * a.C + c] : 1.0f) * (t.post_w ? t.post_w[c] : 1.0f);
-        };
-        auto x_of = [&](int64_t c) { return (at<T>(t.x, o + c) - st[0]) * st[1]; };
-        if (a.post != SELSCAN_NORM_NONE) {
-            for (int64_t c = threadIdx.x; c < a.C; c += 256) {
-                m1 += f_of(c);
-                m2 += f_of(c) * x_of(c);
+        if (KEEP && r + stride < a.R) fetch(r + stride);
+        float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f;
+        if (post) statistics<K, WIDE>(a.post, v, n, inv, a.eps, row, &m1, &r1);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t c = int64_t(row.l + a.lanes * k) * kV;
+            float g[kV], b[kV];
+            weights(t.gate ? t.gate + r / a.per_gate * a.C : nullptr, c, n[k], 1.0f, g);
+            weights(post ? t.post_b : nullptr, c, n[k], 0.0f, b);
+            float (&w)[kV] = w1[KEEP ? k : 0];
+            if constexpr (!KEEP) weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w);
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const float u = post ? fmaf((v[k][i] - m1) * r1, w[i], b[i]) : v[k][i];
+                s[k][i] = fmaf(u, a.scale * g[i], s[k][i]);
             }
-            m1 = a.post == SELSCAN_NORM_LAYER ? block_sum(m1, red) / float(a.C) : 0.0f;
-            m2 = block_sum(m2, red) / float(a.C);
+            if (t.sum) store<S>(t.sum, r * a.C + c, n[k], s[k]);
         }
-        for (int64_t c = threadIdx.x; c < a.C; c += 256) {
-            if (ds_out) ds_out[o + c] = row[c];
+        if (pre) {
+            statistics<K, WIDE>(a.pre, s, n, inv, a.eps, row, &m2, &r2);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int64_t c = int64_t(row.l + a.lanes * k) * kV;
+                float y[kV], b[kV];
+                weights(t.pre_b, c, n[k], 0.0f, b);
+                float (&w)[kV] = w2[KEEP ? k : 0];
+                if constexpr (!KEEP) weights(t.pre_w, c, n[k], 1.0f, w);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) y[i] = fmaf((s[k][i] - m2) * r2, w[i], b[i]);
+                if (t.y) store<T>(t.y, r * a.C + c, n[k], y);
+            }
+        }
+        if (t.stats && row.l == 0) {
+            const float st[4] = {m1, r1, m2, r2};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t.stats[r * 4 + i] = st[i];
+        }
+    }
+}
+
+// The sums that the backward pass forms over rows, by what is wanted of them: weights (0, 1), biases (2, 3).
+enum { kPreW = 0, kPostW = 1, kPreB = 2, kPostB = 3 };
+
+// SUMS false (rows of more than 512 threads, whose registers the sums would not fit): the rows alone, and their
+// averages for cols_kernel.
+template <typename T, typename S, int K, bool WIDE, bool BIAS, bool GATE, bool SUMS>
+__global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(AnArgs a) {
+    __shared__ float red[2][2][16];
+    __shared__ float cols[WIDE ? 1 : 256 * kV];
+    Row<WIDE> row(a.lanes, red);
+    const AddnormTensors& t = a.t;
+    const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
+    const bool use_x = post || (SUMS && GATE && t.dgate);
+    constexpr int NS = BIAS ? 4 : 2, KW = SUMS ? K : 1;
+    int n[K];
+    float w1[KW][kV], w2[KW][kV], acc[NS][KW][kV], accg[GATE ? KW : 1][kV];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t c = int64_t(row.l + a.lanes * k) * kV, left = a.C - c;
+        n[k] = left < 0 ? 0 : left < kV ? int(left) : kV;
+        if constexpr (SUMS) {
+            weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w1[k]);
+            weights(pre ? t.pre_w : nullptr, c, n[k], 1.0f, w2[k]);
+        }
+        if constexpr (SUMS)
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < kV; ++i) acc[j][k][i] = 0.0f;
+    }
+    const float inv = 1.0f / float(a.C);
+    // The thread's sums of its columns joined over the workgroup's rows and written to out[0 .. C).
+    auto flush = [&](const float (&f)[KW][kV], float* out) {
+        if constexpr (!WIDE) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kV; ++i) cols[(row.ri * a.lanes + row.l) * kV + i] = f[0][i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.C; c += 256) {
+                float s = cols[c];
+                for (int j = 1; j < row.step; ++j) s += cols[j * a.lanes * kV + c];
+                out[c] = s;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < KW; ++k) store<float>(out, int64_t(row.l + a.lanes * k) * kV, n[k], f[k]);
+        }
+    };
+    // Rows r0 .. r1 of the workgroup, one gate row's at a time.
+    int64_t r0, r1;
+    if (a.runs) {
+        const int64_t g = blockIdx.x / a.runs;
+        r0 = g * a.per_gate + blockIdx.x % a.runs * a.per;
+        const int64_t e = (g + 1) * a.per_gate;
+        r1 = r0 + a.per < e ? r0 + a.per : e;
+    } else {
+        r0 = blockIdx.x * a.per;
+        r1 = r0 + a.per < a.R ? r0 + a.per : a.R;
+    }
+    Vec<T> nx[K], ny[K];
+    Vec<S> ns[K], nd[K];
+    float nst[4] = {0.0f, 1.0f, 0.0f, 1.0f};
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
+            if (use_x) nx[k] = load<T>(t.x, at, n[k]);
+            if (pre) {
+                ns[k] = load<S>(t.sum, at, n[k]);
+                ny[k] = load<T>(t.dy, at, n[k]);
+            }
+            if (t.dsum) nd[k] = load<S>(t.dsum, at, n[k]);
+        }
+        if (t.stats)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nst[i] = t.stats[r * 4 + i];
+    };
+    for (int64_t g0 = r0; g0 < r1;) {
+        const int64_t gi = g0 / a.per_gate, end = (gi + 1) * a.per_gate, g1 = end < r1 ? end : r1;
+        float gate[GATE ? KW : 1][kV];
+        if constexpr (GATE && SUMS)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                weights(t.gate ? t.gate + gi * a.C : nullptr, int64_t(row.l + a.lanes * k) * kV, n[k], 1.0f, gate[k]);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) accg[k][i] = 0.0f;
+            }
+        int64_t r = g0 + row.ri;
+        if (SUMS && r < g1) fetch(r);
+        for (; r < g1; r += row.step) {
+            if (!SUMS) fetch(r);
+            float ds[K][kV], xh[K][kV], e[K][kV], x1[K][kV];
+            const float m1 = nst[0], q1 = nst[1], m2 = nst[2], q2 = nst[3];
+            float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int i = 0; i < kV; ++i) ds[k][i] = x1[k][i] = 0.0f;
+                if (t.dsum) nd[k].get(ds[k]);
+                if (use_x) {
+                    nx[k].get(x1[k]);
+                    if (post)
+#pragma unroll
+                        for (int i = 0; i < kV; ++i) x1[k][i] = i < n[k] ? (x1[k][i] - m1) * q1 : 0.0f;
+                }
+                if (pre) {
+                    float dy[kV];
+                    ns[k].get(xh[k]);
+                    ny[k].get(dy);
+                    float (&w)[kV] = w2[SUMS ? k : 0];
+                    if constexpr (!SUMS) weights(t.pre_w, int64_t(row.l + a.lanes * k) * kV, n[k], 1.0f, w);
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) {
+                        xh[k][i] = i < n[k] ? (xh[k][i] - m2) * q2 : 0.0f;
+                        e[k][i] = dy[i] * w[i];
+                        s1 += e[k][i];
+                        s2 = fmaf(e[k][i], xh[k][i], s2);
+                        if constexpr (SUMS) acc[kPreW][k][i] = fmaf(dy[i], xh[k][i], acc[kPreW][k][i]);
+                        if constexpr (SUMS && BIAS) acc[kPreB][k][i] += dy[i];
+                    }
+                }
+            }
+            if (SUMS && r + row.step < g1) fetch(r + row.step);
+            if (pre) {
+                row.sums(s1, s2);
+                const float a1 = a.pre == SELSCAN_NORM_LAYER ? s1 * inv : 0.0f, a2 = s2 * inv;
+                if (!SUMS && a.averages && row.l == 0) {
+                    a.averages[r * 2] = a1;
+                    a.averages[r * 2 + 1] = a2;
+                }
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) ds[k][i] = fmaf(q2, e[k][i] - a1 - xh[k][i] * a2, ds[k][i]);
+            }
+            s1 = s2 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
+                if (t.dres) {
+                    float o[kV];
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) o[i] = a.res_scale * ds[k][i];
+                    store<S>(t.dres, at, n[k], o);
+                }
+                const int64_t c = int64_t(row.l + a.lanes * k) * kV;
+                float b1[kV];
+                if constexpr (GATE && SUMS) weights(post ? t.post_b : nullptr, c, n[k], 0.0f, b1);
+                float (&w)[kV] = w1[SUMS ? k : 0];
+                float (&gt)[kV] = gate[GATE && SUMS ? k : 0];
+                if constexpr (!SUMS) {
+                    weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w);
+                    if constexpr (GATE) weights(t.gate + gi * a.C, c, n[k], 1.0f, gt);
+                }
+#pragma unroll
+                for (int i = 0; i < kV; ++i) {
+                    float du = a.scale * ds[k][i];
+                    if constexpr (GATE) {
+                        if constexpr (SUMS) accg[k][i] = fmaf(du, fmaf(x1[k][i], w[i], b1[i]), accg[k][i]);
+                        du *= gt[i];
+                    }
+                    if (post) {
+                        if constexpr (SUMS) acc[kPostW][k][i] = fmaf(du, x1[k][i], acc[kPostW][k][i]);
+                        if constexpr (SUMS && BIAS) acc[kPostB][k][i] += du;
+                        du *= w[i];
+                        s1 += du;
+                        s2 = fmaf(du, x1[k][i], s2);
+                    }
+                    ds[k][i] = du;
+                }
+            }
+            if (post) {
+                row.sums(s1, s2);
+                const float a1 = a.post == SELSCAN_NORM_LAYER ? s1 * inv : 0.0f, a2 = s2 * inv;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) ds[k][i] = q1 * (ds[k][i] - a1 - x1[k][i] * a2);
+            }
             if (t.dx)
-                put<T>(t.dx, o + c, a.post != SELSCAN_NORM_NONE ? st[1] * (f_of(c) - m1 - x_of(c) * m2) : f_of(c));
-            if (t.dres) put<S>(t.dres, o + c, a.res_scale * row[c]);
+#pragma unroll
+                for (int k = 0; k < K; ++k) store<T>(t.dx, r * a.C + int64_t(row.l + a.lanes * k) * kV, n[k], ds[k]);
+        }
+        if constexpr (GATE && SUMS)
+            if (t.dgate) flush(accg, a.gate_part + (a.runs ? int64_t(blockIdx.x) : gi) * a.C);
+        g0 = g1;
+    }
+    if constexpr (SUMS) {
+        if (!a.part) return;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            float* want = j == kPreW ? t.dpre_w : j == kPostW ? t.dpost_w : j == kPreB ? t.dpre_b : t.dpost_b;
+            if (want) flush(acc[j], a.part + (int64_t(blockIdx.x) * NS + j) * a.C);
         }
     }
 }
 
-// Column sums, one thread a column of a gate's rows.
+// The sums over rows where bwd_kernel does not form them: a thread takes a vector of columns down the rows of its
+// workgroup (grid y), from the averages that bwd_kernel left.
 template <typename T, typename S>
-__global__ __launch_bounds__(64) void cols_kernel(AnArgs a, const float* ds, int gates, int mode) {
+__global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
     const AddnormTensors& t = a.t;
-    const int64_t c = int64_t(blockIdx.x) * 64 + threadIdx.x;
-    if (c >= a.C) return;
-    double s[5] = {};
-    for (int64_t r = 0; r < a.R; ++r) {
-        if (mode && r % a.per_gate == 0) s[4] = 0.0;
-        const int64_t i = r * a.C + c;
-        const float* st = t.stats + r * 4;
-        const float g = t.gate ? t.gate[r / a.per_gate * a.C + c] : 1.0f;
-        if (t.dpre_w || t.dpre_b) {
-            const float dy = at<T>(t.dy, i);
-            s[0] += dy * ((at<S>(t.sum, i) - st[2]) * st[3]);
-            s[1] += dy;
+    const int64_t c = (int64_t(blockIdx.x) * 64 + threadIdx.x) * kV, blk = blockIdx.y;
+    const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
+    const bool use_x = post || t.dgate;
+    const int n = a.C - c < 0 ? 0 : a.C - c < kV ? int(a.C - c) : kV;
+    if (n == 0) return;
+    int64_t r0, r1;
+    if (a.runs) {
+        const int64_t g = blk / a.runs, e = (g + 1) * a.per_gate;
+        r0 = g * a.per_gate + blk % a.runs * a.per;
+        r1 = r0 + a.per < e ? r0 + a.per : e;
+    } else {
+        r0 = blk * a.per;
+        r1 = r0 + a.per < a.R ? r0 + a.per : a.R;
+    }
+    float w1[kV], b1[kV], w2[kV], gate[kV], acc[5][kV];
+    weights(post ? t.post_w : nullptr, c, n, 1.0f, w1);
+    weights(post ? t.post_b : nullptr, c, n, 0.0f, b1);
+    weights(pre ? t.pre_w : nullptr, c, n, 1.0f, w2);
+    weights(nullptr, c, n, 1.0f, gate);
+#pragma unroll
+    for (int j = 0; j < 5; ++j)
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[j][i] = 0.0f;
+    for (int64_t r = r0; r < r1; ++r) {
+        const int64_t at = r * a.C + c, gi = r / a.per_gate;
+        if (t.gate && (r == r0 || r % a.per_gate == 0)) weights(t.gate + gi * a.C, c, n, 1.0f, gate);
+        float st[4] = {0.0f, 1.0f, 0.0f, 1.0f}, x[kV] = {}, s[kV], dy[kV], ds[kV] = {};
+        if (t.stats)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st[i] = t.stats[r * 4 + i];
+        if (use_x) load<T>(t.x, at, n).get(x);
+        if (t.dsum) load<S>(t.dsum, at, n).get(ds);
+        if (pre) {
+            load<S>(t.sum, at, n).get(s);
+            load<T>(t.dy, at, n).get(dy);
+            const float a1 = a.averages[r * 2], a2 = a.averages[r * 2 + 1];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const float xh = (s[i] - st[2]) * st[3];
+                acc[kPreW][i] = fmaf(dy[i], xh, acc[kPreW][i]);
+                acc[kPreB][i] += dy[i];
+                ds[i] = fmaf(st[3], dy[i] * w2[i] - a1 - xh * a2, ds[i]);
+            }
         }
-        const bool post = a.post != SELSCAN_NORM_NONE;
-        const float du = a.scale * g * ds[i], xh = t.x ? (post ? (at<T>(t.x, i) - st[0]) * st[1] : at<T>(t.x, i)) : 0.0f;
-        s[2] += du * xh;
-        s[3] += du;
-        if (mode) {
-            const float u = fmaf(xh, t.post_w ? t.post_w[c] : 1.0f, t.post_b ? t.post_b[c] : 0.0f);
-            s[4] += a.scale * u * ds[i];
-            if (r % a.per_gate == a.per_gate - 1) t.dgate[r / a.per_gate * a.C + c] = float(s[4]);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const float du = a.scale * ds[i], xh = post ? (x[i] - st[0]) * st[1] : x[i];
+            acc[4][i] = fmaf(du, fmaf(xh, w1[i], b1[i]), acc[4][i]);
+            acc[kPostW][i] = fmaf(du * gate[i], xh, acc[kPostW][i]);
+            acc[kPostB][i] = fmaf(du, gate[i], acc[kPostB][i]);
+        }
+        if (t.dgate && (r + 1 == r1 || (r + 1) % a.per_gate == 0)) {
+            store<float>(a.gate_part + (a.runs ? blk : gi) * a.C, c, n, acc[4]);
+#pragma unroll
+            for (int i = 0; i < kV; ++i) acc[4][i] = 0.0f;
         }
     }
-    if (t.dpre_w) t.dpre_w[c] = float(s[0]);
-    if (t.dpre_b) t.dpre_b[c] = float(s[1]);
-    if (t.dpost_w) t.dpost_w[c] = float(s[2]);
-    if (t.dpost_b) t.dpost_b[c] = float(s[3]);
+    if (!a.part) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float* want = j == kPreW ? t.dpre_w : j == kPostW ? t.dpost_w : j == kPreB ? t.dpre_b : t.dpost_b;
+        if (want) store<float>(a.part + (blk * NS + j) * a.C, c, n, acc[j]);
+    }
+}
+
+// Sums of columns over parts that lie `pitch` apart: 64 columns a workgroup, 16 interleaved runs of parts joined in
+// order. Grid y: which sum (its first part, `apart` behind the one before), z: which stretch of `count` parts.
+struct JoinArgs {
+    const float* part;
+    int64_t pitch, apart, C;
+    int32_t count, total;  // parts of a stretch, and of all
+    float* out[4];         // of each sum, null: not wanted; stretch z at out + z * step
+    int64_t step;
+};
+__global__ __launch_bounds__(1024) void join_kernel(JoinArgs a) {
+    __shared__ float red[16][64];
+    const int col = threadIdx.x % 64, r = threadIdx.x / 64;
+    const int64_t c = int64_t(blockIdx.x) * 64 + col, z = blockIdx.z;
+    float* out = a.out[blockIdx.y];
+    if (!out) return;
+    const int64_t p0 = z * a.count, p1 = p0 + a.count < a.total ? p0 + a.count : a.total;
+    float s = 0.0f;
+    if (c < a.C)
+#pragma unroll 4
+        for (int64_t p = p0 + r; p < p1; p += 16) s += a.part[p * a.pitch + blockIdx.y * a.apart + c];
+    red[r][col] = s;
+    __syncthreads();
+    if (r == 0 && c < a.C) {
+#pragma unroll
+        for (int k = 1; k < 16; ++k) s += red[k][col];
+        out[z * a.step + c] = s;
+    }
+}
+
+// ---- the split of a call -----------------------------------------------------------
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Threads of a row: K vectors each; a power of two up to a wave, then whole waves.
+int lanes_of(int64_t C, int K) {
+    const int64_t v = ceil_div(C, int64_t(kV) * K);
+    if (v > 64) return int(ceil_div(v, 64) * 64);
+    int n = 1;
+    while (n < v) n *= 2;
+    return n;
 }
 
 AnArgs args_of(const AddnormTensors& t, const AddnormShape& s) {
-    return AnArgs{t, s.R, s.C, s.G ? s.R / s.G : 1, s.post, s.pre, s.eps, s.scale, s.res_scale};
+    AnArgs a{};
+    a.t = t;
+    a.R = s.R; a.C = s.C; a.per_gate = s.G ? s.R / s.G : s.R > 0 ? s.R : 1;
+    a.post = s.post; a.pre = s.pre; a.eps = s.eps; a.scale = s.scale; a.res_scale = s.res_scale;
+    return a;
 }
 
 // f(type, residual's type)
@@ -162,33 +593,136 @@ template <typename F> void dispatch(const AddnormShape& s, F f) {
     else f(bf16_bits{}, bf16_bits{});
 }
 
-bool any_sum(const AddnormTensors& t) { return t.dpost_w || t.dpost_b || t.dpre_w || t.dpre_b || t.dgate; }
+// The backward's workgroups: their rows, and where their sums go.
+struct BwdPlan {
+    int K, lanes, sums;
+    bool wide, apart;  // apart: the sums in a launch of their own
+    int64_t runs, per, blocks;
+    size_t part, part2, gate, averages, bytes;  // places in the workspace
+};
+constexpr int kJoin = 512;
+bool row_sums(const AddnormTensors& w) { return w.dpre_w || w.dpost_w || w.dpre_b || w.dpost_b; }
+
+BwdPlan bwd_plan(const AddnormShape& s, const AddnormTensors& w) {
+    BwdPlan p{};
+    p.K = s.C <= 4096 ? 1 : 2;
+    p.lanes = lanes_of(s.C, p.K);
+    p.wide = p.lanes > 64;
+    p.apart = p.lanes > 512;
+    const int64_t step = p.wide ? 1 : 256 / p.lanes, groups = s.G ? s.G : 1, rows = s.R / groups;
+    // workgroups for 512 threads a CU
+    const int64_t want = 256 * (p.wide ? ceil_div(512, p.lanes) : 4);
+    if (w.dgate && groups >= want) {  // whole gate rows, whose sums are then done
+        p.per = ceil_div(groups, want) * rows;
+        p.blocks = ceil_div(s.R, p.per);
+    } else {  // runs of a gate row's rows; of all rows where the gate's gradient is not wanted
+        const int64_t of = w.dgate ? rows : s.R, g = w.dgate ? groups : 1;
+        p.per = ceil_div(ceil_div(of, ceil_div(want, g)), step) * step;
+        p.blocks = ceil_div(of, p.per) * g;
+        p.runs = w.dgate ? ceil_div(of, p.per) : 0;
+    }
+    p.sums = w.dpre_b || w.dpost_b ? 4 : 2;
+    size_t at = 0;
+    if (row_sums(w)) {
+        at += up256(size_t(p.blocks) * p.sums * s.C * sizeof(float));
+        p.part2 = at;
+        if (p.blocks > kJoin) at += up256(size_t(ceil_div(p.blocks, kJoin)) * p.sums * s.C * sizeof(float));
+    }
+    p.gate = at;
+    if (w.dgate && p.runs) at += up256(size_t(p.blocks) * s.C * sizeof(float));
+    p.averages = at;
+    if (p.apart && (row_sums(w) || w.dgate)) at += up256(size_t(s.R) * 2 * sizeof(float));
+    p.bytes = at;
+    return p;
+}
 
 }  // namespace
 
 size_t addnorm_bwd_workspace_bytes(const AddnormShape& s, const AddnormTensors& wanted) {
-    return any_sum(wanted) ? size_t(s.R) * s.C * sizeof(float) : 0;
+    return bwd_plan(s, wanted).bytes;
 }
 
 hipError_t launch_addnorm(const AddnormTensors& t, const AddnormShape& s, hipStream_t stream) {
-    const AnArgs a = args_of(t, s);
+    AnArgs a = args_of(t, s);
+    const int K = s.C <= 4096 ? 1 : 2;
+    a.lanes = lanes_of(s.C, K);
+    const bool wide = a.lanes > 64;
+    const int threads = wide ? a.lanes : 256, step = wide ? 1 : 256 / a.lanes;
+    const int64_t blocks = ceil_div(s.R, step), most = int64_t(256) * 2048 / threads;
+    const dim3 grid(unsigned(blocks < most ? blocks : most)), block{unsigned(threads)};
     dispatch(s, [&](auto T, auto S) {
-        hipLaunchKernelGGL((fwd_kernel<decltype(T), decltype(S)>), dim3(unsigned(s.R < 1 << 16 ? s.R : 1 << 16)),
-                           dim3(256), unsigned(s.C * 4), stream, a);
+        using X = decltype(T);
+        using Y = decltype(S);
+        if (!wide) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, false, true>), grid, block, 0, stream, a);
+        else if (K == 1) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, true, true>), grid, block, 0, stream, a);
+        else if (a.lanes <= 512) hipLaunchKernelGGL((fwd_kernel<X, Y, 2, true, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((fwd_kernel<X, Y, 2, true, false>), grid, block, 0, stream, a);
     });
     return hipGetLastError();
 }
 
 hipError_t launch_addnorm_bwd(const AddnormTensors& t, const AddnormShape& s, void* workspace, hipStream_t stream) {
-    const AnArgs a = args_of(t, s);
-    float* ds = any_sum(t) ? static_cast<float*>(workspace) : nullptr;
+    AnArgs a = args_of(t, s);
+    const BwdPlan p = bwd_plan(s, t);
+    char* ws = static_cast<char*>(workspace);
+    const bool sums = row_sums(t);
+    a.lanes = p.lanes; a.runs = p.runs; a.per = p.per;
+    a.part = sums ? reinterpret_cast<float*>(ws) : nullptr;
+    a.gate_part = p.runs ? reinterpret_cast<float*>(ws + p.gate) : t.dgate;
+    a.averages = p.apart && (sums || t.dgate) ? reinterpret_cast<float*>(ws + p.averages) : nullptr;
+    const dim3 grid(unsigned(p.blocks)), block(unsigned(p.wide ? p.lanes : 256));
     dispatch(s, [&](auto T, auto S) {
-        hipLaunchKernelGGL((bwd_kernel<decltype(T), decltype(S)>), dim3(unsigned(s.R < 1 << 16 ? s.R : 1 << 16)),
-                           dim3(256), unsigned(s.C * 4), stream, a, ds);
-        if (ds)
-            hipLaunchKernelGGL((cols_kernel<decltype(T), decltype(S)>), dim3(unsigned((s.C + 63) / 64)), dim3(64), 0,
-                               stream, a, ds, int(s.G), t.dgate ? 1 : 0);
+        auto with = [&](auto bias, auto gate) {
+            using X = decltype(T);
+            using Y = decltype(S);
+            constexpr bool B = decltype(bias)::value, G = decltype(gate)::value;
+            if (!p.wide) hipLaunchKernelGGL((bwd_kernel<X, Y, 1, false, B, G, true>), grid, block, 0, stream, a);
+            else if (p.K == 1) hipLaunchKernelGGL((bwd_kernel<X, Y, 1, true, B, G, true>), grid, block, 0, stream, a);
+            else if (!p.apart) hipLaunchKernelGGL((bwd_kernel<X, Y, 2, true, B, G, true>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((bwd_kernel<X, Y, 2, true, false, G, false>), grid, block, 0, stream, a);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        if (p.sums == 4) {
+            if (t.gate) with(yes, yes);
+            else with(yes, no);
+        } else {
+            if (t.gate) with(no, yes);
+            else with(no, no);
+        }
+        if (a.averages)
+            hipLaunchKernelGGL((cols_kernel<decltype(T), decltype(S)>),
+                               dim3(unsigned(ceil_div(s.C, 64 * kV)), unsigned(p.blocks)), dim3(64), 0, stream, a, p.sums);
     });
+    const unsigned cols = unsigned(ceil_div(s.C, 64));
+    if (sums) {
+        float* const outs[4] = {t.dpre_w, t.dpost_w, t.dpre_b, t.dpost_b};
+        JoinArgs j{};
+        j.part = a.part;
+        j.pitch = int64_t(p.sums) * s.C; j.apart = s.C; j.C = s.C;
+        j.count = j.total = int32_t(p.blocks);
+        if (p.blocks > kJoin) {  // in two stages
+            float* mid = reinterpret_cast<float*>(ws + p.part2);
+            const int64_t stretches = ceil_div(p.blocks, kJoin);
+            j.count = kJoin;
+            j.step = j.pitch;
+            for (int i = 0; i < p.sums; ++i) j.out[i] = outs[i] ? mid + i * s.C : nullptr;
+            hipLaunchKernelGGL(join_kernel, dim3(cols, unsigned(p.sums), unsigned(stretches)), dim3(1024), 0, stream, j);
+            j.part = mid;
+            j.count = j.total = int32_t(stretches);
+        }
+        for (int i = 0; i < p.sums; ++i) j.out[i] = outs[i];
+        hipLaunchKernelGGL(join_kernel, dim3(cols, unsigned(p.sums)), dim3(1024), 0, stream, j);
+    }
+    if (t.dgate && p.runs) {
+        JoinArgs j{};
+        j.part = a.gate_part;
+        j.pitch = s.C; j.C = s.C;
+        j.count = int32_t(p.runs); j.total = int32_t(p.blocks);
+        j.out[0] = t.dgate;
+        j.step = s.C;
+        hipLaunchKernelGGL(join_kernel, dim3(cols, 1, unsigned(s.G)), dim3(1024), 0, stream, j);
+    }
     return hipGetLastError();
 }
 
