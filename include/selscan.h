@@ -941,7 +941,7 @@ int selscan_addnorm_bwd_workspace_size(const selscan_addnorm_dims_t* dims,
  *               context where that is wanted
  *   positions : [B, L] int32 or NULL
  * dims: 0 < rot <= W <= 4096, rot even (else SELSCAN_ERR_DSTATE); L < 2^27; B L
- * (H + Hkv) < 2^38; -2^31 < offset < 2^31; scale finite, 0 means 1. The angle
+ * (H + Hkv) < 2^38; (H + Hkv) W <= 2^22; -2^31 < offset < 2^31; scale finite, 0 means 1. The angle
  * is formed in 64 bits and its whole turns taken off, so that far positions
  * keep fp32 accuracy. q_out may be q itself and k_out k; otherwise outputs must
  * not overlap inputs or each other. No workspace. Deterministic.

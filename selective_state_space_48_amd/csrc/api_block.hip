@@ -329,10 +329,11 @@ int selscan_rotary(const void* q, const void* k, const float* inv_freq, const in
     if (!known_dtype(d->dtype)) return SELSCAN_ERR_DTYPE;
     if (d->rot < 1 || d->rot % 2 || d->rot > d->width || d->width > 4096) return SELSCAN_ERR_DSTATE;
     int64_t tokens, th;
-    const int64_t most = int64_t(1) << 38;
+    const int64_t most = int64_t(1) << 38;  // (heads up to 2^38 by a width up to 2^12 stay in 64 bits)
     if (d->heads >= most || d->kv_heads >= most || !mul_ok(d->batch, d->seqlen, &tokens) || tokens >= most ||
         !mul_ok(tokens, d->heads + d->kv_heads, &th) || th >= most)
         return SELSCAN_ERR_DIMS;
+    if ((d->heads + d->kv_heads) * d->width > (int64_t(1) << 22)) return SELSCAN_ERR_DIMS;
     if (d->offset <= -(int64_t(1) << 31) || d->offset >= (int64_t(1) << 31)) return SELSCAN_ERR_DIMS;
     if ((d->layout != SELSCAN_ROTARY_HALF && d->layout != SELSCAN_ROTARY_INTERLEAVED) || !finite_f32(d->scale))
         return SELSCAN_ERR_CONFIG;

@@ -289,6 +289,7 @@ def test_rotary_refusals():
     assert rotary(ro(seqlen=1 << 27)) == S.ERR_DIMS
     assert rotary(ro(batch=1 << 40)) == S.ERR_DIMS
     assert rotary(ro(heads=1 << 62, kv_heads=1 << 62)) == S.ERR_DIMS
+    assert rotary(ro(heads=(1 << 16) - 1, kv_heads=2)) == S.ERR_DIMS
     assert rotary(ro(dtype=9)) == S.ERR_DTYPE
     for rot, width in ((0, 64), (-2, 64), (3, 64), (66, 64), (64, 4097)):
         assert rotary(ro(rot=rot, width=width)) == S.ERR_DSTATE, (rot, width)
