@@ -156,12 +156,13 @@ template <typename T, int V, int CL, int N> struct Place {
     int64_t d0, d, b;  // the workgroup's first channel, the lane's, the entry
     bool live;
     uint32_t off;      // bytes from the wave's first value in a tile to the lane's
-    __device__ __forceinline__ Place(int64_t block, int64_t D) {
+    __device__ __forceinline__ Place(int64_t block, int64_t D) : Place(uint32_t(block), D, uint32_t((D + kChan - 1) / kChan)) {}
+    // (fewer than 2^32 workgroups; 32-bit divisions)
+    __device__ __forceinline__ Place(uint32_t block, int64_t D, uint32_t blocks) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
         c = threadIdx.x % CL;
         tg = threadIdx.x % 64 / CL;
-        const int64_t blocks = (D + kChan - 1) / kChan;
-        d0 = block % blocks * kChan;
+        d0 = int64_t(block % blocks) * kChan;
         d = d0 + c * V;
         b = block / blocks;
         live = d < D;
@@ -198,32 +199,34 @@ template <int CL> __device__ __forceinline__ Stretch after_in_wave(Stretch& own,
     return tg + 1 < n ? next : Stretch{1.0, 0.0};
 }
 
-// A pointer that the whole wave shares, kept in scalar registers: rows then cost no vector additions (the compiler
-// adds the lane's offset first, and then to every row in 64 bits).
-template <typename P> __device__ __forceinline__ P* uniform(P* p) {
-    asm("" : "+s"(p));
-    return p;
+// Global memory at a pointer that the whole wave shares, kept in scalar registers: rows then cost no vector additions
+// (the compiler adds the lane's offset first, and then to every row in 64 bits).
+#define SELSCAN_GLOBAL __attribute__((address_space(1)))
+__device__ __forceinline__ SELSCAN_GLOBAL char* uniform(const void* p, int64_t bytes) {
+    SELSCAN_GLOBAL char* q = (SELSCAN_GLOBAL char*)(static_cast<char*>(const_cast<void*>(p)) + bytes);
+    asm("" : "+s"(q));
+    return q;
 }
 
 // The lane's N tokens of one tensor, `base` the wave's first value; tokens past `left` (the last that exists)
 // taken from it. `row`: bytes of a row.
 template <typename T, int V, int N>
 __device__ __forceinline__ void fetch(const void* p, int64_t base, uint32_t off, int64_t row, raw_t<T, V> (&r)[N]) {
-    const char* q = reinterpret_cast<const char*>(static_cast<const T*>(p) + base);
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const raw_t<T, V>*>(uniform(q + i * row) + off);
+    for (int i = 0; i < N; ++i)
+        r[i] = *(const SELSCAN_GLOBAL raw_t<T, V>*)(uniform(p, base * int64_t(sizeof(T)) + i * row) + off);
 }
 template <typename T, int V, int N>
 __device__ __forceinline__ void fetch_some(const void* p, int64_t base, uint32_t off, int64_t row, int left,
                                            raw_t<T, V> (&r)[N]) {
-    const char* q = reinterpret_cast<const char*>(static_cast<const T*>(p) + base);
+    const SELSCAN_GLOBAL char* q = uniform(p, base * int64_t(sizeof(T)));
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const raw_t<T, V>*>(q + (off + uint32_t(i < left ? i : left) * uint32_t(row)));
+    for (int i = 0; i < N; ++i)
+        r[i] = *(const SELSCAN_GLOBAL raw_t<T, V>*)(q + (off + uint32_t(i < left ? i : left) * uint32_t(row)));
 }
 template <typename T, int V, int N>
 __device__ __forceinline__ void store_rows(void* p, int64_t base, uint32_t off, int64_t row, int i, const float (&o)[V]) {
-    char* q = uniform(reinterpret_cast<char*>(static_cast<T*>(p) + base) + i * row);
-    *reinterpret_cast<raw_t<T, V>*>(q + off) = pack<T, V>(o);
+    *(SELSCAN_GLOBAL raw_t<T, V>*)(uniform(p, base * int64_t(sizeof(T)) + i * row) + off) = pack<T, V>(o);
 }
 
 // The state after the first `n` waves' stretches (against time: after those behind wave n), from h: their entries
@@ -266,10 +269,110 @@ __device__ __forceinline__ void join_back(const Stretch (&whole)[kWaves][C], int
 // Forward: outputs from the state entering the run (kOut), checkpoints alone (kKeep), or the run's own stretch (kRun).
 enum { kOut = 0, kKeep = 1, kRun = 2 };
 
+// The forward's inputs of a lane's N tokens, as loaded.
+template <typename T, bool DECAY, bool GATE, int V, int N> struct FwdInputs {
+    raw_t<T, V> x[N], g[N], r[DECAY ? N : 1], z[GATE ? N : 1];
+    __device__ __forceinline__ void load(const GaArgs& a, int64_t at, uint32_t off, int64_t row) {
+        fetch<T, V, N>(a.x, at, off, row, x);
+        fetch<T, V, N>(a.g, at, off, row, g);
+        if constexpr (DECAY) fetch<T, V, N>(a.r, at, off, row, r);
+        if constexpr (GATE) fetch<T, V, N>(a.z, at, off, row, z);
+    }
+    __device__ __forceinline__ void load_some(const GaArgs& a, int64_t at, uint32_t off, int64_t row, int left) {
+        fetch_some<T, V, N>(a.x, at, off, row, left, x);
+        fetch_some<T, V, N>(a.g, at, off, row, left, g);
+        if constexpr (DECAY) fetch_some<T, V, N>(a.r, at, off, row, left, r);
+        if constexpr (GATE) fetch_some<T, V, N>(a.z, at, off, row, left, z);
+    }
+};
+
+// What the forward keeps of them: each token's decay and input, the gate, the group's stretch.
+template <typename T, bool DECAY, bool GATE, int V, int N> struct FwdTokens {
+    float dec[N][V], b[N][V];
+    raw_t<T, V> z[GATE ? N : 1];
+    double P[V];
+    float S[V];
+
+    template <bool FULL, bool FAR>
+    __device__ __forceinline__ void eval_as(const FwdInputs<T, DECAY, GATE, V, N>& in, const float (&A)[V], int have) {
+        Product prod[V];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float x[V], g[V], r[V];
+            unpack<T, V>(in.x[i], x);
+            unpack<T, V>(in.g[i], g);
+            if constexpr (DECAY) unpack<T, V>(in.r[i], r);
+            if constexpr (GATE) z[i] = in.z[i];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                Token k;
+                float slope;
+                if constexpr (DECAY) {
+                    k = decay_of<FAR>(A[v] * sigmoid(r[v]));
+                    k.f *= sigmoid(g[v]);
+                } else {
+                    k = mix_of(g[v], &slope);
+                }
+                dec[i][v] = k.a;
+                b[i][v] = k.f * x[v];
+                if constexpr (!FULL) {
+                    const bool there = i < have;
+                    k.e = there ? k.e : 0.0f;
+                    dec[i][v] = there ? k.a : 1.0f;
+                    b[i][v] = there ? b[i][v] : 0.0f;
+                }
+                prod[v].step(dec[i][v], k.e);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) P[v] = prod[v].value();
+    }
+    // FULL: all N tokens exist, else the first `have`. any: a channel of the wave has a rate below kNear.
+    template <bool FULL>
+    __device__ __forceinline__ void eval(const FwdInputs<T, DECAY, GATE, V, N>& in, const float (&A)[V], bool any,
+                                         int have) {
+        if (DECAY && !any) eval_as<FULL, false>(in, A, have);
+        else eval_as<FULL, true>(in, A, have);
+    }
+    __device__ __forceinline__ void step_from_zero() {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            S[v] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) S[v] = fmaf(dec[i][v], S[v], b[i][v]);
+        }
+    }
+    // y from the state entering the group; `left` rows exist of the tensor.
+    template <bool FULL>
+    __device__ __forceinline__ void put(void* y, int64_t at, uint32_t off, int64_t row, float (&h)[V], int have,
+                                        int64_t left) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                h[v] = fmaf(dec[i][v], h[v], b[i][v]);
+                o[v] = h[v];
+            }
+            if constexpr (GATE) {
+                float f[V];
+                unpack<T, V>(z[i], f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] *= silu(f[v]);
+            }
+            if constexpr (!FULL) {
+                if (i >= left) continue;
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = i < have ? o[v] : 0.0f;
+            }
+            store_rows<T, V, N>(y, at, off, row, i, o);
+        }
+    }
+};
+
 template <typename T, bool DECAY, bool GATE, int V, int CL, int N, int MODE>
 __global__ __launch_bounds__(kWaves * 64, N == 8 ? 4 : 2) void fwd_kernel(GaArgs a) {
     using W = Place<T, V, CL, N>;
-    using R = raw_t<T, V>;
     __shared__ Stretch whole[2][kWaves][W::kChan];
     __shared__ double carry[2][W::kChan];
     const int64_t per = (a.D + W::kChan - 1) / W::kChan * a.B, idx = xcd_tile(blockIdx.x, gridDim.x);
@@ -294,70 +397,21 @@ __global__ __launch_bounds__(kWaves * 64, N == 8 ? 4 : 2) void fwd_kernel(GaArgs
                                                             : 0.0;
     }
     any = __any(any);
-    R nx[N], ng[N], nr[DECAY ? N : 1], nz[GATE ? N : 1];
-    auto load = [&](int64_t t0) {
-        const int64_t at = w.base(a, t0);
-        fetch<T, V, N>(a.x, at, w.off, row, nx);
-        fetch<T, V, N>(a.g, at, w.off, row, ng);
-        if constexpr (DECAY) fetch<T, V, N>(a.r, at, w.off, row, nr);
-        if constexpr (GATE) fetch<T, V, N>(a.z, at, w.off, row, nz);
-    };
-    auto load_some = [&](int64_t t0, int left) {
-        const int64_t at = w.base(a, t0);
-        fetch_some<T, V, N>(a.x, at, w.off, row, left, nx);
-        fetch_some<T, V, N>(a.g, at, w.off, row, left, ng);
-        if constexpr (DECAY) fetch_some<T, V, N>(a.r, at, w.off, row, left, nr);
-        if constexpr (GATE) fetch_some<T, V, N>(a.z, at, w.off, row, left, nz);
-    };
+    FwdInputs<T, DECAY, GATE, V, N> in;
     // One tile; all its tokens exist if `whole_tile`, and the next one's loads are sent off if `more`.
     int buf = 0;
     auto tile = [&](int64_t t0, auto whole_tile, bool more) {
         constexpr bool FULL = decltype(whole_tile)::value;
         const int64_t t = w.token(t0);
         const int have = FULL ? N : n - t < 0 ? 0 : n - t < N ? int(n - t) : N;
-        float dec[N][V], b[N][V];
-        R z[GATE ? N : 1];
-        Product prod[V];
-        auto tokens = [&](auto far) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float x[V], g[V], r[V];
-                unpack<T, V>(nx[i], x);
-                unpack<T, V>(ng[i], g);
-                if constexpr (DECAY) unpack<T, V>(nr[i], r);
-                if constexpr (GATE) z[i] = nz[i];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    Token k;
-                    float slope;
-                    if constexpr (DECAY) {
-                        k = decay_of<decltype(far)::value>(A[v] * sigmoid(r[v]));
-                        k.f *= sigmoid(g[v]);
-                    } else {
-                        k = mix_of(g[v], &slope);
-                    }
-                    dec[i][v] = k.a;
-                    b[i][v] = k.f * x[v];
-                    if constexpr (!FULL) {
-                        const bool in = i < have;
-                        k.e = in ? k.e : 0.0f;
-                        dec[i][v] = in ? k.a : 1.0f;
-                        b[i][v] = in ? b[i][v] : 0.0f;
-                    }
-                    prod[v].step(dec[i][v], k.e);
-                }
-            }
-        };
-        if (DECAY && !any) tokens(std::false_type{});
-        else tokens(std::true_type{});
-        if (more) load(t0 + W::kTile);
+        FwdTokens<T, DECAY, GATE, V, N> tok;
+        tok.template eval<FULL>(in, A, any, have);
+        if (more) in.load(a, w.base(a, t0 + W::kTile), w.off, row);
+        tok.step_from_zero();
         Stretch own[V], before[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float S = 0.0f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) S = fmaf(dec[i][v], S, b[i][v]);
-            own[v] = {prod[v].value(), double(S)};
+            own[v] = {tok.P[v], double(tok.S[v])};
             before[v] = before_in_wave<CL>(own[v], w.tg);
             if (w.tg == W::kGroups - 1) whole[buf][w.wave][w.c * V + v] = own[v];
         }
@@ -384,43 +438,19 @@ __global__ __launch_bounds__(kWaves * 64, N == 8 ? 4 : 2) void fwd_kernel(GaArgs
             if (a.ckpt && w.live && t % SELSCAN_GATED_CKPT == 0 && t < a.L)
 #pragma unroll
                 for (int v = 0; v < V; ++v) a.ckpt[t / SELSCAN_GATED_CKPT * lanes + lane + v] = hf[v];
-            if constexpr (MODE == kOut) {
-                const int64_t at = w.base(a, t0);
-                if (w.live) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        float o[V];
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            hf[v] = fmaf(dec[i][v], hf[v], b[i][v]);
-                            o[v] = hf[v];
-                        }
-                        if constexpr (GATE) {
-                            float f[V];
-                            unpack<T, V>(z[i], f);
-#pragma unroll
-                            for (int v = 0; v < V; ++v) o[v] *= silu(f[v]);
-                        }
-                        if constexpr (!FULL) {
-                            if (t + i >= a.L) continue;
-#pragma unroll
-                            for (int v = 0; v < V; ++v) o[v] = i < have ? o[v] : 0.0f;
-                        }
-                        store_rows<T, V, N>(a.y, at, w.off, row, i, o);
-                    }
-                }
-            }
+            if constexpr (MODE == kOut)
+                if (w.live) tok.template put<FULL>(a.y, w.base(a, t0), w.off, row, hf, have, a.L - t);
         }
         buf ^= 1;
     };
     int64_t t0 = begin;
     const int64_t whole_end = begin + (stop > begin ? (stop - begin) / W::kTile * W::kTile : 0);
-    if (t0 < whole_end) load(t0);
+    if (t0 < whole_end) in.load(a, w.base(a, t0), w.off, row);
     for (; t0 < whole_end; t0 += W::kTile) tile(t0, std::true_type{}, t0 + W::kTile < whole_end);
     if (t0 < stop) {
         if (w.token(t0) < n) {
             const int64_t left = n - w.token(t0);
-            load_some(t0, int(left < N ? left : N) - 1);
+            in.load_some(a, w.base(a, t0), w.off, row, int(left < N ? left : N) - 1);
         }
         tile(t0, std::false_type{}, false);
         t0 += W::kTile;
@@ -449,6 +479,267 @@ __global__ __launch_bounds__(kWaves * 64, N == 8 ? 4 : 2) void fwd_kernel(GaArgs
     if (last_group && w.live && a.last && end == a.L) {
 #pragma unroll
         for (int v = 0; v < V; ++v) a.last[lane + v] = float(carry[buf][w.c * V + v]);
+    }
+}
+
+// ---- chained tiles -------------------------------------------------------------
+//
+// Where the channels are too few for a workgroup each to fill the chip, workgroups
+// take single tiles, all of a tile's channels before the next tile's, each tile by
+// the order in which a counter hands them out. A tile publishes its own stretch; the
+// state that enters it is folded from the state entering its link (kLink tiles) and
+// the stretches of the link's tiles before it, always in that order, so that results
+// do not depend on who came first; a link's last tile publishes the state entering
+// the next one. Every value is again read once. What is published is a word of 64
+// bits that says by itself whether it is there (kUnset, a NaN with low bits set,
+// which no conversion of a 32-bit value and no operation on such gives), stored and
+// read by atomics of the device's scope: no fence, and no order of several words.
+//
+// Every wait ends: a tile waits only for tiles that the counter handed out before
+// it, whose workgroups therefore run (a workgroup takes its next tile before it
+// finishes the one it has, but works on them in their order). Should a caller let two
+// calls share a workspace, the waits give up after kPatience rounds and hand on NaN.
+constexpr uint64_t kUnset = ~uint64_t(0);
+constexpr int kLink = 8, kPatience = 1 << 18;
+
+struct Chain {
+    uint64_t* P;       // [tile][batch * dim], the tiles' stretches
+    uint64_t* S;
+    uint64_t* enter;   // [link][batch * dim], the states entering the links from the second on
+    uint32_t* counter;
+    uint32_t tiles;
+};
+
+// Words of tile or link `i` (uniform), `lane` the lane's channel from the first of the workgroup's, `row`.
+struct Words {
+    uint64_t* p;
+    int64_t rows, row;
+    uint32_t lane;
+    __device__ __forceinline__ SELSCAN_GLOBAL uint64_t* at(uint32_t i) const {
+        const uint64_t first = reinterpret_cast<uint64_t>(p) + uint64_t((int64_t(i) * rows + row) * 8);
+        const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(first)),
+                       hi = __builtin_amdgcn_readfirstlane(uint32_t(first >> 32));
+        return (SELSCAN_GLOBAL uint64_t*)((SELSCAN_GLOBAL char*)(uint64_t(hi) << 32 | lo) + lane * 8u);
+    }
+    __device__ __forceinline__ void publish(uint32_t i, double v) const {
+        uint64_t u = __builtin_bit_cast(uint64_t, v);
+        if (u == kUnset) u = __builtin_bit_cast(uint64_t, __builtin_nan(""));
+        __hip_atomic_store(at(i), u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ uint64_t look(uint32_t i) const {
+        return __hip_atomic_load(at(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+};
+
+// What a wave does for tile `k`, a lane for each channel (`live` of them): publishes the tile's own stretch, waits for
+// the state that enters it (`from` enters tile 0), and returns that; a link's last tile hands on the next link's.
+__device__ __forceinline__ double link_tile(const Words& P, const Words& S, const Words& enter, uint32_t k, uint32_t tiles,
+                                            double from, bool live, const Stretch& own) {
+    const uint32_t m = k % kLink, base = k - m;
+    const bool more = k + 1 < tiles;
+    if (live && more && m != kLink - 1) {
+        P.publish(k, own.P);
+        S.publish(k, own.S);
+    }
+    uint64_t e = __builtin_bit_cast(uint64_t, from), p[kLink - 1], s[kLink - 1];
+    // Rounds over the words that come last, the state entering the link and the stretch of the tile before; then all
+    // at once, one trip to memory. (For those of tiles from k on, an earlier one's. Rounds over all of them would
+    // take the memory's time from everyone's inputs.)
+    bool all = false;
+    for (int round = 0;; ++round) {
+        bool wait = false;
+        if (live) {
+            if (base && !all) e = enter.look(base / kLink - 1);
+            if (m) {
+                if (all) {
+#pragma unroll
+                    for (int j = 0; j < kLink - 1; ++j) {
+                        p[j] = P.look(base + (j < int(m) ? j : m - 1));
+                        s[j] = S.look(base + (j < int(m) ? j : m - 1));
+                    }
+#pragma unroll
+                    for (int j = 0; j < kLink - 1; ++j) wait |= p[j] == kUnset || s[j] == kUnset;
+                } else {
+                    wait = S.look(k - 1) == kUnset;
+                }
+            }
+            wait |= base && e == kUnset;
+        }
+        if (!__any(wait)) {
+            if (all || !m) break;
+            all = true;
+            continue;
+        }
+        if (round == kPatience) {
+            e = __builtin_bit_cast(uint64_t, __builtin_nan(""));
+            break;
+        }
+        __builtin_amdgcn_s_sleep(4);
+    }
+    double h = __builtin_bit_cast(double, e);
+#pragma unroll
+    for (int j = 0; j < kLink - 1; ++j)
+        if (j < int(m)) h = __builtin_bit_cast(double, p[j]) * h + __builtin_bit_cast(double, s[j]);
+    if (live && more && m == kLink - 1) enter.publish(k / kLink, own.P * h + own.S);
+    return h;
+}
+
+// A chain's words unset and its counter 0; `copy` the entering states (zeros without them), as last_state may take
+// their place while tiles still start from them.
+__global__ __launch_bounds__(256) void start_chain_kernel(Chain ch, int64_t words, const float* from, float* copy,
+                                                          int64_t rows) {
+    const int64_t i0 = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+    if (i0 == 0) *ch.counter = 0;
+    for (int64_t i = i0; i < words; i += step) ch.P[i] = kUnset;
+    for (int64_t i = i0; i < rows; i += step) copy[i] = from ? from[i] : 0.0f;
+}
+
+// Eight waves compute; a ninth hands out the tiles and looks back. While it does that for a tile, the others
+// evaluate the next one and keep the tile's tokens in registers: one barrier a tile.
+template <typename T, bool DECAY, bool GATE, int V, int CL, int N, int MODE>
+__global__ __launch_bounds__(kWaves * 64 + 64, 3) void fwd_chain_kernel(GaArgs a, Chain ch) {
+    using W = Place<T, V, CL, N>;
+    static_assert(W::kChan <= 64, "a lane of the ninth wave for each channel");
+    __shared__ Stretch whole[3][kWaves][W::kChan];
+    __shared__ double enter[3][W::kChan];
+    __shared__ uint32_t tickets[3];
+    const uint32_t blocks = uint32_t((a.D + W::kChan - 1) / W::kChan), per = blocks * uint32_t(a.B);
+    const uint32_t total = ch.tiles * per;
+    const int64_t lanes = a.B * a.D, row = a.D * int64_t(sizeof(T));
+    const bool links = __builtin_amdgcn_readfirstlane(threadIdx.x / 64) == kWaves;
+    if (threadIdx.x == kWaves * 64) tickets[0] = atomicAdd(ch.counter, 1u);
+    __syncthreads();
+    uint32_t item = __builtin_amdgcn_readfirstlane(tickets[0]), before_item = total;
+    FwdInputs<T, DECAY, GATE, V, N> in;
+    float A[V];
+    auto load = [&](uint32_t it) {
+        const W w(it % per, a.D, blocks);
+        const int64_t n = entry_length(a.lengths, w.b, a.L), t0 = int64_t(it / per) * W::kTile;
+#pragma unroll
+        for (int v = 0; v < V; ++v) A[v] = DECAY ? rate_of(a.A, w.live ? w.d + v : w.d0) : 0.0f;
+        if (t0 + W::kTile <= n) {
+            in.load(a, w.base(a, t0), w.off, row);
+        } else if (w.token(t0) < n) {
+            const int64_t left = n - w.token(t0);
+            in.load_some(a, w.base(a, t0), w.off, row, int(left < N ? left : N) - 1);
+        }
+    };
+    // The tokens of the tile whose outputs are still to come: decays and inputs in LDS (a lane's own, two tiles in
+    // turn), the gate in registers.
+    constexpr int kQuads = N * V / 2;
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    __shared__ f32x4 kept[2][kQuads][kWaves * 64];
+    FwdTokens<T, DECAY, GATE, V, N> tok;
+    raw_t<T, V> prev_z[GATE ? N : 1];
+    Stretch before[V], prev_before[V];
+    int side = 0;
+    if (!links && item < total) load(item);
+    for (int buf = 0;; buf = buf == 2 ? 0 : buf + 1) {
+        const int after_buf = buf == 2 ? 0 : buf + 1, last_buf = buf == 0 ? 2 : buf - 1;
+        if (!links) {
+            if (item < total) {
+                const W w(item % per, a.D, blocks);
+                const int64_t n = entry_length(a.lengths, w.b, a.L), t0 = int64_t(item / per) * W::kTile, t = w.token(t0);
+                const int have = n - t < 0 ? 0 : n - t < N ? int(n - t) : N;
+                bool any = false;
+#pragma unroll
+                for (int v = 0; v < V; ++v) any |= A[v] < kNear;
+                any = __any(any);
+                if (t0 + W::kTile <= n) tok.template eval<true>(in, A, any, N);
+                else tok.template eval<false>(in, A, any, have);
+                tok.step_from_zero();
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q) {
+                    constexpr int per_quad = 2 / V;
+                    f32x4 f;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        f[2 * j] = tok.dec[q * per_quad + (V == 1 ? j : 0)][V == 1 ? 0 : j];
+                        f[2 * j + 1] = tok.b[q * per_quad + (V == 1 ? j : 0)][V == 1 ? 0 : j];
+                    }
+                    kept[side][q][threadIdx.x] = f;
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    Stretch own = {tok.P[v], double(tok.S[v])};
+                    before[v] = before_in_wave<CL>(own, w.tg);
+                    if (w.tg == W::kGroups - 1) whole[buf][w.wave][w.c * V + v] = own;
+                }
+            }
+        } else if (item < total && threadIdx.x == kWaves * 64) {
+            tickets[after_buf] = atomicAdd(ch.counter, 1u);
+        }
+        __syncthreads();
+        const uint32_t next = item < total ? __builtin_amdgcn_readfirstlane(tickets[after_buf]) : total;
+        if (!links) {
+            if (next < total) load(next);
+            if (before_item < total) {
+                const W w(before_item % per, a.D, blocks);
+                const int64_t n = entry_length(a.lengths, w.b, a.L), lane = w.b * a.D + w.d;
+                const int64_t t0 = int64_t(before_item / per) * W::kTile, t = w.token(t0);
+                const int have = n - t < 0 ? 0 : n - t < N ? int(n - t) : N;
+                double h[V];
+                float hf[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = enter[last_buf][w.c * V + v];
+                join<V>(whole[last_buf], w.c * V, w.wave, h);
+#pragma unroll
+                for (int v = 0; v < V; ++v) hf[v] = float(prev_before[v].P * h[v] + prev_before[v].S);
+                if (a.ckpt && w.live && t % SELSCAN_GATED_CKPT == 0 && t < a.L)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) a.ckpt[t / SELSCAN_GATED_CKPT * lanes + lane + v] = hf[v];
+                if constexpr (MODE == kOut) {
+                    const int64_t at = w.base(a, t0);
+#pragma unroll
+                    for (int q = 0; q < kQuads; ++q) {
+                        const f32x4 f = kept[side ^ 1][q][threadIdx.x];
+#pragma unroll
+                        for (int u = 0; u < 2 / V; ++u) {
+                            const int i = q * (2 / V) + u;
+                            float o[V];
+#pragma unroll
+                            for (int v = 0; v < V; ++v) {
+                                const int j = V == 1 ? u : v;
+                                hf[v] = fmaf(f[2 * j], hf[v], f[2 * j + 1]);
+                                o[v] = i < have ? hf[v] : 0.0f;
+                            }
+                            if constexpr (GATE) {
+                                float z[V];
+                                unpack<T, V>(prev_z[i], z);
+#pragma unroll
+                                for (int v = 0; v < V; ++v) o[v] *= i < have ? silu(z[v]) : 1.0f;
+                            }
+                            if (w.live && t + i < a.L) store_rows<T, V, N>(a.y, at, w.off, row, i, o);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < (GATE ? N : 0); ++i) prev_z[i] = tok.z[i];
+#pragma unroll
+            for (int v = 0; v < V; ++v) prev_before[v] = before[v];
+            side ^= 1;
+        } else if (item < total) {
+            const uint32_t k = item / per;
+            const W w(item % per, a.D, blocks);
+            const int c = threadIdx.x % 64;
+            const bool live = c < W::kChan && w.d0 + c < a.D;
+            const int64_t at = w.b * a.D + w.d0 + (live ? c : 0);
+            Stretch s = whole[buf][0][live ? c : 0];
+#pragma unroll
+            for (int j = 1; j < kWaves; ++j) s = after(s, whole[buf][j][live ? c : 0]);
+            const int64_t first = w.b * a.D + w.d0;
+            const uint32_t lane = live ? c : 0;
+            const double hin = link_tile(Words{ch.P, lanes, first, lane}, Words{ch.S, lanes, first, lane},
+                                         Words{ch.enter, lanes, first, lane}, k, ch.tiles, a.h0[at], live, s);
+            if (live) {
+                enter[buf][c] = hin;
+                if (k + 1 == ch.tiles && a.last) a.last[at] = float(s.P * hin + s.S);
+            }
+        }
+        if (item >= total) break;
+        before_item = item;
+        item = next;
     }
 }
 
@@ -781,6 +1072,7 @@ constexpr int kWide = 32, kNarrow = 16;
 constexpr int kNF = 8, kNFNarrow = 16, kNB = 4;
 constexpr int tile_of(int lanes, int tokens) { return kWaves * (64 / lanes) * tokens; }
 constexpr int kTile = tile_of(kWide, kNF);  // runs are of whole tiles
+constexpr int kChainGroups = 256;           // workgroups of a chain: one a CU
 static_assert(kTile % tile_of(kWide, kNB) == 0 && tile_of(kWide, kNB) % SELSCAN_GATED_CKPT == 0 &&
                   tile_of(kNarrow, kNFNarrow) % SELSCAN_GATED_CKPT == 0 && tile_of(kNarrow, kNB) % SELSCAN_GATED_CKPT == 0 &&
                   SELSCAN_GATED_CKPT % kNFNarrow == 0 && SELSCAN_GATED_CKPT % kNF == 0,
@@ -848,10 +1140,13 @@ void run_carry(Stretch* runs, double* enter, const float* first, int64_t rows, i
                        segments, against);
 }
 
-// Workspace: the runs' stretches and entering states, then (backward) the checkpoints and the sums of dA.
+// Workspace: the runs' stretches and entering states, or a chain's words, its counter and the states that it starts
+// from, then (backward) the checkpoints and the sums of dA.
 struct Layout {
-    size_t enter, ckpt, part, bytes;
+    size_t enter, counter, from, ckpt, part, bytes;
 };
+int64_t chain_links(const GatedPlan& p) { return ceil_div(p.chain, kLink); }
+int64_t chain_words(const GatedShape& s, const GatedPlan& p) { return (2 * p.chain + chain_links(p)) * s.batch * s.dim; }
 Layout layout_of(const GatedShape& s, const GatedPlan& p, bool backward, bool ckpt_given) {
     const size_t rows = size_t(s.batch) * s.dim;
     Layout l{};
@@ -860,6 +1155,11 @@ Layout layout_of(const GatedShape& s, const GatedPlan& p, bool backward, bool ck
         at = up256(rows * p.segments * sizeof(Stretch));
         l.enter = at;
         at += up256(rows * p.segments * sizeof(double));
+    }
+    if (p.chain) {
+        l.counter = up256(size_t(chain_words(s, p)) * sizeof(uint64_t));
+        l.from = l.counter + 256;
+        at = l.from + up256(rows * sizeof(float));
     }
     l.ckpt = at;
     if (backward && !ckpt_given) at += up256(size_t(ceil_div(s.L, SELSCAN_GATED_CKPT)) * rows * sizeof(float));
@@ -872,17 +1172,16 @@ Layout layout_of(const GatedShape& s, const GatedPlan& p, bool backward, bool ck
 }  // namespace
 
 bool gated_plan(const GatedShape& s, int32_t requested, bool backward, GatedPlan* p) {
-    (void)backward;
-    *p = GatedPlan{1, s.L};
+    *p = GatedPlan{1, s.L, 0};
     const int64_t blocks = blocks_of(s, kWide);
     int64_t want = requested;
     if (!requested) {
-        // Runs, which read what the decays hang on twice, where even narrow workgroups
-        // leave CUs idle, of eight tiles at least (bf16 1 x 8192, us with and without:
-        // 2560 channels 89 and 101, gradients 160 and 265; 5120 140 and 139).
-        want = blocks > 0 && blocks < 96 ? 512 / blocks : 1;
-        const int64_t most = s.L / (8 * kTile);
-        want = want < most ? want : most;
+        want = 1;
+#ifndef CHAIN_BELOW
+#define CHAIN_BELOW 96
+#endif
+        if (!backward && blocks < CHAIN_BELOW) p->chain = ceil_div(s.L, kTile);
+        if (p->chain < 4) p->chain = 0;
     }
     if (want > 1 && s.L > kTile) {
         p->seg_len = ceil_div(ceil_div(s.L, want), kTile) * kTile;
@@ -898,6 +1197,34 @@ size_t gated_bwd_workspace_bytes(const GatedShape& s, const GatedPlan& p, bool c
     return layout_of(s, p, true, ckpt_given).bytes;
 }
 
+namespace {
+// The chain in `ws`, made ready: its words unset, and the states (gradients) that it starts from in a.h0 (a.dlast).
+Chain start_chain(char* ws, const Layout& l, const GatedShape& s, const GatedPlan& p, const float** from,
+                  hipStream_t st) {
+    const int64_t rows = s.batch * s.dim, words = chain_words(s, p);
+    Chain ch{};
+    ch.P = reinterpret_cast<uint64_t*>(ws);
+    ch.S = ch.P + p.chain * rows;
+    ch.enter = ch.S + p.chain * rows;
+    ch.counter = reinterpret_cast<uint32_t*>(ws + l.counter);
+    ch.tiles = uint32_t(p.chain);
+    float* copy = reinterpret_cast<float*>(ws + l.from);
+    const int64_t groups = ceil_div(words, 1024);
+    hipLaunchKernelGGL(start_chain_kernel, dim3(unsigned(groups < 4096 ? groups : 4096)), dim3(256), 0, st, ch, words,
+                       *from, copy, rows);
+    *from = copy;
+    return ch;
+}
+template <int MODE> void run_fwd_chain(const GaArgs& a, const Chain& ch, const GatedShape& s, hipStream_t st) {
+    dispatch(s, MODE == kOut && a.z, [&](auto T, auto decay, auto gate, auto V) {
+        const int64_t tiles = blocks_of(s, kWide) * int64_t(ch.tiles);
+        hipLaunchKernelGGL((fwd_chain_kernel<decltype(T), decltype(decay)::value, MODE == kOut && decltype(gate)::value,
+                                             decltype(V)::value, kWide, kNF, MODE>),
+                           dim3(unsigned(tiles < kChainGroups ? tiles : kChainGroups)), dim3(kWaves * 64 + 64), 0, st, a, ch);
+    });
+}
+}  // namespace
+
 hipError_t launch_gated_fwd(const GatedTensors& t, const GatedShape& s, const GatedPlan& p, void* workspace,
                             hipStream_t stream) {
     GaArgs a = args_of(t, s, p);
@@ -909,7 +1236,12 @@ hipError_t launch_gated_fwd(const GatedTensors& t, const GatedShape& s, const Ga
         run_carry(a.runs, enter, a.h0, s.batch * s.dim, p.segments, false, stream);
         a.enter = enter;
     }
-    run_fwd<kOut>(a, s, p.segments, stream);
+    if (p.chain) {
+        const Chain ch = start_chain(static_cast<char*>(workspace), layout_of(s, p, false, false), s, p, &a.h0, stream);
+        run_fwd_chain<kOut>(a, ch, s, stream);
+    } else {
+        run_fwd<kOut>(a, s, p.segments, stream);
+    }
     return hipGetLastError();
 }
 
@@ -947,7 +1279,7 @@ hipError_t launch_gated_bwd(const GatedTensors& t, const GatedShape& s, const Ga
 }
 
 hipError_t launch_gated_step(float* state, const GatedTensors& t, const GatedShape& s, hipStream_t stream) {
-    const GaArgs a = args_of(t, s, GatedPlan{1, 1});
+    const GaArgs a = args_of(t, s, GatedPlan{1, 1, 0});
     auto kind = [&](auto T, auto decay) {
         hipLaunchKernelGGL((step_kernel<decltype(T), decltype(decay)::value>),
                            dim3(unsigned(ceil_div(s.batch * s.dim, 256))), dim3(256), 0, stream, state, a);

@@ -278,6 +278,7 @@ struct GatedShape {
 struct GatedPlan {
     int32_t segments;  // runs of seg_len tokens (a multiple of the tile when segments > 1)
     int64_t seg_len;
+    int64_t chain;  // tiles of the sequence, taken one by one and chained (0: walks, or runs of them)
 };
 struct GatedTensors {
     const void* x;
