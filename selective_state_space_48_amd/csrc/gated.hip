@@ -1177,11 +1177,18 @@ bool gated_plan(const GatedShape& s, int32_t requested, bool backward, GatedPlan
     int64_t want = requested;
     if (!requested) {
         want = 1;
-#ifndef CHAIN_BELOW
-#define CHAIN_BELOW 96
-#endif
-        if (!backward && blocks < CHAIN_BELOW) p->chain = ceil_div(s.L, kTile);
-        if (p->chain < 4) p->chain = 0;
+        const int64_t single = narrow(s) ? ceil_div(blocks_of(s, kNarrow), 256) * 23 : ceil_div(blocks, 256) * 40;
+        if (!backward) {
+            // Chained tiles, which share out evenly what workgroups of whole sequences do not, at 1.3 of its cost and
+            // some 10 us (bf16, us, single and chained: 1 x 2048 x 2560 33 and 24, 1 x 32771 x 2560 588 and 217, 2 x
+            // 4096 x 5120 135 and 113; but 2 x 4096 x 4096 66 and 85, 3 x 4096 x 5120 143 and 163).
+            if (s.L >= 16 * kTile && blocks * 52 < single * 256) p->chain = ceil_div(s.L, kTile);
+        } else if (blocks > 0 && blocks < 96) {
+            // Runs, which read what the decays hang on twice, where even narrow workgroups leave CUs idle, of eight
+            // tiles at least (bf16 1 x 8192 x 2560, us with and without: 160 and 265).
+            const int64_t most = s.L / (8 * kTile);
+            want = 512 / blocks < most ? 512 / blocks : most;
+        }
     }
     if (want > 1 && s.L > kTile) {
         p->seg_len = ceil_div(ceil_div(s.L, want), kTile) * kTile;

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -872,24 +873,29 @@ def _gated_args(x, g, r, A, z, shape, **others) -> "GatedDims":
     return GatedDims(shape[0], L, shape[-1], _DTYPES[x.dtype], GATED_MIX if r is None else GATED_DECAY)
 
 
+# (The sizes alone decide: a call of the same sizes as one before saves the query.)
+@functools.lru_cache(maxsize=256)
+def _gated_need(batch: int, L: int, dim: int, dtype: int, kind: int, segments: int, backward: bool, ckpt: bool) -> int:
+    dims, n = GatedDims(batch, L, dim, dtype, kind), ctypes.c_uint64(0)
+    if backward:
+        opts = GatedBwdOpts(ckpt=16 if ckpt else None, segments=segments)
+        _check(lib.selscan_gated_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(n)))
+    else:
+        _check(lib.selscan_gated_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(GatedOpts(segments=segments)),
+                                                    ctypes.byref(n)))
+    return int(n.value)
+
+
 def gated_workspace_size(batch: int, L: int, dim: int, dtype: torch.dtype, *, decay: bool = True,
                          segments: int = 0) -> int:
     """Bytes of workspace ``gated_fwd`` needs for this shape and number of segments."""
-    dims = GatedDims(batch, L, dim, _DTYPES[dtype], int(decay))
-    n = ctypes.c_uint64(0)
-    _check(lib.selscan_gated_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(GatedOpts(segments=int(segments))),
-                                                ctypes.byref(n)))
-    return int(n.value)
+    return _gated_need(batch, L, dim, _DTYPES[dtype], int(decay), int(segments), False, False)
 
 
 def gated_bwd_workspace_size(batch: int, L: int, dim: int, dtype: torch.dtype, *, decay: bool = True,
                              ckpt_given: bool = False, segments: int = 0) -> int:
     """Bytes of workspace ``gated_bwd`` needs for this shape and these choices."""
-    dims = GatedDims(batch, L, dim, _DTYPES[dtype], int(decay))
-    opts = GatedBwdOpts(ckpt=16 if ckpt_given else None, segments=int(segments))
-    n = ctypes.c_uint64(0)
-    _check(lib.selscan_gated_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(n)))
-    return int(n.value)
+    return _gated_need(batch, L, dim, _DTYPES[dtype], int(decay), int(segments), True, bool(ckpt_given))
 
 
 def gated_fwd(x: torch.Tensor, g: torch.Tensor, r: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
@@ -919,15 +925,15 @@ def gated_fwd(x: torch.Tensor, g: torch.Tensor, r: Optional[torch.Tensor] = None
     _req(ckpt, "ckpt", torch.float32, gated_ckpt_shape(batch, L, dim), dev)
     with _device(dev):
         if y is None:
-            y = torch.empty((batch, L, dim), dtype=dt, device=dev)
-        _req(y, "y", dt, (batch, L, dim), dev)
-        if last_state is None and return_last_state:
+            y = torch.empty_like(x)
+        else:
+            _req(y, "y", dt, x.shape, dev)
+        if last_state is not None:
+            _req(last_state, "last_state", torch.float32, (batch, dim), dev)
+        elif return_last_state:
             last_state = torch.empty((batch, dim), dtype=torch.float32, device=dev)
-        _req(last_state, "last_state", torch.float32, (batch, dim), dev)
         opts = GatedOpts(_ptr(h0), _ptr(lengths), _ptr(ckpt), int(segments), None, 0)
-        need = ctypes.c_uint64(0)
-        _check(lib.selscan_gated_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(need)))
-        workspace = _scratch(workspace, int(need.value), dev)
+        workspace = _scratch(workspace, _gated_need(batch, L, dim, dims.dtype, dims.kind, opts.segments, False, False), dev)
         if workspace is not None:
             opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
         _check(lib.selscan_gated_fwd(_ptr(x), _ptr(g), _ptr(r), _ptr(A), _ptr(z), _ptr(y), _ptr(last_state),
@@ -948,8 +954,9 @@ def gated_step(state: torch.Tensor, x: torch.Tensor, g: torch.Tensor, r: Optiona
     _req(state, "state", torch.float32, state.shape, dev)
     with _device(dev):
         if y is None:
-            y = torch.empty(state.shape, dtype=dt, device=dev)
-        _req(y, "y", dt, state.shape, dev)
+            y = torch.empty_like(x)
+        else:
+            _req(y, "y", dt, state.shape, dev)
         _check(lib.selscan_gated_step(_ptr(state), _ptr(x), _ptr(g), _ptr(r), _ptr(A), _ptr(z), _ptr(y),
                                       ctypes.byref(dims), _stream(dev)))
     return y
@@ -990,9 +997,8 @@ def gated_bwd(x: torch.Tensor, g: torch.Tensor, r: Optional[torch.Tensor] = None
             out["dh0"] = torch.empty((batch, dim), dtype=torch.float32, device=dev)
         opts = GatedBwdOpts(_ptr(h0), _ptr(lengths), _ptr(dlast_state), _ptr(out.get("dh0")), _ptr(ckpt),
                             int(segments), None, 0)
-        need = ctypes.c_uint64(0)
-        _check(lib.selscan_gated_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(need)))
-        workspace = _scratch(workspace, int(need.value), dev)
+        workspace = _scratch(workspace, _gated_need(batch, L, dim, dims.dtype, dims.kind, opts.segments, True,
+                                                    ckpt is not None), dev)
         if workspace is not None:
             opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
         _check(lib.selscan_gated_bwd(_ptr(x), _ptr(g), _ptr(r), _ptr(A), _ptr(z), _ptr(dy), _ptr(out["dx"]),
@@ -1055,12 +1061,14 @@ def addnorm(x: torch.Tensor, res: Optional[torch.Tensor] = None, *, pre: str = "
     _req(res, "res", rt, shape, dev)
     opts = _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate)
     with _device(dev):
-        if y is None and pre != "none":
-            y = torch.empty(shape, dtype=dt, device=dev)
-        _req(y, "y", dt, shape, dev)
-        if res_out is None and return_res:
-            res_out = torch.empty(shape, dtype=rt, device=dev)
-        _req(res_out, "res_out", rt, shape, dev)
+        if y is not None:
+            _req(y, "y", dt, shape, dev)
+        elif pre != "none":
+            y = torch.empty_like(x)
+        if res_out is not None:
+            _req(res_out, "res_out", rt, shape, dev)
+        elif return_res:
+            res_out = torch.empty_like(x if res is None else res, dtype=rt)
         stats = torch.empty((rows, 4), dtype=torch.float32, device=dev) if return_stats else None
         _check(lib.selscan_addnorm(_ptr(x), _ptr(res), _ptr(res_out), _ptr(y), _ptr(stats), ctypes.byref(dims),
                                    ctypes.byref(opts), _stream(dev)))
@@ -1202,11 +1210,13 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor, *
     with _device(dev):
         if q_out is None:
             q_out = torch.empty_like(q)
-        _req(q_out, "q_out", dt, q.shape, dev)
+        else:
+            _req(q_out, "q_out", dt, q.shape, dev)
         if k is not None:
             if k_out is None:
                 k_out = torch.empty_like(k)
-            _req(k_out, "k_out", dt, k.shape, dev)
+            else:
+                _req(k_out, "k_out", dt, k.shape, dev)
         _check(lib.selscan_rotary(_ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(q_out), _ptr(k_out),
                                   ctypes.byref(dims), _stream(dev)))
     return q_out, k_out

@@ -170,6 +170,31 @@ def test_many_rows():
         check(make(R, C, ("bf16", "bf16"), seed=4, post="layer", gates=gates), "layer", "rms", what)
 
 
+@pytest.mark.parametrize("types", TYPES)
+def test_wide_rows_with_gates(types):
+    """Rows of more than 512 threads, whose sums over rows are formed in a launch of their own."""
+    for R, C, gates in ((6, 9000, 0), (6, 9000, 2), (4, 16384, 1), (9, 8200, 9)):
+        what = f"{(R, C, gates)} {types}"
+        case(what)
+        check(make(R, C, types, seed=14, post="layer", gates=gates), "layer", "rms", what)
+    case("a gate without its gradient, sums without a gate")
+    p = make(12, 9000, types, seed=15, post="none", gates=3)
+    _, s, st = selscan.addnorm(p["x"], p["res"], gate=p["gate"], pre_weight=p["pre_weight"])
+    r = selscan.addnorm_bwd(None, s, dy=p["dy"], stats=st, gate=p["gate"], pre_weight=p["pre_weight"],
+                            want_dparams=False)
+    full = selscan.addnorm_bwd(p["x"], s, dy=p["dy"], stats=st, gate=p["gate"], pre_weight=p["pre_weight"])
+    torch.cuda.synchronize()
+    assert sorted(r) == ["dres", "dx"] and all(torch.equal(r[k], full[k]) for k in r)
+
+
+def test_many_gate_rows():
+    """As many gate rows as workgroups, or more: each workgroup takes whole ones."""
+    for R, C, gates in ((4000, 24, 2000), (3000, 600, 1500), (1024, 1000, 1024), (600, 9000, 300), (5000, 8, 5000)):
+        what = f"{(R, C, gates)}"
+        case(what)
+        check(make(R, C, ("f32", "f32"), seed=16, post="rms", gates=gates, bias=False), "rms", "layer", what)
+
+
 def test_far_mean_no_weights_other_eps():
     case("far mean")
     check(make(4, 700, ("f32", "f32"), seed=5, weight=False, bias=False, mean=300.0), "layer", "layer", "far mean",

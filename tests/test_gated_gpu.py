@@ -337,3 +337,93 @@ def test_token_loop_in_a_graph():
         want = selscan.gated_step(eager, p["x"], p["g"], p["r"], p["A"], p["z"])
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(state, eager)
+
+
+CHAINED = [
+    # long and few channels: tiles in a chain (batch, tokens, channels)
+    (1, 2048, 64),
+    (1, 2049, 2),
+    (2, 2200, 70),
+    (1, 4097, 33),
+    (3, 2311, 130),
+    (1, 6000, 1),
+]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", CHAINED)
+def test_chained_tiles(shape, dtype, kind):
+    """Against the definition; the gradients from the chain's checkpoints; whole, padded, from a state in place."""
+    B, L, D = shape
+    for z, h0 in ((False, False), (True, True)):
+        lengths = [L - 700 * b for b in range(B)] if h0 else None
+        what = f"chain {shape} {dtype} {kind} z={z} h0={h0}"
+        case(what)
+        p = make(B, L, D, kind, DT[dtype], seed=30, z=z, h0=h0, lengths=lengths, grads=True)
+        q = np_of(p)
+        y, last, c = forward(p, ckpt=True)
+        check_fwd(y, last, q, what, c)
+        check_bwd(backward(p, c), q, what)
+        if h0:
+            state = p["h0"].clone()
+            y2, _ = selscan.gated_fwd(p["x"], p["g"], p["r"], p["A"], p["z"], h0=state, lengths=p["lengths"],
+                                      last_state=state)
+            torch.cuda.synchronize()
+            assert torch.equal(y, y2) and torch.equal(last, state)
+
+
+def test_chain_is_deterministic():
+    """Over many calls, from workspaces of any contents, beside another call on another stream, in a graph."""
+    case("chain, determinism")
+    p = make(1, 9000, 200, "decay", torch.float32, seed=31, z=True, h0=True)
+    q = make(1, 12000, 64, "mix", torch.bfloat16, seed=32)
+    y, last, c = forward(p, ckpt=True)
+    yq, lastq, _ = forward(q)
+    need = selscan.gated_workspace_size(1, 9000, 200, torch.float32)
+    ws, ws2 = (torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    for turn in range(12):
+        ws.fill_(turn * 23 % 256)
+        y2, last2, c2 = forward(p, ckpt=True, workspace=ws)
+        assert torch.equal(y, y2) and torch.equal(last, last2) and torch.equal(c, c2), turn
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            a = selscan.gated_fwd(q["x"], q["g"])
+        b = selscan.gated_fwd(p["x"], p["g"], p["r"], p["A"], p["z"], h0=p["h0"], workspace=ws2)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], yq) and torch.equal(a[1], lastq)
+        assert torch.equal(b[0], y) and torch.equal(b[1], last)
+    graphs = []
+    for _ in range(2):  # two graphs that share a workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = selscan.gated_fwd(p["x"], p["g"], p["r"], p["A"], p["z"], h0=p["h0"], workspace=ws)
+        graphs.append((g, out))
+    for turn in range(3):
+        for g, out in graphs:
+            out[0].zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], y) and torch.equal(out[1], last)
+        p["x"].mul_(1.0)  # (the program's own work between the replays)
+
+
+def test_chain_not_finite():
+    case("chain, not finite")
+    for kind in KINDS:
+        p = make(1, 4000, 70, kind, torch.float32, seed=33)
+        clean, _, _ = forward(p)
+        p["x"][0, 1303, 17] = float("nan")
+        p["g"][0, 2900, 68] = float("nan")
+        y, last, _ = forward(p)
+        same = torch.ones_like(y, dtype=torch.bool)
+        same[0, 1303:, 17] = same[0, 2900:, 68] = False
+        assert torch.equal(y[same], clean[same]) and torch.isnan(y[0, 1303:, 17]).all() and torch.isnan(last[0, 68])
+        if kind == "decay":
+            p["r"][0, :] = float("-inf")  # nothing is forgotten, nothing added
+            p["x"].zero_()
+            p["g"].zero_()
+            y, last = selscan.gated_fwd(p["x"], p["g"], p["r"], p["A"], h0=torch.full((1, 70), 3.0, device="cuda"))
+            torch.cuda.synchronize()
+            assert (y == 3).all() and (last == 3).all()
