@@ -466,11 +466,11 @@ __global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(An
 }
 
 // The sums over rows where bwd_kernel does not form them: a thread takes a vector of columns down the rows of its
-// workgroup (grid y), from the averages that bwd_kernel left.
+// workgroup (grid x), from the averages that bwd_kernel left.
 template <typename T, typename S>
 __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
     const AddnormTensors& t = a.t;
-    const int64_t c = (int64_t(blockIdx.x) * 64 + threadIdx.x) * kV, blk = blockIdx.y;
+    const int64_t c = (int64_t(blockIdx.y) * 64 + threadIdx.x) * kV, blk = blockIdx.x;
     const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
     const bool use_x = post || t.dgate;
     const int n = a.C - c < 0 ? 0 : a.C - c < kV ? int(a.C - c) : kV;
@@ -612,12 +612,18 @@ BwdPlan bwd_plan(const AddnormShape& s, const AddnormTensors& w) {
     const int64_t step = p.wide ? 1 : 256 / p.lanes, groups = s.G ? s.G : 1, rows = s.R / groups;
     // workgroups for 512 threads a CU
     const int64_t want = 256 * (p.wide ? ceil_div(512, p.lanes) : 4);
-    if (w.dgate && groups >= want) {  // whole gate rows, whose sums are then done
-        p.per = ceil_div(groups, want) * rows;
+    // A thread's sums of 256 rows at most (more where that would take more than 2^20 workgroups), so that long sums
+    // lose no more than short ones.
+    int64_t most = ceil_div(s.R, int64_t(1) << 20);
+    most = most < 256 * step ? 256 * step : most;
+    if (w.dgate && groups >= want && rows <= most) {  // whole gate rows, whose sums are then done
+        const int64_t share = ceil_div(groups, want), fit = rows > 0 ? most / rows : 1;
+        p.per = (share < fit ? share : fit) * rows;
         p.blocks = ceil_div(s.R, p.per);
     } else {  // runs of a gate row's rows; of all rows where the gate's gradient is not wanted
         const int64_t of = w.dgate ? rows : s.R, g = w.dgate ? groups : 1;
-        p.per = ceil_div(ceil_div(of, ceil_div(want, g)), step) * step;
+        const int64_t per = ceil_div(of, ceil_div(want, g));
+        p.per = ceil_div(per < most ? per : most, step) * step;
         p.blocks = ceil_div(of, p.per) * g;
         p.runs = w.dgate ? ceil_div(of, p.per) : 0;
     }
@@ -692,7 +698,7 @@ hipError_t launch_addnorm_bwd(const AddnormTensors& t, const AddnormShape& s, vo
         }
         if (a.averages)
             hipLaunchKernelGGL((cols_kernel<decltype(T), decltype(S)>),
-                               dim3(unsigned(ceil_div(s.C, 64 * kV)), unsigned(p.blocks)), dim3(64), 0, stream, a, p.sums);
+                               dim3(unsigned(p.blocks), unsigned(ceil_div(s.C, 64 * kV))), dim3(64), 0, stream, a, p.sums);
     });
     const unsigned cols = unsigned(ceil_div(s.C, 64));
     if (sums) {
@@ -719,9 +725,15 @@ hipError_t launch_addnorm_bwd(const AddnormTensors& t, const AddnormShape& s, vo
         j.part = a.gate_part;
         j.pitch = s.C; j.C = s.C;
         j.count = int32_t(p.runs); j.total = int32_t(p.blocks);
-        j.out[0] = t.dgate;
         j.step = s.C;
-        hipLaunchKernelGGL(join_kernel, dim3(cols, 1, unsigned(s.G)), dim3(1024), 0, stream, j);
+        const int64_t most = 65535;  // workgroups along z
+        for (int64_t g = 0; g < s.G; g += most) {
+            const int64_t n = s.G - g < most ? s.G - g : most;
+            j.part = a.gate_part + g * p.runs * s.C;
+            j.total = int32_t(n * p.runs);
+            j.out[0] = t.dgate + g * s.C;
+            hipLaunchKernelGGL(join_kernel, dim3(cols, 1, unsigned(n)), dim3(1024), 0, stream, j);
+        }
     }
     return hipGetLastError();
 }

@@ -760,14 +760,14 @@ __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
     const int64_t stop = end < n ? end : n, row = a.D * int64_t(sizeof(T));
     const int64_t tiles = stop > begin ? (stop - begin + W::kTile - 1) / W::kTile : 0;
     const bool first_group = w.wave == 0 && w.tg == 0;
-    float A[V], dA[V];
-    double allP[V];
+    float A[V];
+    double dA[V], allP[V];
     bool any = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         A[v] = DECAY ? rate_of(a.A, w.live ? w.d + v : w.d0) : 0.0f;
         any |= A[v] < kNear;
-        dA[v] = 0.0f;
+        dA[v] = 0.0;
         allP[v] = 1.0;
         if (first_group)
             carry[0][w.c * V + v] = MODE == kRun || !w.live ? 0.0
@@ -935,6 +935,7 @@ __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
                 }
             }
             if (w.live) {
+                float sum[V] = {};  // a tile's share of dA; tiles are added in 64 bits
 #pragma unroll
                 for (int i = N - 1; i >= 0; --i) {
                     float ox[V], og[V], orr[V], oz[V];
@@ -949,7 +950,7 @@ __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
                         } else {
                             og[v] = in ? G * fs[i][v] : 0.0f;
                             const float dl = in ? G * fmaf(dec[i][v], hb[i][v], -rest[i][v]) : 0.0f;
-                            dA[v] = fmaf(dl, sr[i][v], dA[v]);
+                            sum[v] = fmaf(dl, sr[i][v], sum[v]);
                             orr[v] = in ? dl * rs[i][v] : 0.0f;
                         }
                         if constexpr (GATE) oz[v] = in ? dz[i][v] : 0.0f;
@@ -960,6 +961,9 @@ __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
                     if constexpr (DECAY) store_rows<T, V, N>(a.dr, at, w.off, row, i, orr);
                     if constexpr (GATE) store_rows<T, V, N>(a.dz, at, w.off, row, i, oz);
                 }
+                if constexpr (DECAY)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) dA[v] += double(sum[v]);
             }
         }
         buf ^= 1;
@@ -988,16 +992,16 @@ __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
     }
     if constexpr (DECAY) {
         if (a.dA_part) {  // the groups' sums in order
-            __shared__ float sums[kWaves * W::kGroups][W::kChan];
+            __shared__ double sums[kWaves * W::kGroups][W::kChan];
 #pragma unroll
             for (int v = 0; v < V; ++v) sums[w.wave * W::kGroups + w.tg][w.c * V + v] = dA[v];
             __syncthreads();
             if (first_group && w.live)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float s = 0.0f;
+                    double s = 0.0;
                     for (int j = 0; j < kWaves * W::kGroups; ++j) s += sums[j][w.c * V + v];
-                    a.dA_part[(run * a.B + w.b) * a.D + w.d + v] = s;
+                    a.dA_part[(run * a.B + w.b) * a.D + w.d + v] = float(s);
                 }
         }
     }
