@@ -741,12 +741,15 @@ typedef struct {
  *               inputs (behind an entry's length: its last state).
  *   segments  : runs of tokens scanned in parallel (1 = one walk per channel;
  *               > 1 = the runs' own decays and states, their carries, then the
- *               outputs); 0 = automatic. At most 65536; the run length is
- *               rounded up to whole tiles. Results agree to rounding.
+ *               outputs); 0 = automatic (one walk, or where channels are few and
+ *               tokens many single tiles in a chain; the backward: runs). At
+ *               most 65536; the run length is rounded up to whole tiles.
+ *               Results agree to rounding.
  *   workspace : caller-owned device memory of workspace_bytes bytes, 256-byte
  *               aligned, at least selscan_gated_fwd_workspace_size(); NULL
- *               means the library takes and returns its own on the stream. It
- *               must not overlap any input or output.
+ *               means the library takes and returns its own on the stream. The
+ *               contents on entry do not matter; calls that overlap in time
+ *               must not share it. It must not overlap any input or output.
  */
 typedef struct {
     const float* h0;

@@ -1083,10 +1083,12 @@ static_assert(kTile % tile_of(kWide, kNB) == 0 && tile_of(kWide, kNB) % SELSCAN_
               "a checkpoint is the state entering a group of tokens, and every tile's first");
 
 int64_t blocks_of(const GatedShape& s, int lanes) { return ceil_div(s.dim, lanes * lane_channels(s)) * s.batch; }
-bool narrow(const GatedShape& s) {
-    const int64_t wide = ceil_div(blocks_of(s, kWide), 256), half = ceil_div(blocks_of(s, kNarrow), 256);
-    return half * 23 < wide * 40;  // half the work each, at 1.15 of its cost
-}
+// Rounds of workgroups over the CUs, weighed: a wide one 40; a narrow one half the work at 1.15 of its cost, or twice
+// it where a lane's channel is 2 bytes and a row 32 (8 x 2048 x 2049 bf16 76 and 160).
+int64_t wide_cost(const GatedShape& s) { return ceil_div(blocks_of(s, kWide), 256) * 40; }
+bool thin(const GatedShape& s) { return s.dtype == DType::BF16 && lane_channels(s) == 1; }
+int64_t narrow_cost(const GatedShape& s) { return ceil_div(blocks_of(s, kNarrow), 256) * (thin(s) ? 46 : 23); }
+bool narrow(const GatedShape& s) { return narrow_cost(s) < wide_cost(s); }
 
 // f(type, decay, gate, channels of a lane) with the call's choices as constants.
 template <typename F> void dispatch(const GatedShape& s, bool gate, F f) {
@@ -1181,17 +1183,23 @@ bool gated_plan(const GatedShape& s, int32_t requested, bool backward, GatedPlan
     int64_t want = requested;
     if (!requested) {
         want = 1;
-        const int64_t single = narrow(s) ? ceil_div(blocks_of(s, kNarrow), 256) * 23 : ceil_div(blocks, 256) * 40;
+        const int64_t single = narrow(s) ? narrow_cost(s) : wide_cost(s);
         if (!backward) {
-            // Chained tiles, which share out evenly what workgroups of whole sequences do not, at 1.3 of its cost and
-            // some 10 us (bf16, us, single and chained: 1 x 2048 x 2560 33 and 24, 1 x 32771 x 2560 588 and 217, 2 x
-            // 4096 x 5120 135 and 113; but 2 x 4096 x 4096 66 and 85, 3 x 4096 x 5120 143 and 163).
-            if (s.L >= 16 * kTile && blocks * 52 < single * 256) p->chain = ceil_div(s.L, kTile);
+            // Chained tiles, which share out evenly what workgroups of whole sequences do not, at 1.3 of its cost (2.6 of
+            // rows of 32 values of 2 bytes) and some 10 us (bf16, us, single and chained: 8 x 2048 x 64 31 and 17, 1 x
+            // 2048 x 2560 33 and 24, 1 x 32771 x 2560 588 and 217, 2 x 4096 x 5120 135 and 113; but 2 x 1024 x 2560 20
+            // and 23, 2 x 4096 x 4096 66 and 85, 3 x 4096 x 5120 143 and 163, 8 x 2048 x 2049 84 and 159).
+            if (s.L > 12 * kTile && blocks * (thin(s) ? 104 : 52) < single * 256) p->chain = ceil_div(s.L, kTile);
         } else if (blocks > 0 && blocks < 96) {
-            // Runs, which read what the decays hang on twice, where even narrow workgroups leave CUs idle, of eight
-            // tiles at least (bf16 1 x 8192 x 2560, us with and without: 160 and 265).
-            const int64_t most = s.L / (8 * kTile);
-            want = 512 / blocks < most ? 512 / blocks : most;
+            // Runs, which read what the decays hang on twice, where even narrow workgroups leave CUs idle: for one round of
+            // workgroups over the CUs, or for two and a half where that makes less than four runs; of two tiles at least
+            // (bf16, us, without and with runs: 1 x 16384 x 512 32 runs 68, 24 81, 48 89; 1 x 16384 x 1024 16 runs 101, 12
+            // 127, 20 150; 1 x 8192 x 2560 270, 6 runs 130, 8 168, 16 136; 1 x 8192 x 5120 288, 8 runs 237; 8 x 2048 x 64 67,
+            // 8 runs 46, 16 53).
+            const int64_t most = ceil_div(s.L, 2 * kTile);
+            want = blocks <= 64 ? 256 / blocks : 640 / blocks;
+            want = want < most ? want : most;
+            if (want < 4) want = 1;
         }
     }
     if (want > 1 && s.L > kTile) {

@@ -1024,8 +1024,8 @@ def _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate) ->
                     ("pre_bias", pre_bias)):
         _req(t, name, torch.float32, (C,), dev)
     if gate is not None:
-        if gate.dim() != 2:
-            raise ValueError("gate must be [gate_rows, channels]")
+        if gate.dim() != 2 or gate.shape[0] < 1:
+            raise ValueError("gate must be [gate_rows, channels], of at least one row")
         _req(gate, "gate", torch.float32, (gate.shape[0], C), dev)
     return AddnormOpts(_ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), _ptr(gate), None, 0)
 
@@ -1075,6 +1075,16 @@ def addnorm(x: torch.Tensor, res: Optional[torch.Tensor] = None, *, pre: str = "
     return y, res_out, stats
 
 
+@functools.lru_cache(maxsize=256)
+def _addnorm_need(rows: int, C: int, gate_rows: int, dt: int, rt: int, post: int, pre: int, wanted: int) -> int:
+    """Bytes of workspace of addnorm_bwd; ``wanted``: a bit for each field of AddnormGrads."""
+    dims, n = AddnormDims(rows, C, gate_rows, dt, rt, post, pre, 0.0, 1.0, 1.0), ctypes.c_uint64(0)
+    grads = AddnormGrads(*(16 if wanted >> i & 1 else None for i in range(5)))
+    _check(lib.selscan_addnorm_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(AddnormOpts(gate=16 if gate_rows else None)),
+                                                  ctypes.byref(grads), ctypes.byref(n)))
+    return int(n.value)
+
+
 def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, dy: Optional[torch.Tensor],
                 dres_out: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor], pre: str = "rms",
                 pre_weight: Optional[torch.Tensor] = None, pre_bias: Optional[torch.Tensor] = None,
@@ -1090,7 +1100,7 @@ def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, d
     ``want_dparams``, dpost_weight, dpost_bias, dpre_weight, dpre_bias [channels]
     and dgate (like gate), all fp32, of the parameters that are given. ``x`` may
     be None where there is neither a post norm nor a gate whose gradient is
-    wanted, ``res_out`` with pre "none".
+    wanted; with pre "none" ``res_out`` and ``dy`` must be None.
     """
     like = next((t for t in (dy, x, res_out, dres_out) if t is not None), None)
     if like is None or like.dim() < 1:
@@ -1116,12 +1126,11 @@ def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, d
             _req(out["dres"], "dres", rt, shape, dev)
         if want_dparams:
             out.update({"d" + n: torch.empty_like(p) for n, p in params.items() if p is not None})
-        grads = AddnormGrads(*(_ptr(out.get("d" + n)) for n in ("post_weight", "post_bias", "pre_weight", "pre_bias",
-                                                                "gate")))
-        need = ctypes.c_uint64(0)
-        _check(lib.selscan_addnorm_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(grads),
-                                                      ctypes.byref(need)))
-        workspace = _scratch(workspace, int(need.value), dev)
+        names = ("dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias", "dgate")
+        grads = AddnormGrads(*(_ptr(out.get(n)) for n in names))
+        need = _addnorm_need(rows, C, dims.gate_rows, dims.dtype, dims.res_dtype, dims.post, dims.pre,
+                             sum(1 << i for i, n in enumerate(names) if n in out))
+        workspace = _scratch(workspace, need, dev)
         if workspace is not None:
             opts.workspace, opts.workspace_bytes = workspace.data_ptr(), workspace.numel()
         _check(lib.selscan_addnorm_bwd(_ptr(x), _ptr(res_out), _ptr(stats), _ptr(dy), _ptr(dres_out),

@@ -145,6 +145,31 @@ def test_gated_workspace():
     assert gbwd(d, ws=P(0), ws_bytes=need) == S.ERR_ALIAS
 
 
+def test_gated_automatic_splits():
+    """Chained tiles where channels are few and tokens many (workspace: two words a tile and channel, one a link of 8
+    tiles); runs of tokens backward (a stretch and a state each)."""
+    def forward(**kw):
+        return gated_size(ga(**kw), False)[1]
+
+    assert forward(batch=1, seqlen=1024, dim=64) == 0      # too short to pay for it
+    assert forward(batch=8, seqlen=4096, dim=4096) == 0    # two workgroups for every CU
+    assert forward(batch=2, seqlen=4096, dim=4096) == 0    # narrow ones fill the CUs
+    tiles, rows = 32, 2 * 64
+    assert 0 <= forward(seqlen=4096) - (2 * tiles + 4) * rows * 8 - 256 - rows * 4 < 1024
+    assert forward(seqlen=4097) > forward(seqlen=4096)
+
+    def runs(**kw):  # one run needs no workspace with checkpoints and no dA
+        d = ga(kind=S.GATED_MIX, **kw)
+        return gated_size(d, True, ckpt=True)[1] / (d.batch * d.dim * 24)
+
+    assert runs(batch=8, seqlen=4096, dim=4096) == 0
+    assert runs(batch=1, seqlen=512, dim=64) == 0
+    assert runs(batch=1, seqlen=16384, dim=512) == 32
+    assert runs(batch=8, seqlen=2048, dim=64) == 8
+    assert gated_size(ga(batch=1 << 18, dim=8), False, segments=65536)[0] == S.OK      # 100 tokens: one tile
+    assert gated_size(ga(batch=1 << 18, dim=8, seqlen=1 << 14), False, segments=64)[0] == S.ERR_DIMS
+
+
 def an(rows=12, channels=64, gate_rows=3, dtype=S.BF16, res_dtype=S.F32, post=1, pre=2, eps=1e-5, scale=1.0,
        res_scale=1.0):
     return S.AddnormDims(rows, channels, gate_rows, dtype, res_dtype, post, pre, eps, scale, res_scale)
@@ -339,7 +364,7 @@ def test_binding_refusals():
     x = z(6, 8)
     for a, kw, e in (((x, z(6, 7)), {}, ValueError), ((x, x.bfloat16()), dict(pre="rms"), S.SelscanError),
                      ((x,), dict(pre="batch"), ValueError), ((x,), dict(pre_weight=z(7)), ValueError),
-                     ((x,), dict(gate=z(8)), ValueError), ((x,), dict(gate=z(2, 7)), ValueError),
+                     ((x,), dict(gate=z(8)), ValueError), ((x,), dict(gate=z(0, 8)), ValueError), ((x,), dict(gate=z(2, 7)), ValueError),
                      ((x.half(),), {}, TypeError), ((x.t(),), {}, ValueError), ((x,), {}, ValueError)):
         with pytest.raises((e, ValueError) if e is S.SelscanError else e):
             S.addnorm(*a, **kw)
