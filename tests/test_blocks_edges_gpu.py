@@ -1,0 +1,67 @@
+"""The recurrence on the GPU in runs without tokens, and in two calls at once."""
+import pytest
+import torch
+
+from blocks_util import check_bwd, check_fwd, make, np_of
+from selective_state_space_48_amd import selscan
+
+pytestmark = pytest.mark.gpu
+
+
+def case(msg):
+    print(f"[case] {msg}", flush=True)
+
+
+@pytest.mark.parametrize("kind", ["mix", "decay"])
+def test_runs_without_tokens(kind):
+    """Runs that lie behind an entry's length leave its state as it was, whatever ran on the CUs before."""
+    B, L, D = 64, 2100, 130
+    big = make(B, 600, D, kind, torch.float32, seed=1, h0=True)
+    big["h0"] = big["h0"] * 1e30
+    lengths = [0, 1, 255, 256, 257, 700, 2100, 0] * (B // 8)
+    p = make(B, L, D, kind, torch.float32, seed=2, h0=True, lengths=lengths, grads=True)
+    q = np_of(p)
+    args = (p["x"], p["g"], p["r"], p["A"])
+    empty = [b for b in range(B) if lengths[b] == 0]
+    for segments in (8, 3):
+        case(f"runs without tokens {kind} {segments}")
+        selscan.gated_fwd(big["x"], big["g"], big["r"], big["A"], h0=big["h0"])
+        y, last = selscan.gated_fwd(*args, h0=p["h0"], lengths=p["lengths"], segments=segments)
+        selscan.gated_fwd(big["x"], big["g"], big["r"], big["A"], h0=big["h0"])
+        r = selscan.gated_bwd(*args, dy=p["dy"], h0=p["h0"], lengths=p["lengths"], dlast_state=p["dlast"],
+                              segments=segments, want_dh0=True)
+        torch.cuda.synchronize()
+        assert torch.equal(last[empty], p["h0"][empty]) and torch.equal(r["dh0"][empty], p["dlast"][empty])
+        check_fwd(y, last, q, f"runs without tokens {kind} {segments}")
+        check_bwd(r, q, f"runs without tokens {kind} {segments}")
+
+
+@pytest.mark.parametrize("kind", ["mix", "decay"])
+def test_two_calls_at_once(kind):
+    """Chained calls, calls in runs and their gradients on two streams at once give what they give alone."""
+    p = make(1, 9000, 700, kind, torch.bfloat16, seed=3, z=True, h0=True, grads=True)
+    args = (p["x"], p["g"], p["r"], p["A"], p["z"])
+
+    def both(segments):
+        y, last = selscan.gated_fwd(*args, h0=p["h0"], segments=segments)
+        r = selscan.gated_bwd(*args, dy=p["dy"], h0=p["h0"], dlast_state=p["dlast"], segments=segments, want_dh0=True)
+        return [y, last, *(r[k] for k in sorted(r))]
+
+    case(f"two calls at once {kind}")
+    want = {s: both(s) for s in (0, 4)}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        for st, s in zip(streams, (0, 0)):
+            with torch.cuda.stream(st):
+                got.append((s, both(s)))
+    for st, s in zip(streams, (0, 4)):
+        with torch.cuda.stream(st):
+            got.append((s, both(s)))
+    torch.cuda.synchronize()
+    for s, outs in got:
+        for a, b in zip(outs, want[s]):
+            assert torch.equal(a, b)
