@@ -275,7 +275,7 @@ __global__ __launch_bounds__(!WIDE ? 256 : KEEP ? 512 : 1024) void fwd_kernel(An
 enum { kPreW = 0, kPostW = 1, kPreB = 2, kPostB = 3 };
 
 // SUMS false (rows of more than 512 threads, whose registers the sums would not fit): the rows alone, and their
-// averages for cols_kernel.
+// averages for cols_kernel, which then writes dres.
 template <typename T, typename S, int K, bool WIDE, bool BIAS, bool GATE, bool SUMS>
 __global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(AnArgs a) {
     __shared__ float red[2][2][16];
@@ -410,7 +410,7 @@ __global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(An
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
-                if (t.dres) {
+                if (t.dres && (SUMS || !a.averages)) {
                     float o[kV];
 #pragma unroll
                     for (int i = 0; i < kV; ++i) o[i] = a.res_scale * ds[k][i];
@@ -469,7 +469,7 @@ __global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(An
 }
 
 // The sums over rows where bwd_kernel does not form them: a thread takes a vector of columns down the rows of its
-// workgroup (grid x), from the averages that bwd_kernel left.
+// workgroup (grid x), from the averages that bwd_kernel left. It writes dres too, which may stand in dsum's place.
 template <typename T, typename S>
 __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
     const AddnormTensors& t = a.t;
@@ -516,6 +516,12 @@ __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
                 acc[kPreB][i] += dy[i];
                 ds[i] = fmaf(st[3], dy[i] * w2[i] - a1 - xh * a2, ds[i]);
             }
+        }
+        if (t.dres) {
+            float o[kV];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) o[i] = a.res_scale * ds[i];
+            store<S>(t.dres, at, n, o);
         }
 #pragma unroll
         for (int i = 0; i < kV; ++i) {

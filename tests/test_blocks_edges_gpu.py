@@ -1,8 +1,9 @@
-"""The recurrence on the GPU in runs without tokens, and in two calls at once."""
+"""The recurrence, the norms and the rotary positions on the GPU in calls that meet each other: outputs in place of
+inputs, runs without tokens, two calls at once."""
 import pytest
 import torch
 
-from blocks_util import check_bwd, check_fwd, make, np_of
+from blocks_util import DT, check_bwd, check_fwd, make, np_of
 from selective_state_space_48_amd import selscan
 
 pytestmark = pytest.mark.gpu
@@ -10,6 +11,35 @@ pytestmark = pytest.mark.gpu
 
 def case(msg):
     print(f"[case] {msg}", flush=True)
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("C", [100, 2560, 8192, 8200, 16384])
+def test_norm_gradients_in_place(C, types):
+    """dres in place of dres_out gives what dres beside it gives, where the sums over rows are a launch of their own
+    too (they need dres_out)."""
+    dt, rt = DT[types[0]], DT[types[1]]
+    R, gates = 6, 3
+    g = torch.Generator().manual_seed(1)
+    rn = lambda *s, d=torch.float32: torch.randn(s, generator=g).to(d).cuda()  # noqa: E731
+    x, res, dy, ds, gate = rn(R, C, d=dt), rn(R, C, d=rt), rn(R, C, d=dt), rn(R, C, d=rt), rn(gates, C)
+    for post, pre in (("layer", "rms"), ("rms", "none")):
+        w = dict(post_weight=rn(C), post_bias=rn(C), pre_weight=rn(C) if pre != "none" else None,
+                 pre_bias=rn(C) if pre != "none" else None, gate=gate)
+        kw = dict(pre=pre, post=post, scale=0.5, res_scale=0.25, **w)
+        case(f"{C} {types} {post} {pre}")
+        _, s, stats = selscan.addnorm(x, res, **kw)
+        if pre == "none":
+            args, bw = (x, None), dict(dy=None, stats=stats, **kw)
+        else:
+            args, bw = (x, s), dict(dy=dy, stats=stats, **kw)
+        want = selscan.addnorm_bwd(*args, dres_out=ds, **bw)
+        own = ds.clone()
+        got = selscan.addnorm_bwd(*args, dres_out=own, dres=own, **bw)
+        torch.cuda.synchronize()
+        assert got["dres"].data_ptr() == own.data_ptr()
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
 
 
 @pytest.mark.parametrize("kind", ["mix", "decay"])
