@@ -707,7 +707,7 @@ int selscan_groupnorm_workspace_size(const selscan_groupnorm_dims_t* dims, int32
  *                   the logarithm of the channel's smallest decay per token.
  *                   Above 0, where 1 - a^2 < 0, the state is a NaN
  *   last_state    : [B, D] fp32 output or NULL
- * dims: L < 2^27; D <= 2^20; B * ceil(D / 8) * segments <= 4194304 (else
+ * dims: L < 2^27; D <= 2^20; B and B * ceil(D / 8) * segments <= 4194304 (else
  * SELSCAN_ERR_DIMS). Fully fp32 arithmetic on values that are rounded once;
  * 1 - a and sqrt(1 - a^2) are formed without cancellation, and the state that
  * passes from tile to tile of tokens is held in 64 bits. Tokens behind an
@@ -944,9 +944,9 @@ int selscan_addnorm_bwd_workspace_size(const selscan_addnorm_dims_t* dims,
  *               context where that is wanted
  *   positions : [B, L] int32 or NULL
  * dims: 0 < rot <= W <= 4096, rot even (else SELSCAN_ERR_DSTATE); L < 2^27; B L
- * (H + Hkv) < 2^38; (H + Hkv) W <= 2^22; -2^31 < offset < 2^31; scale finite, 0 means 1. The angle
- * is formed in 64 bits and its whole turns taken off, so that far positions
- * keep fp32 accuracy. q_out may be q itself and k_out k; otherwise outputs must
+ * (H + Hkv) < 2^38; (H + Hkv) W <= 2^22; -2^31 < offset < 2^31; scale finite, 0
+ * means 1. The angle is formed in 64 bits and its whole turns taken off, so that
+ * far positions keep fp32 accuracy (angles below 2^27; 2^-20 at 2^31). q_out may be q itself and k_out k; otherwise outputs must
  * not overlap inputs or each other. No workspace. Deterministic.
  */
 #define SELSCAN_ROTARY_HALF 0

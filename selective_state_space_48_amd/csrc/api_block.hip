@@ -37,7 +37,7 @@ int check_gated(const selscan_gated_dims_t* d, bool step, GatedShape* s) {
     if (d->kind != SELSCAN_GATED_MIX && d->kind != SELSCAN_GATED_DECAY) return SELSCAN_ERR_CONFIG;
     int64_t t;
     // one workgroup or more for every 8 channels of an entry
-    if (!mul_ok(d->batch, (d->dim + 7) / 8, &t) || t > (int64_t(1) << 22)) return SELSCAN_ERR_DIMS;
+    if (!mul_ok(d->batch, d->dim > 8 ? (d->dim + 7) / 8 : 1, &t) || t > (int64_t(1) << 22)) return SELSCAN_ERR_DIMS;
     if (!mul_ok(d->batch * d->dim, L, &t) || !mul_ok(t, 4, &t)) return SELSCAN_ERR_DIMS;
     *s = GatedShape{d->batch, L, d->dim, dtype_of(d->dtype), d->kind};
     return SELSCAN_OK;
@@ -60,7 +60,8 @@ int check_addnorm(const selscan_addnorm_dims_t* d, const float* gate, bool forwa
     if (!d) return SELSCAN_ERR_NULL;
     if (d->rows < 0 || d->channels < 0 || d->rows >= (int64_t(1) << 31) || d->channels > 16384)
         return SELSCAN_ERR_DIMS;
-    if (gate && (d->gate_rows < 1 || d->rows % d->gate_rows)) return SELSCAN_ERR_DIMS;
+    if (gate && (d->gate_rows < 1 || d->gate_rows >= (int64_t(1) << 31) || d->rows % d->gate_rows))
+        return SELSCAN_ERR_DIMS;
     if (!known_dtype(d->dtype) || (d->res_dtype != SELSCAN_F32 && d->res_dtype != d->dtype)) return SELSCAN_ERR_DTYPE;
     for (const int32_t n : {d->post, d->pre})
         if (n < SELSCAN_NORM_NONE || n > SELSCAN_NORM_LAYER) return SELSCAN_ERR_CONFIG;
@@ -306,9 +307,7 @@ int selscan_addnorm_bwd(const void* x, const void* sum, const float* stats, cons
     if (n == 0) {  // no terms
         for (float* p : {gr.dpost_weight, gr.dpost_bias, gr.dpre_weight, gr.dpre_bias})
             if (p && s.C > 0 && launch_fill_zero(p, s.C, st) != hipSuccess) return SELSCAN_ERR_LAUNCH;
-        if (gr.dgate && s.G * s.C > 0 && launch_fill_zero(gr.dgate, s.G * s.C, st) != hipSuccess)
-            return SELSCAN_ERR_LAUNCH;
-        return SELSCAN_OK;
+        return done(pass_state(gr.dgate, nullptr, s.G * s.C, st));
     }
     t.x = x; t.sum = const_cast<void*>(sum); t.stats = const_cast<float*>(stats);
     t.dy = dy; t.dsum = dres_out; t.dx = dx; t.dres = dres;

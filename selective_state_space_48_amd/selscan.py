@@ -1056,10 +1056,10 @@ def addnorm(x: torch.Tensor, res: Optional[torch.Tensor] = None, *, pre: str = "
     for n in shape[:-1]:
         rows *= n
     rt = res.dtype if res is not None else res_out.dtype if res_out is not None else res_dtype or dt
+    opts = _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate)
     dims = _addnorm_dims(rows, C, dt, rt, pre, post, gate, eps, scale, res_scale)
     _req(x, "x", dt, None, dev)
     _req(res, "res", rt, shape, dev)
-    opts = _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate)
     with _device(dev):
         if y is not None:
             _req(y, "y", dt, shape, dev)
@@ -1111,11 +1111,11 @@ def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, d
     rows = 1
     for n in shape[:-1]:
         rows *= n
+    opts = _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate)
     dims = _addnorm_dims(rows, C, dt, rt, pre, post, gate, 0.0, scale, res_scale)
     for t, name, tt in ((x, "x", dt), (dy, "dy", dt), (res_out, "res_out", rt), (dres_out, "dres_out", rt)):
         _req(t, name, tt, shape, dev)
     _req(stats, "stats", torch.float32, (rows, 4), dev)
-    opts = _addnorm_opts(C, dev, post_weight, post_bias, pre_weight, pre_bias, gate)
     params = dict(post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight, pre_bias=pre_bias, gate=gate)
     with _device(dev):
         out = {}

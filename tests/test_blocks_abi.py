@@ -397,3 +397,26 @@ def test_rotary_frequencies():
                dict(rot=8, scaling="parts"), dict(rot=8, scaling="cubic")):
         with pytest.raises(ValueError):
             S.rotary_frequencies(**kw)
+
+
+@pytest.mark.parametrize("call", [gfwd, gstep, gbwd])
+def test_gated_entries_without_channels(call):
+    """The bound on entries holds without channels too, where no product of sizes says anything."""
+    assert call(ga(batch=(1 << 22) + 1, dim=0)) == S.ERR_DIMS
+    assert call(ga(batch=1 << 62, dim=0)) == S.ERR_DIMS
+
+
+@pytest.mark.parametrize("call", [anorm, anorm_bwd])
+def test_addnorm_gates_without_rows(call):
+    """Any number of gate rows divides no rows; it is bounded as rows are."""
+    for gates in (1 << 31, 1 << 62):
+        assert call(an(rows=0, gate_rows=gates)) == S.ERR_DIMS
+
+
+def test_gate_without_axes():
+    x = torch.zeros(6, 8)
+    for gate in (torch.zeros(()), torch.zeros(2, 3, 8)):
+        with pytest.raises(ValueError):
+            S.addnorm(x, gate=gate)
+        with pytest.raises(ValueError):
+            S.addnorm_bwd(x, x, dy=x, stats=torch.zeros(6, 4), gate=gate)
