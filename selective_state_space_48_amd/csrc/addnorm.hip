@@ -11,8 +11,8 @@
 // what its rows give to the gradients of weights, biases and gate in registers and
 // writes them once; join_kernel adds the workgroups' parts in order.
 //
-// 16384 x 4096 bf16, both norms, residual fp32: 162 us (5.0 TB/s, the rate of a large
-// copy); gradients with biases and 8 gate rows, residual bf16: 187 (4.4 with the parts).
+// 16384 x 4096 bf16, both norms, residual fp32: 147 us (5.5 TB/s; a large copy has 4.9);
+// gradients with biases and 8 gate rows, residual bf16: 172 (4.8 with the parts).
 #include "../../include/selscan.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -111,42 +111,60 @@ __device__ __forceinline__ void weights(const float* w, int64_t at, int n, float
     }
 }
 
+// Sums over the lanes of a wave, by moves inside the vector unit: every lane adds its partner's value (neighbours,
+// then pairs, quads, ...), so that all end with the same bits. M: lanes that are summed, a power of two.
+template <int CTRL> __device__ __forceinline__ float partner(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float add_16(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+}
+__device__ __forceinline__ float add_32(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+}
+__device__ __forceinline__ void lane_sums(int m, float& a, float& b) {
+    if (m < 2) return;
+    a += partner<0xB1>(a); b += partner<0xB1>(b);      // the neighbour
+    if (m < 4) return;
+    a += partner<0x4E>(a); b += partner<0x4E>(b);      // the other pair of four
+    if (m < 8) return;
+    a += partner<0x141>(a); b += partner<0x141>(b);    // mirrored in eight
+    if (m < 16) return;
+    a += partner<0x140>(a); b += partner<0x140>(b);   // mirrored in sixteen
+    if (m < 32) return;
+    a = add_16(a); b = add_16(b);
+    if (m < 64) return;
+    a = add_32(a); b = add_32(b);
+}
+
 // A thread's place, and sums over a row: in the lanes of a wave (WIDE false), or over the workgroup.
 template <bool WIDE> struct Row {
     int l, ri, step, lanes;
-    float (*red)[2][16];
+    float2 (*red)[16];
     int slot = 0;
-    __device__ __forceinline__ Row(int lanes_, float (*red_)[2][16]) : lanes(lanes_), red(red_) {
+    __device__ __forceinline__ Row(int lanes_, float2 (*red_)[16]) : lanes(lanes_), red(red_) {
         l = WIDE ? threadIdx.x : threadIdx.x % lanes;
         ri = WIDE ? 0 : threadIdx.x / lanes;
         step = WIDE ? 1 : 256 / lanes;
     }
     __device__ __forceinline__ void sums(float& a, float& b) {
         if constexpr (WIDE) {
-#pragma unroll
-            for (int m = 32; m; m >>= 1) {
-                a += __shfl_xor(a, m, 64);
-                b += __shfl_xor(b, m, 64);
-            }
-            const int waves = blockDim.x / 64;
-            if (threadIdx.x % 64 == 0) {
-                red[slot][0][threadIdx.x / 64] = a;
-                red[slot][1][threadIdx.x / 64] = b;
-            }
+            lane_sums(64, a, b);
+            if (threadIdx.x % 64 == 0) red[slot][threadIdx.x / 64] = {a, b};
             __syncthreads();
-            a = red[slot][0][0];
-            b = red[slot][1][0];
-            for (int i = 1; i < waves; ++i) {
-                a += red[slot][0][i];
-                b += red[slot][1][i];
-            }
+            const uint32_t i = threadIdx.x % 16;
+            const float2 w = i < blockDim.x / 64 ? red[slot][i] : float2{0.0f, 0.0f};
+            a = w.x;
+            b = w.y;
+            lane_sums(16, a, b);
             // an entry is written again only behind a barrier that follows every read of it
             slot ^= 1;
         } else {
-            for (int m = lanes / 2; m; m >>= 1) {
-                a += __shfl_xor(a, m, 64);
-                b += __shfl_xor(b, m, 64);
-            }
+            lane_sums(lanes, a, b);
         }
     }
     __device__ __forceinline__ float sum(float a) {
@@ -182,13 +200,16 @@ __device__ __forceinline__ void statistics(int kind, const float (&v)[K][kV], co
 #pragma unroll
             for (int i = 0; i < kV; ++i) s = fmaf(v[k][i], v[k][i], s);
     }
-    *rstd = 1.0f / sqrtf(row.sum(s) * inv + eps);
+    // (off by one rounding; what it would flush is left to the root and the division)
+    const float q = row.sum(s) * inv + eps;
+    *rstd = q < 1e-36f ? 1.0f / sqrtf(q) : __builtin_amdgcn_rsqf(q);
 }
 
-// KEEP: weights and the next row's loads stay in registers, which takes at most 512 threads a row.
-template <typename T, typename S, int K, bool WIDE, bool KEEP>
-__global__ __launch_bounds__(!WIDE ? 256 : KEEP ? 512 : 1024) void fwd_kernel(AnArgs a) {
-    __shared__ float red[2][2][16];
+// K: vectors of a thread. With one, weights and the next row's loads stay in registers.
+template <typename T, typename S, int K, bool WIDE>
+__global__ __launch_bounds__(WIDE ? 1024 : 256) void fwd_kernel(AnArgs a) {
+    constexpr bool KEEP = K == 1;
+    __shared__ float2 red[2][16];
     Row<WIDE> row(a.lanes, red);
     const AddnormTensors& t = a.t;
     const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
@@ -237,15 +258,27 @@ __global__ __launch_bounds__(!WIDE ? 256 : KEEP ? 512 : 1024) void fwd_kernel(An
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int64_t c = int64_t(row.l + a.lanes * k) * kV;
-            float g[kV], b[kV];
-            weights(t.gate ? t.gate + r / a.per_gate * a.C : nullptr, c, n[k], 1.0f, g);
-            weights(post ? t.post_b : nullptr, c, n[k], 0.0f, b);
-            float (&w)[kV] = w1[KEEP ? k : 0];
-            if constexpr (!KEEP) weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w);
+            float (&u)[kV] = v[k];
+            if (post) {
+                float (&w)[kV] = w1[KEEP ? k : 0];
+                if constexpr (!KEEP) weights(t.post_w, c, n[k], 1.0f, w);
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const float u = post ? fmaf((v[k][i] - m1) * r1, w[i], b[i]) : v[k][i];
-                s[k][i] = fmaf(u, a.scale * g[i], s[k][i]);
+                for (int i = 0; i < kV; ++i) u[i] = (u[i] - m1) * r1 * w[i];
+                if (t.post_b) {
+                    float b[kV];
+                    load<float>(t.post_b, c, n[k]).get(b);
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) u[i] += b[i];
+                }
+            }
+            if (t.gate) {
+                float g[kV];
+                load<float>(t.gate + r / a.per_gate * a.C, c, n[k]).get(g);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) s[k][i] = fmaf(u[i], a.scale * g[i], s[k][i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kV; ++i) s[k][i] = fmaf(u[i], a.scale, s[k][i]);
             }
             if (t.sum) store<S>(t.sum, r * a.C + c, n[k], s[k]);
         }
@@ -254,12 +287,17 @@ __global__ __launch_bounds__(!WIDE ? 256 : KEEP ? 512 : 1024) void fwd_kernel(An
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int64_t c = int64_t(row.l + a.lanes * k) * kV;
-                float y[kV], b[kV];
-                weights(t.pre_b, c, n[k], 0.0f, b);
+                float y[kV];
                 float (&w)[kV] = w2[KEEP ? k : 0];
                 if constexpr (!KEEP) weights(t.pre_w, c, n[k], 1.0f, w);
 #pragma unroll
-                for (int i = 0; i < kV; ++i) y[i] = fmaf((s[k][i] - m2) * r2, w[i], b[i]);
+                for (int i = 0; i < kV; ++i) y[i] = (s[k][i] - m2) * r2 * w[i];
+                if (t.pre_b) {
+                    float b[kV];
+                    load<float>(t.pre_b, c, n[k]).get(b);
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) y[i] += b[i];
+                }
                 if (t.y) store<T>(t.y, r * a.C + c, n[k], y);
             }
         }
@@ -274,11 +312,16 @@ __global__ __launch_bounds__(!WIDE ? 256 : KEEP ? 512 : 1024) void fwd_kernel(An
 // The sums that the backward pass forms over rows, by what is wanted of them: weights (0, 1), biases (2, 3).
 enum { kPreW = 0, kPostW = 1, kPreB = 2, kPostB = 3 };
 
-// SUMS false (rows of more than 512 threads, whose registers the sums would not fit): the rows alone, and their
-// averages for cols_kernel, which then writes dres.
-template <typename T, typename S, int K, bool WIDE, bool BIAS, bool GATE, bool SUMS>
-__global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(AnArgs a) {
-    __shared__ float red[2][2][16];
+// ROWS: rows in a wave's lanes, of up to 512, 768 or 1024 threads (256, 168 and 128 registers), or of threads whose
+// registers the sums do not fit, one vector each or two: the rows alone, and their averages for cols_kernel, which then
+// writes dres.
+enum { kLanes, k512, k768, k1024, kApart, kApart2 };
+template <typename T, typename S, int ROWS, bool BIAS, bool GATE>
+__global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS == k768 ? 768 : 1024,
+                             ROWS == kLanes && sizeof(S) == 2 && !BIAS && !GATE ? 4 : 1) void bwd_kernel(AnArgs a) {
+    constexpr bool WIDE = ROWS != kLanes, SUMS = ROWS < kApart;
+    constexpr int K = ROWS == kApart2 ? 2 : 1;
+    __shared__ float2 red[2][16];
     __shared__ float cols[WIDE ? 1 : 256 * kV];
     Row<WIDE> row(a.lanes, red);
     const AddnormTensors& t = a.t;
@@ -348,6 +391,18 @@ __global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(An
 #pragma unroll
             for (int i = 0; i < 4; ++i) nst[i] = t.stats[r * 4 + i];
     };
+    // What else a row's vector needs: the gradient from behind, and x (normed by post).
+    auto passed = [&](int k, float m1, float q1, float (&ds)[kV], float (&x1)[kV]) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) ds[i] = x1[i] = 0.0f;
+        if (t.dsum) nd[k].get(ds);
+        if (use_x) {
+            nx[k].get(x1);
+            if (post)
+#pragma unroll
+                for (int i = 0; i < kV; ++i) x1[i] = i < n[k] ? (x1[i] - m1) * q1 : 0.0f;
+        }
+    };
     for (int64_t g0 = r0; g0 < r1;) {
         const int64_t gi = g0 / a.per_gate, end = (gi + 1) * a.per_gate, g1 = end < r1 ? end : r1;
         float gate[GATE ? KW : 1][kV];
@@ -361,23 +416,23 @@ __global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(An
         int64_t r = g0 + row.ri;
         if (SUMS && r < g1) fetch(r);
         for (; r < g1; r += row.step) {
-            if (!SUMS) fetch(r);
+            // (without the sums two vectors' values would spill: each tensor is loaded where it is needed)
+            if (!SUMS && t.stats)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) nst[i] = t.stats[r * 4 + i];
             float ds[K][kV], xh[K][kV], e[K][kV], x1[K][kV];
             const float m1 = nst[0], q1 = nst[1], m2 = nst[2], q2 = nst[3];
             float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-#pragma unroll
-                for (int i = 0; i < kV; ++i) ds[k][i] = x1[k][i] = 0.0f;
-                if (t.dsum) nd[k].get(ds[k]);
-                if (use_x) {
-                    nx[k].get(x1[k]);
-                    if (post)
-#pragma unroll
-                        for (int i = 0; i < kV; ++i) x1[k][i] = i < n[k] ? (x1[k][i] - m1) * q1 : 0.0f;
-                }
+                if constexpr (SUMS) passed(k, m1, q1, ds[k], x1[k]);
                 if (pre) {
                     float dy[kV];
+                    if constexpr (!SUMS) {
+                        const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
+                        ns[k] = load<S>(t.sum, at, n[k]);
+                        ny[k] = load<T>(t.dy, at, n[k]);
+                    }
                     ns[k].get(xh[k]);
                     ny[k].get(dy);
                     float (&w)[kV] = w2[SUMS ? k : 0];
@@ -404,8 +459,22 @@ __global__ __launch_bounds__(!WIDE ? 256 : SUMS ? 512 : 1024) void bwd_kernel(An
 #pragma unroll
                 for (int k = 0; k < K; ++k)
 #pragma unroll
-                    for (int i = 0; i < kV; ++i) ds[k][i] = fmaf(q2, e[k][i] - a1 - xh[k][i] * a2, ds[k][i]);
+                    for (int i = 0; i < kV; ++i) {
+                        e[k][i] = q2 * (e[k][i] - a1 - xh[k][i] * a2);
+                        if constexpr (SUMS) ds[k][i] += e[k][i];
+                    }
             }
+            if constexpr (!SUMS)
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
+                    if (use_x) nx[k] = load<T>(t.x, at, n[k]);
+                    if (t.dsum) nd[k] = load<S>(t.dsum, at, n[k]);
+                    passed(k, m1, q1, ds[k], x1[k]);
+                    if (pre)
+#pragma unroll
+                        for (int i = 0; i < kV; ++i) ds[k][i] += e[k][i];
+                }
             s1 = s2 = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -578,9 +647,11 @@ __global__ __launch_bounds__(1024) void join_kernel(JoinArgs a) {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Threads of a row: K vectors each; a power of two up to a wave, then whole waves.
-int lanes_of(int64_t C, int K) {
-    const int64_t v = ceil_div(C, int64_t(kV) * K);
+// Threads of a row: a power of two up to a wave, then whole waves; a vector each in rows of up to kOne values, else two
+// (8192 x 5120 bf16 136 us in two, 61 in one).
+constexpr int64_t kOne = 1024 * kV;
+int lanes_of(int64_t C) {
+    const int64_t v = ceil_div(C, C <= kOne ? kV : 2 * kV);
     if (v > 64) return int(ceil_div(v, 64) * 64);
     int n = 1;
     while (n < v) n *= 2;
@@ -604,8 +675,8 @@ template <typename F> void dispatch(const AddnormShape& s, F f) {
 
 // The backward's workgroups: their rows, and where their sums go.
 struct BwdPlan {
-    int K, lanes, sums;
-    bool wide, apart;  // apart: the sums in a launch of their own
+    int rows, lanes, sums;  // rows: kLanes, ...
+    bool apart;             // the sums in a launch of their own
     int64_t runs, per, blocks;
     size_t part, part2, gate, averages, bytes;  // places in the workspace
 };
@@ -614,13 +685,15 @@ bool row_sums(const AddnormTensors& w) { return w.dpre_w || w.dpost_w || w.dpre_
 
 BwdPlan bwd_plan(const AddnormShape& s, const AddnormTensors& w) {
     BwdPlan p{};
-    p.K = s.C <= 4096 ? 1 : 2;
-    p.lanes = lanes_of(s.C, p.K);
-    p.wide = p.lanes > 64;
-    p.apart = p.lanes > 512;
-    const int64_t step = p.wide ? 1 : 256 / p.lanes, groups = s.G ? s.G : 1, rows = s.R / groups;
+    p.lanes = lanes_of(s.C);
+    const bool wide = p.lanes > 64;
+    p.sums = w.dpre_b || w.dpost_b ? 4 : 2;
+    p.rows = !wide ? kLanes : p.lanes <= 512 ? k512 : s.C > kOne ? kApart2 : p.lanes <= 768 ? k768
+             : !s.G && p.sums == 2 ? k1024 : kApart;
+    p.apart = p.rows >= kApart;
+    const int64_t step = wide ? 1 : 256 / p.lanes, groups = s.G ? s.G : 1, rows = s.R / groups;
     // workgroups for 512 threads a CU
-    const int64_t want = 256 * (p.wide ? ceil_div(512, p.lanes) : 4);
+    const int64_t want = 256 * (wide ? ceil_div(512, p.lanes) : 4);
     // A thread's sums of 256 rows at most (more where that would take more than 2^20 workgroups), so that long sums
     // lose no more than short ones.
     int64_t most = ceil_div(s.R, int64_t(1) << 20);
@@ -636,7 +709,6 @@ BwdPlan bwd_plan(const AddnormShape& s, const AddnormTensors& w) {
         p.blocks = ceil_div(of, p.per) * g;
         p.runs = w.dgate ? ceil_div(of, p.per) : 0;
     }
-    p.sums = w.dpre_b || w.dpost_b ? 4 : 2;
     size_t at = 0;
     if (row_sums(w)) {
         at += up256(size_t(p.blocks) * p.sums * s.C * sizeof(float));
@@ -659,19 +731,19 @@ size_t addnorm_bwd_workspace_bytes(const AddnormShape& s, const AddnormTensors& 
 
 hipError_t launch_addnorm(const AddnormTensors& t, const AddnormShape& s, hipStream_t stream) {
     AnArgs a = args_of(t, s);
-    const int K = s.C <= 4096 ? 1 : 2;
-    a.lanes = lanes_of(s.C, K);
+    a.lanes = lanes_of(s.C);
     const bool wide = a.lanes > 64;
     const int threads = wide ? a.lanes : 256, step = wide ? 1 : 256 / a.lanes;
-    const int64_t blocks = ceil_div(s.R, step), most = int64_t(256) * 2048 / threads;
+    // what a CU holds at once, 1280 threads or a row, so that all workgroups have the same rows to do (us, bf16, 2048 threads
+    // and 1280: 8192 x 5120 80 and 62, 16384 x 4096 107 and 93)
+    const int64_t blocks = ceil_div(s.R, step), most = int64_t(256) * (threads < 1280 ? 1280 / threads : 1);
     const dim3 grid(unsigned(blocks < most ? blocks : most)), block{unsigned(threads)};
     dispatch(s, [&](auto T, auto S) {
         using X = decltype(T);
         using Y = decltype(S);
-        if (!wide) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, false, true>), grid, block, 0, stream, a);
-        else if (K == 1) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, true, true>), grid, block, 0, stream, a);
-        else if (a.lanes <= 512) hipLaunchKernelGGL((fwd_kernel<X, Y, 2, true, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((fwd_kernel<X, Y, 2, true, false>), grid, block, 0, stream, a);
+        if (!wide) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, false>), grid, block, 0, stream, a);
+        else if (s.C <= kOne) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((fwd_kernel<X, Y, 2, true>), grid, block, 0, stream, a);
     });
     return hipGetLastError();
 }
@@ -685,16 +757,18 @@ hipError_t launch_addnorm_bwd(const AddnormTensors& t, const AddnormShape& s, vo
     a.part = sums ? reinterpret_cast<float*>(ws) : nullptr;
     a.gate_part = p.runs ? reinterpret_cast<float*>(ws + p.gate) : t.dgate;
     a.averages = p.apart && (sums || t.dgate) ? reinterpret_cast<float*>(ws + p.averages) : nullptr;
-    const dim3 grid(unsigned(p.blocks)), block(unsigned(p.wide ? p.lanes : 256));
+    const dim3 grid(unsigned(p.blocks)), block(unsigned(p.rows == kLanes ? 256 : p.lanes));
     dispatch(s, [&](auto T, auto S) {
         auto with = [&](auto bias, auto gate) {
             using X = decltype(T);
             using Y = decltype(S);
             constexpr bool B = decltype(bias)::value, G = decltype(gate)::value;
-            if (!p.wide) hipLaunchKernelGGL((bwd_kernel<X, Y, 1, false, B, G, true>), grid, block, 0, stream, a);
-            else if (p.K == 1) hipLaunchKernelGGL((bwd_kernel<X, Y, 1, true, B, G, true>), grid, block, 0, stream, a);
-            else if (!p.apart) hipLaunchKernelGGL((bwd_kernel<X, Y, 2, true, B, G, true>), grid, block, 0, stream, a);
-            else hipLaunchKernelGGL((bwd_kernel<X, Y, 2, true, false, G, false>), grid, block, 0, stream, a);
+            if (p.rows == kLanes) hipLaunchKernelGGL((bwd_kernel<X, Y, kLanes, B, G>), grid, block, 0, stream, a);
+            else if (p.rows == k512) hipLaunchKernelGGL((bwd_kernel<X, Y, k512, B, G>), grid, block, 0, stream, a);
+            else if (p.rows == k768) hipLaunchKernelGGL((bwd_kernel<X, Y, k768, B, G>), grid, block, 0, stream, a);
+            else if (p.rows == k1024) hipLaunchKernelGGL((bwd_kernel<X, Y, k1024, false, false>), grid, block, 0, stream, a);
+            else if (p.rows == kApart) hipLaunchKernelGGL((bwd_kernel<X, Y, kApart, false, G>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((bwd_kernel<X, Y, kApart2, false, G>), grid, block, 0, stream, a);
         };
         const std::true_type yes;
         const std::false_type no;
