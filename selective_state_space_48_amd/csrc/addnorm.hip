@@ -11,7 +11,7 @@
 // what its rows give to the gradients of weights, biases and gate in registers and
 // writes them once; join_kernel adds the workgroups' parts in order.
 //
-// 16384 x 4096 bf16, both norms, residual fp32: 147 us (5.5 TB/s; a large copy has 4.9);
+// 16384 x 4096 bf16, both norms, residual fp32: 145 us (5.6 TB/s; a large copy has 4.9);
 // gradients with biases and 8 gate rows, residual bf16: 172 (4.8 with the parts).
 #include "../../include/selscan.h"
 #include "common.hpp"
@@ -61,25 +61,41 @@ template <> struct Vec<bf16_bits> {
     }
 };
 
-// n values from p (8, fewer at a row's end, or none); the others are 0.
-template <typename T> __device__ __forceinline__ Vec<T> load(const void* base, int64_t at, int n) {
+// Rows of whole vectors; of others (their last vector ends at the row's end, and the values before `lo` are another
+// thread's: loads then take no branch, and what is loaded early stays in flight; value by value 50445 x 495 bf16 took
+// 57 us instead of 34, its gradients 176 instead of 77); of fewer than 8 values.
+enum { kWhole, kPart, kFew };
+
+// A vector's first column (below 0 for kFew), and its first value that is the thread's own: 8 if it has none.
+struct Column {
+    int c, lo;
+    __device__ __forceinline__ Column() {}
+    __device__ __forceinline__ Column(int vector, int64_t C) {
+        const int at = vector * kV, last = int(C) - kV;
+        c = at < last ? at : last;
+        lo = at - c < kV ? at - c : kV;
+    }
+};
+
+template <int EDGE, typename T> __device__ __forceinline__ Vec<T> load(const void* base, int64_t at, int lo) {
     const T* p = static_cast<const T*>(base) + at;
     Vec<T> v{};
-    if (n == kV) {
+    if constexpr (EDGE != kFew) {
         v.a = reinterpret_cast<const Any16*>(p)->v;
         if constexpr (sizeof(T) == 4) v.b = reinterpret_cast<const Any16*>(p + 4)->v;
-    } else if (n > 0) {
+    } else {
         struct Values { T t[kV]; } s{};
 #pragma unroll
         for (int i = 0; i < kV; ++i)
-            if (i < n) s.t[i] = p[i];
+            if (i >= lo) s.t[i] = p[i];
         v = __builtin_bit_cast(Vec<T>, s);
     }
     return v;
 }
-template <typename T> __device__ __forceinline__ void store(void* base, int64_t at, int n, const float (&f)[kV]) {
+template <int EDGE, typename T>
+__device__ __forceinline__ void store(void* base, int64_t at, int lo, const float (&f)[kV]) {
     T* p = static_cast<T*>(base) + at;
-    if (n == kV) {
+    if (EDGE != kFew && lo == 0) {
         if constexpr (sizeof(T) == 4) {
             u32x4 a, b;
 #pragma unroll
@@ -95,21 +111,26 @@ template <typename T> __device__ __forceinline__ void store(void* base, int64_t 
             for (int i = 0; i < 4; ++i) a[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
             reinterpret_cast<Any16*>(p)->v = a;
         }
-    } else {
+    } else if constexpr (EDGE != kWhole) {
 #pragma unroll
         for (int i = 0; i < kV; ++i)
-            if (i < n) p[i] = from_f32<T>(f[i]);
+            if (i >= lo) p[i] = from_f32<T>(f[i]);
     }
 }
-// Weights (n values, the others 0), `dflt` without them.
-__device__ __forceinline__ void weights(const float* w, int64_t at, int n, float dflt, float (&f)[kV]) {
+// Weights, `dflt` without them.
+template <int EDGE> __device__ __forceinline__ void weights(const float* w, const Column& c, float dflt, float (&f)[kV]) {
     if (w) {
-        load<float>(w, at, n).get(f);
+        load<EDGE, float>(w, c.c, c.lo).get(f);
     } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) f[i] = i < n ? dflt : 0.0f;
+        for (int i = 0; i < kV; ++i) f[i] = dflt;
     }
 }
+// A value's term of a row's sum: only the thread's own count. (Whole vectors: their sum at once, own().)
+template <int EDGE> __device__ __forceinline__ float term(float t, int i, int lo) {
+    return EDGE != kWhole && i < lo ? 0.0f : t;
+}
+template <int EDGE> __device__ __forceinline__ float own(float sum, int lo) { return EDGE == kWhole && lo ? 0.0f : sum; }
 
 // Sums over the lanes of a wave, by moves inside the vector unit: every lane adds its partner's value (neighbours,
 // then pairs, quads, ...), so that all end with the same bits. M: lanes that are summed, a power of two.
@@ -174,31 +195,33 @@ template <bool WIDE> struct Row {
     }
 };
 
-// mean and 1 / sqrt of a row's values (0 past its end).
-template <int K, bool WIDE>
-__device__ __forceinline__ void statistics(int kind, const float (&v)[K][kV], const int (&n)[K], float inv, float eps,
+// mean and 1 / sqrt of a row's values.
+template <int K, int EDGE, bool WIDE>
+__device__ __forceinline__ void statistics(int kind, const float (&v)[K][kV], const Column (&c)[K], float inv, float eps,
                                            Row<WIDE>& row, float* mean, float* rstd) {
     *mean = 0.0f;
     float s = 0.0f;
     if (kind == SELSCAN_NORM_LAYER) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            float p = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kV; ++i) s += v[k][i];
+            for (int i = 0; i < kV; ++i) p += term<EDGE>(v[k][i], i, c[k].lo);
+            s += own<EDGE>(p, c[k].lo);
+        }
         *mean = row.sum(s) * inv;
         s = 0.0f;
+    }
+    // (an RMS norm's mean is 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+        float p = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const float d = i < n[k] ? v[k][i] - *mean : 0.0f;
-                s = fmaf(d, d, s);
-            }
-    } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < kV; ++i) s = fmaf(v[k][i], v[k][i], s);
+        for (int i = 0; i < kV; ++i) {
+            const float d = term<EDGE>(v[k][i] - *mean, i, c[k].lo);
+            p = fmaf(d, d, p);
+        }
+        s += own<EDGE>(p, c[k].lo);
     }
     // (off by one rounding; what it would flush is left to the root and the division)
     const float q = row.sum(s) * inv + eps;
@@ -206,22 +229,21 @@ __device__ __forceinline__ void statistics(int kind, const float (&v)[K][kV], co
 }
 
 // K: vectors of a thread. With one, weights and the next row's loads stay in registers.
-template <typename T, typename S, int K, bool WIDE>
+template <typename T, typename S, int K, bool WIDE, int EDGE>
 __global__ __launch_bounds__(WIDE ? 1024 : 256) void fwd_kernel(AnArgs a) {
     constexpr bool KEEP = K == 1;
     __shared__ float2 red[2][16];
     Row<WIDE> row(a.lanes, red);
     const AddnormTensors& t = a.t;
     const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
-    int n[K];
+    Column c[K];
     float w1[KEEP ? K : 1][kV], w2[KEEP ? K : 1][kV];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int64_t c = int64_t(row.l + a.lanes * k) * kV, left = a.C - c;
-        n[k] = left < 0 ? 0 : left < kV ? int(left) : kV;
+        c[k] = Column(row.l + a.lanes * k, a.C);
         if constexpr (KEEP) {
-            weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w1[k]);
-            weights(pre ? t.pre_w : nullptr, c, n[k], 1.0f, w2[k]);
+            weights<EDGE>(post ? t.post_w : nullptr, c[k], 1.0f, w1[k]);
+            weights<EDGE>(pre ? t.pre_w : nullptr, c[k], 1.0f, w2[k]);
         }
     }
     const float inv = 1.0f / float(a.C > 0 ? a.C : 1);
@@ -230,9 +252,9 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void fwd_kernel(AnArgs a) {
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
-            nx[k] = load<T>(t.x, at, n[k]);
-            if (t.res) ns[k] = load<S>(t.res, at, n[k]);
+            const int64_t at = r * a.C + c[k].c;
+            nx[k] = load<EDGE, T>(t.x, at, c[k].lo);
+            if (t.res) ns[k] = load<EDGE, S>(t.res, at, c[k].lo);
         }
     };
     const int64_t stride = int64_t(gridDim.x) * row.step;
@@ -254,51 +276,49 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void fwd_kernel(AnArgs a) {
         }
         if (KEEP && r + stride < a.R) fetch(r + stride);
         float m1 = 0.0f, r1 = 1.0f, m2 = 0.0f, r2 = 1.0f;
-        if (post) statistics<K, WIDE>(a.post, v, n, inv, a.eps, row, &m1, &r1);
+        if (post) statistics<K, EDGE>(a.post, v, c, inv, a.eps, row, &m1, &r1);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t c = int64_t(row.l + a.lanes * k) * kV;
             float (&u)[kV] = v[k];
             if (post) {
                 float (&w)[kV] = w1[KEEP ? k : 0];
-                if constexpr (!KEEP) weights(t.post_w, c, n[k], 1.0f, w);
+                if constexpr (!KEEP) weights<EDGE>(t.post_w, c[k], 1.0f, w);
 #pragma unroll
                 for (int i = 0; i < kV; ++i) u[i] = (u[i] - m1) * r1 * w[i];
                 if (t.post_b) {
                     float b[kV];
-                    load<float>(t.post_b, c, n[k]).get(b);
+                    load<EDGE, float>(t.post_b, c[k].c, c[k].lo).get(b);
 #pragma unroll
                     for (int i = 0; i < kV; ++i) u[i] += b[i];
                 }
             }
             if (t.gate) {
                 float g[kV];
-                load<float>(t.gate + r / a.per_gate * a.C, c, n[k]).get(g);
+                load<EDGE, float>(t.gate + r / a.per_gate * a.C, c[k].c, c[k].lo).get(g);
 #pragma unroll
                 for (int i = 0; i < kV; ++i) s[k][i] = fmaf(u[i], a.scale * g[i], s[k][i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < kV; ++i) s[k][i] = fmaf(u[i], a.scale, s[k][i]);
             }
-            if (t.sum) store<S>(t.sum, r * a.C + c, n[k], s[k]);
+            if (t.sum) store<EDGE, S>(t.sum, r * a.C + c[k].c, c[k].lo, s[k]);
         }
         if (pre) {
-            statistics<K, WIDE>(a.pre, s, n, inv, a.eps, row, &m2, &r2);
+            statistics<K, EDGE>(a.pre, s, c, inv, a.eps, row, &m2, &r2);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int64_t c = int64_t(row.l + a.lanes * k) * kV;
-                float y[kV];
+                    float y[kV];
                 float (&w)[kV] = w2[KEEP ? k : 0];
-                if constexpr (!KEEP) weights(t.pre_w, c, n[k], 1.0f, w);
+                if constexpr (!KEEP) weights<EDGE>(t.pre_w, c[k], 1.0f, w);
 #pragma unroll
                 for (int i = 0; i < kV; ++i) y[i] = (s[k][i] - m2) * r2 * w[i];
                 if (t.pre_b) {
                     float b[kV];
-                    load<float>(t.pre_b, c, n[k]).get(b);
+                    load<EDGE, float>(t.pre_b, c[k].c, c[k].lo).get(b);
 #pragma unroll
                     for (int i = 0; i < kV; ++i) y[i] += b[i];
                 }
-                if (t.y) store<T>(t.y, r * a.C + c, n[k], y);
+                if (t.y) store<EDGE, T>(t.y, r * a.C + c[k].c, c[k].lo, y);
             }
         }
         if (t.stats && row.l == 0) {
@@ -316,7 +336,7 @@ enum { kPreW = 0, kPostW = 1, kPreB = 2, kPostB = 3 };
 // registers the sums do not fit, one vector each or two: the rows alone, and their averages for cols_kernel, which then
 // writes dres.
 enum { kLanes, k512, k768, k1024, kApart, kApart2 };
-template <typename T, typename S, int ROWS, bool BIAS, bool GATE>
+template <typename T, typename S, int ROWS, bool BIAS, bool GATE, int EDGE>
 __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS == k768 ? 768 : 1024,
                              ROWS == kLanes && sizeof(S) == 2 && !BIAS && !GATE ? 4 : 1) void bwd_kernel(AnArgs a) {
     constexpr bool WIDE = ROWS != kLanes, SUMS = ROWS < kApart;
@@ -328,15 +348,14 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
     const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
     const bool use_x = post || (SUMS && GATE && t.dgate);
     constexpr int NS = BIAS ? 4 : 2, KW = SUMS ? K : 1;
-    int n[K];
+    Column col[K];
     float w1[KW][kV], w2[KW][kV], acc[NS][KW][kV], accg[GATE ? KW : 1][kV];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int64_t c = int64_t(row.l + a.lanes * k) * kV, left = a.C - c;
-        n[k] = left < 0 ? 0 : left < kV ? int(left) : kV;
+        col[k] = Column(row.l + a.lanes * k, a.C);
         if constexpr (SUMS) {
-            weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w1[k]);
-            weights(pre ? t.pre_w : nullptr, c, n[k], 1.0f, w2[k]);
+            weights<EDGE>(post ? t.post_w : nullptr, col[k], 1.0f, w1[k]);
+            weights<EDGE>(pre ? t.pre_w : nullptr, col[k], 1.0f, w2[k]);
         }
         if constexpr (SUMS)
 #pragma unroll
@@ -350,7 +369,8 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
         if constexpr (!WIDE) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kV; ++i) cols[(row.ri * a.lanes + row.l) * kV + i] = f[0][i];
+            for (int i = 0; i < kV; ++i)
+                if (i >= col[0].lo) cols[row.ri * a.lanes * kV + col[0].c + i] = f[0][i];
             __syncthreads();
             for (int c = threadIdx.x; c < a.C; c += 256) {
                 float s = cols[c];
@@ -359,7 +379,7 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < KW; ++k) store<float>(out, int64_t(row.l + a.lanes * k) * kV, n[k], f[k]);
+            for (int k = 0; k < KW; ++k) store<EDGE, float>(out, col[k].c, col[k].lo, f[k]);
         }
     };
     // Rows r0 .. r1 of the workgroup, one gate row's at a time.
@@ -379,13 +399,13 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
-            if (use_x) nx[k] = load<T>(t.x, at, n[k]);
+            const int64_t at = r * a.C + col[k].c;
+            if (use_x) nx[k] = load<EDGE, T>(t.x, at, col[k].lo);
             if (pre) {
-                ns[k] = load<S>(t.sum, at, n[k]);
-                ny[k] = load<T>(t.dy, at, n[k]);
+                ns[k] = load<EDGE, S>(t.sum, at, col[k].lo);
+                ny[k] = load<EDGE, T>(t.dy, at, col[k].lo);
             }
-            if (t.dsum) nd[k] = load<S>(t.dsum, at, n[k]);
+            if (t.dsum) nd[k] = load<EDGE, S>(t.dsum, at, col[k].lo);
         }
         if (t.stats)
 #pragma unroll
@@ -400,7 +420,7 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
             nx[k].get(x1);
             if (post)
 #pragma unroll
-                for (int i = 0; i < kV; ++i) x1[i] = i < n[k] ? (x1[i] - m1) * q1 : 0.0f;
+                for (int i = 0; i < kV; ++i) x1[i] = (x1[i] - m1) * q1;
         }
     };
     for (int64_t g0 = r0; g0 < r1;) {
@@ -409,7 +429,7 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
         if constexpr (GATE && SUMS)
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                weights(t.gate ? t.gate + gi * a.C : nullptr, int64_t(row.l + a.lanes * k) * kV, n[k], 1.0f, gate[k]);
+                weights<EDGE>(t.gate ? t.gate + gi * a.C : nullptr, col[k], 1.0f, gate[k]);
 #pragma unroll
                 for (int i = 0; i < kV; ++i) accg[k][i] = 0.0f;
             }
@@ -429,23 +449,26 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
                 if (pre) {
                     float dy[kV];
                     if constexpr (!SUMS) {
-                        const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
-                        ns[k] = load<S>(t.sum, at, n[k]);
-                        ny[k] = load<T>(t.dy, at, n[k]);
+                        const int64_t at = r * a.C + col[k].c;
+                        ns[k] = load<EDGE, S>(t.sum, at, col[k].lo);
+                        ny[k] = load<EDGE, T>(t.dy, at, col[k].lo);
                     }
                     ns[k].get(xh[k]);
                     ny[k].get(dy);
                     float (&w)[kV] = w2[SUMS ? k : 0];
-                    if constexpr (!SUMS) weights(t.pre_w, int64_t(row.l + a.lanes * k) * kV, n[k], 1.0f, w);
+                    if constexpr (!SUMS) weights<EDGE>(t.pre_w, col[k], 1.0f, w);
+                    float p1 = 0.0f, p2 = 0.0f;
 #pragma unroll
                     for (int i = 0; i < kV; ++i) {
-                        xh[k][i] = i < n[k] ? (xh[k][i] - m2) * q2 : 0.0f;
-                        e[k][i] = dy[i] * w[i];
-                        s1 += e[k][i];
-                        s2 = fmaf(e[k][i], xh[k][i], s2);
+                        xh[k][i] = (xh[k][i] - m2) * q2;
+                        e[k][i] = term<EDGE>(dy[i] * w[i], i, col[k].lo);
+                        p1 += e[k][i];
+                        p2 = fmaf(e[k][i], xh[k][i], p2);
                         if constexpr (SUMS) acc[kPreW][k][i] = fmaf(dy[i], xh[k][i], acc[kPreW][k][i]);
                         if constexpr (SUMS && BIAS) acc[kPreB][k][i] += dy[i];
                     }
+                    s1 += own<EDGE>(p1, col[k].lo);
+                    s2 += own<EDGE>(p2, col[k].lo);
                 }
             }
             if (SUMS && r + row.step < g1) fetch(r + row.step);
@@ -467,9 +490,9 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
             if constexpr (!SUMS)
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
-                    if (use_x) nx[k] = load<T>(t.x, at, n[k]);
-                    if (t.dsum) nd[k] = load<S>(t.dsum, at, n[k]);
+                    const int64_t at = r * a.C + col[k].c;
+                    if (use_x) nx[k] = load<EDGE, T>(t.x, at, col[k].lo);
+                    if (t.dsum) nd[k] = load<EDGE, S>(t.dsum, at, col[k].lo);
                     passed(k, m1, q1, ds[k], x1[k]);
                     if (pre)
 #pragma unroll
@@ -478,22 +501,22 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
             s1 = s2 = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int64_t at = r * a.C + int64_t(row.l + a.lanes * k) * kV;
+                const int64_t at = r * a.C + col[k].c;
                 if (t.dres && (SUMS || !a.averages)) {
                     float o[kV];
 #pragma unroll
                     for (int i = 0; i < kV; ++i) o[i] = a.res_scale * ds[k][i];
-                    store<S>(t.dres, at, n[k], o);
+                    store<EDGE, S>(t.dres, at, col[k].lo, o);
                 }
-                const int64_t c = int64_t(row.l + a.lanes * k) * kV;
                 float b1[kV];
-                if constexpr (GATE && SUMS) weights(post ? t.post_b : nullptr, c, n[k], 0.0f, b1);
+                if constexpr (GATE && SUMS) weights<EDGE>(post ? t.post_b : nullptr, col[k], 0.0f, b1);
                 float (&w)[kV] = w1[SUMS ? k : 0];
                 float (&gt)[kV] = gate[GATE && SUMS ? k : 0];
                 if constexpr (!SUMS) {
-                    weights(post ? t.post_w : nullptr, c, n[k], 1.0f, w);
-                    if constexpr (GATE) weights(t.gate + gi * a.C, c, n[k], 1.0f, gt);
+                    weights<EDGE>(post ? t.post_w : nullptr, col[k], 1.0f, w);
+                    if constexpr (GATE) weights<EDGE>(t.gate + gi * a.C, col[k], 1.0f, gt);
                 }
+                float p1 = 0.0f, p2 = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kV; ++i) {
                     float du = a.scale * ds[k][i];
@@ -504,12 +527,14 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
                     if (post) {
                         if constexpr (SUMS) acc[kPostW][k][i] = fmaf(du, x1[k][i], acc[kPostW][k][i]);
                         if constexpr (SUMS && BIAS) acc[kPostB][k][i] += du;
-                        du *= w[i];
-                        s1 += du;
-                        s2 = fmaf(du, x1[k][i], s2);
+                        du = term<EDGE>(du * w[i], i, col[k].lo);
+                        p1 += du;
+                        p2 = fmaf(du, x1[k][i], p2);
                     }
                     ds[k][i] = du;
                 }
+                s1 += own<EDGE>(p1, col[k].lo);
+                s2 += own<EDGE>(p2, col[k].lo);
             }
             if (post) {
                 row.sums(s1, s2);
@@ -521,7 +546,7 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
             }
             if (t.dx)
 #pragma unroll
-                for (int k = 0; k < K; ++k) store<T>(t.dx, r * a.C + int64_t(row.l + a.lanes * k) * kV, n[k], ds[k]);
+                for (int k = 0; k < K; ++k) store<EDGE, T>(t.dx, r * a.C + col[k].c, col[k].lo, ds[k]);
         }
         if constexpr (GATE && SUMS)
             if (t.dgate) flush(accg, a.gate_part + (a.runs ? int64_t(blockIdx.x) : gi) * a.C);
@@ -539,14 +564,14 @@ __global__ __launch_bounds__(ROWS == kLanes ? 256 : ROWS == k512 ? 512 : ROWS ==
 
 // The sums over rows where bwd_kernel does not form them: a thread takes a vector of columns down the rows of its
 // workgroup (grid x), from the averages that bwd_kernel left. It writes dres too, which may stand in dsum's place.
-template <typename T, typename S>
+template <typename T, typename S, int EDGE>
 __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
     const AddnormTensors& t = a.t;
-    const int64_t c = (int64_t(blockIdx.y) * 64 + threadIdx.x) * kV, blk = blockIdx.x;
+    const int64_t blk = blockIdx.x;
+    const Column c(int(blockIdx.y * 64 + threadIdx.x), a.C);
     const bool post = a.post != SELSCAN_NORM_NONE, pre = a.pre != SELSCAN_NORM_NONE;
     const bool use_x = post || t.dgate;
-    const int n = a.C - c < 0 ? 0 : a.C - c < kV ? int(a.C - c) : kV;
-    if (n == 0) return;
+    if (c.lo == kV) return;
     int64_t r0, r1;
     if (a.runs) {
         const int64_t g = blk / a.runs, e = (g + 1) * a.per_gate;
@@ -557,26 +582,26 @@ __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
         r1 = r0 + a.per < a.R ? r0 + a.per : a.R;
     }
     float w1[kV], b1[kV], w2[kV], gate[kV], acc[5][kV];
-    weights(post ? t.post_w : nullptr, c, n, 1.0f, w1);
-    weights(post ? t.post_b : nullptr, c, n, 0.0f, b1);
-    weights(pre ? t.pre_w : nullptr, c, n, 1.0f, w2);
-    weights(nullptr, c, n, 1.0f, gate);
+    weights<EDGE>(post ? t.post_w : nullptr, c, 1.0f, w1);
+    weights<EDGE>(post ? t.post_b : nullptr, c, 0.0f, b1);
+    weights<EDGE>(pre ? t.pre_w : nullptr, c, 1.0f, w2);
+    weights<EDGE>(nullptr, c, 1.0f, gate);
 #pragma unroll
     for (int j = 0; j < 5; ++j)
 #pragma unroll
         for (int i = 0; i < kV; ++i) acc[j][i] = 0.0f;
     for (int64_t r = r0; r < r1; ++r) {
-        const int64_t at = r * a.C + c, gi = r / a.per_gate;
-        if (t.gate && (r == r0 || r % a.per_gate == 0)) weights(t.gate + gi * a.C, c, n, 1.0f, gate);
+        const int64_t at = r * a.C + c.c, gi = r / a.per_gate;
+        if (t.gate && (r == r0 || r % a.per_gate == 0)) weights<EDGE>(t.gate + gi * a.C, c, 1.0f, gate);
         float st[4] = {0.0f, 1.0f, 0.0f, 1.0f}, x[kV] = {}, s[kV], dy[kV], ds[kV] = {};
         if (t.stats)
 #pragma unroll
             for (int i = 0; i < 4; ++i) st[i] = t.stats[r * 4 + i];
-        if (use_x) load<T>(t.x, at, n).get(x);
-        if (t.dsum) load<S>(t.dsum, at, n).get(ds);
+        if (use_x) load<EDGE, T>(t.x, at, c.lo).get(x);
+        if (t.dsum) load<EDGE, S>(t.dsum, at, c.lo).get(ds);
         if (pre) {
-            load<S>(t.sum, at, n).get(s);
-            load<T>(t.dy, at, n).get(dy);
+            load<EDGE, S>(t.sum, at, c.lo).get(s);
+            load<EDGE, T>(t.dy, at, c.lo).get(dy);
             const float a1 = a.averages[r * 2], a2 = a.averages[r * 2 + 1];
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
@@ -590,7 +615,7 @@ __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
             float o[kV];
 #pragma unroll
             for (int i = 0; i < kV; ++i) o[i] = a.res_scale * ds[i];
-            store<S>(t.dres, at, n, o);
+            store<EDGE, S>(t.dres, at, c.lo, o);
         }
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
@@ -600,7 +625,7 @@ __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
             acc[kPostB][i] = fmaf(du, gate[i], acc[kPostB][i]);
         }
         if (t.dgate && (r + 1 == r1 || (r + 1) % a.per_gate == 0)) {
-            store<float>(a.gate_part + (a.runs ? blk : gi) * a.C, c, n, acc[4]);
+            store<EDGE, float>(a.gate_part + (a.runs ? blk : gi) * a.C, c.c, c.lo, acc[4]);
 #pragma unroll
             for (int i = 0; i < kV; ++i) acc[4][i] = 0.0f;
         }
@@ -609,7 +634,7 @@ __global__ __launch_bounds__(64) void cols_kernel(AnArgs a, int NS) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float* want = j == kPreW ? t.dpre_w : j == kPostW ? t.dpost_w : j == kPreB ? t.dpre_b : t.dpost_b;
-        if (want) store<float>(a.part + (blk * NS + j) * a.C, c, n, acc[j]);
+        if (want) store<EDGE, float>(a.part + (blk * NS + j) * a.C, c.c, c.lo, acc[j]);
     }
 }
 
@@ -666,11 +691,16 @@ AnArgs args_of(const AddnormTensors& t, const AddnormShape& s) {
     return a;
 }
 
-// f(type, residual's type)
+// f(type, residual's type, how rows end)
 template <typename F> void dispatch(const AddnormShape& s, F f) {
-    if (s.dtype == DType::F32) f(float{}, float{});
-    else if (s.res_dtype == DType::F32) f(bf16_bits{}, float{});
-    else f(bf16_bits{}, bf16_bits{});
+    auto types = [&](auto edge) {
+        if (s.dtype == DType::F32) f(float{}, float{}, edge);
+        else if (s.res_dtype == DType::F32) f(bf16_bits{}, float{}, edge);
+        else f(bf16_bits{}, bf16_bits{}, edge);
+    };
+    if (s.C % kV == 0 && s.C > 0) types(std::integral_constant<int, kWhole>{});
+    else if (s.C > kV) types(std::integral_constant<int, kPart>{});
+    else types(std::integral_constant<int, kFew>{});
 }
 
 // The backward's workgroups: their rows, and where their sums go.
@@ -738,12 +768,15 @@ hipError_t launch_addnorm(const AddnormTensors& t, const AddnormShape& s, hipStr
     // and 1280: 8192 x 5120 80 and 62, 16384 x 4096 107 and 93)
     const int64_t blocks = ceil_div(s.R, step), most = int64_t(256) * (threads < 1280 ? 1280 / threads : 1);
     const dim3 grid(unsigned(blocks < most ? blocks : most)), block{unsigned(threads)};
-    dispatch(s, [&](auto T, auto S) {
+    dispatch(s, [&](auto T, auto S, auto edge) {
         using X = decltype(T);
         using Y = decltype(S);
-        if (!wide) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, false>), grid, block, 0, stream, a);
-        else if (s.C <= kOne) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((fwd_kernel<X, Y, 2, true>), grid, block, 0, stream, a);
+        constexpr int E = decltype(edge)::value;
+        if (!wide) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, false, E>), grid, block, 0, stream, a);
+        if constexpr (E != kFew) {
+            if (wide && s.C <= kOne) hipLaunchKernelGGL((fwd_kernel<X, Y, 1, true, E>), grid, block, 0, stream, a);
+            else if (wide) hipLaunchKernelGGL((fwd_kernel<X, Y, 2, true, E>), grid, block, 0, stream, a);
+        }
     });
     return hipGetLastError();
 }
@@ -758,17 +791,20 @@ hipError_t launch_addnorm_bwd(const AddnormTensors& t, const AddnormShape& s, vo
     a.gate_part = p.runs ? reinterpret_cast<float*>(ws + p.gate) : t.dgate;
     a.averages = p.apart && (sums || t.dgate) ? reinterpret_cast<float*>(ws + p.averages) : nullptr;
     const dim3 grid(unsigned(p.blocks)), block(unsigned(p.rows == kLanes ? 256 : p.lanes));
-    dispatch(s, [&](auto T, auto S) {
+    dispatch(s, [&](auto T, auto S, auto edge) {
+        constexpr int E = decltype(edge)::value;
         auto with = [&](auto bias, auto gate) {
             using X = decltype(T);
             using Y = decltype(S);
             constexpr bool B = decltype(bias)::value, G = decltype(gate)::value;
-            if (p.rows == kLanes) hipLaunchKernelGGL((bwd_kernel<X, Y, kLanes, B, G>), grid, block, 0, stream, a);
-            else if (p.rows == k512) hipLaunchKernelGGL((bwd_kernel<X, Y, k512, B, G>), grid, block, 0, stream, a);
-            else if (p.rows == k768) hipLaunchKernelGGL((bwd_kernel<X, Y, k768, B, G>), grid, block, 0, stream, a);
-            else if (p.rows == k1024) hipLaunchKernelGGL((bwd_kernel<X, Y, k1024, false, false>), grid, block, 0, stream, a);
-            else if (p.rows == kApart) hipLaunchKernelGGL((bwd_kernel<X, Y, kApart, false, G>), grid, block, 0, stream, a);
-            else hipLaunchKernelGGL((bwd_kernel<X, Y, kApart2, false, G>), grid, block, 0, stream, a);
+            if (p.rows == kLanes) hipLaunchKernelGGL((bwd_kernel<X, Y, kLanes, B, G, E>), grid, block, 0, stream, a);
+            if constexpr (E != kFew) {
+                if (p.rows == k512) hipLaunchKernelGGL((bwd_kernel<X, Y, k512, B, G, E>), grid, block, 0, stream, a);
+                else if (p.rows == k768) hipLaunchKernelGGL((bwd_kernel<X, Y, k768, B, G, E>), grid, block, 0, stream, a);
+                else if (p.rows == k1024) hipLaunchKernelGGL((bwd_kernel<X, Y, k1024, false, false, E>), grid, block, 0, stream, a);
+                else if (p.rows == kApart) hipLaunchKernelGGL((bwd_kernel<X, Y, kApart, false, G, E>), grid, block, 0, stream, a);
+                else if (p.rows == kApart2) hipLaunchKernelGGL((bwd_kernel<X, Y, kApart2, false, G, E>), grid, block, 0, stream, a);
+            }
         };
         const std::true_type yes;
         const std::false_type no;
@@ -779,9 +815,10 @@ hipError_t launch_addnorm_bwd(const AddnormTensors& t, const AddnormShape& s, vo
             if (t.gate) with(no, yes);
             else with(no, no);
         }
-        if (a.averages)
-            hipLaunchKernelGGL((cols_kernel<decltype(T), decltype(S)>),
-                               dim3(unsigned(p.blocks), unsigned(ceil_div(s.C, 64 * kV))), dim3(64), 0, stream, a, p.sums);
+        if constexpr (E != kFew)
+            if (a.averages)
+                hipLaunchKernelGGL((cols_kernel<decltype(T), decltype(S), E>),
+                                   dim3(unsigned(p.blocks), unsigned(ceil_div(s.C, 64 * kV))), dim3(64), 0, stream, a, p.sums);
     });
     const unsigned cols = unsigned(ceil_div(s.C, 64));
     if (sums) {

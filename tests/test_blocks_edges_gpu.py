@@ -5,6 +5,7 @@ import torch
 
 from blocks_util import DT, check_bwd, check_fwd, make, np_of
 from selective_state_space_48_amd import selscan
+from test_addnorm_gpu import check as check_norm, make as make_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,33 @@ def test_two_calls_at_once(kind):
     for s, outs in got:
         for a, b in zip(outs, want[s]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("C", [3, 8, 9, 15, 16, 17, 520, 4095, 4096, 4103, 5120, 5121, 6144, 6145, 7001, 8191, 8193, 9001])
+def test_norms_where_the_split_changes(C, types):
+    """Rows of a vector and its neighbours, and where threads of a row or vectors of a thread change: with gates and
+    biases, with weights alone, and without a gradient of either."""
+    for gates, bias, weight, post, pre in ((3, True, True, "layer", "rms"), (0, False, True, "rms", "layer"),
+                                           (0, True, True, "rms", "rms"), (3, False, False, "none", "layer")):
+        p = make_norm(6, C, types, seed=C, post=post, pre=pre, gates=gates, bias=bias, weight=weight)
+        check_norm(p, post, pre, f"{C} {types} gates={gates} bias={bias} {post} {pre}")
+
+
+@pytest.mark.parametrize("C", [5, 100, 2049, 4100, 9001])
+def test_norms_in_place_and_beside(C):
+    """res_out in place of res, where a row's last vector also reads values of its neighbour: the same bits, and
+    nothing past the tensors' ends is written."""
+    g = torch.Generator().manual_seed(C)
+    R = 700
+    x, res = (torch.randn(R, C, generator=g).bfloat16().cuda() for _ in range(2))
+    for post, pre in (("none", "none"), ("rms", "layer")):
+        case(f"{C} {post} {pre}")
+        y, s, stats = selscan.addnorm(x, res, pre=pre, post=post)
+        room = torch.full((R * C + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        own = room[:R * C].view(R, C)
+        own.copy_(res)
+        y2, s2, stats2 = selscan.addnorm(x, own, pre=pre, post=post, res_out=own)
+        torch.cuda.synchronize()
+        assert s2.data_ptr() == own.data_ptr() and torch.equal(s, own) and torch.equal(stats, stats2)
+        assert (room[R * C:] == 7.0).all() and (y is None or torch.equal(y, y2))
