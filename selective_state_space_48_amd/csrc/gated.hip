@@ -1024,12 +1024,20 @@ __global__ __launch_bounds__(64) void carry_kernel(Stretch* runs, double* enter,
     }
 }
 
-// out[d] = the sum of part[i][d] over i, in order.
-__global__ __launch_bounds__(64) void join_kernel(const float* part, int64_t n, int64_t D, float* out) {
-    const int64_t d = int64_t(blockIdx.x) * 64 + threadIdx.x;
-    if (d >= D) return;
+// out[d] = the sum of part[i][d] over i: 64 columns a workgroup, sixteen interleaved sums joined in order.
+__global__ __launch_bounds__(1024) void join_kernel(const float* part, int64_t n, int64_t D, float* out) {
+    __shared__ double sums[16][64];
+    const int c = threadIdx.x % 64, r = threadIdx.x / 64;
+    const int64_t d = int64_t(blockIdx.x) * 64 + c;
     double s = 0.0;
-    for (int64_t i = 0; i < n; ++i) s += part[i * D + d];
+    if (d < D)
+#pragma unroll 4
+        for (int64_t i = r; i < n; i += 16) s += part[i * D + d];
+    sums[r][c] = s;
+    __syncthreads();
+    if (r || d >= D) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += sums[k][c];
     out[d] = float(s);
 }
 
@@ -1194,11 +1202,11 @@ bool gated_plan(const GatedShape& s, int32_t requested, bool backward, GatedPlan
             if (s.L > 12 * kTile && blocks * (thin(s) ? 104 : 52) < single * 256) p->chain = ceil_div(s.L, kTile);
         } else if (blocks > 0 && blocks < 96) {
             // Runs, which read what the decays hang on twice, where even narrow workgroups leave CUs idle: for one round of
-            // workgroups over the CUs, or for two and a half where that makes less than four runs; of two tiles at least
-            // (bf16, us, without and with runs: 1 x 16384 x 512 32 runs 68, 24 81, 48 89; 1 x 16384 x 1024 16 runs 101, 12
-            // 127, 20 150; 1 x 8192 x 2560 270, 6 runs 130, 8 168, 16 136; 1 x 8192 x 5120 288, 8 runs 237; 8 x 2048 x 64 67,
-            // 8 runs 46, 16 53).
-            const int64_t most = ceil_div(s.L, 2 * kTile);
+            // workgroups over the CUs, or for two and a half where that makes less than four runs; of a tile at least
+            // (bf16, us, single and with runs: 1 x 16384 x 512 221 and 62, 1 x 8192 x 2560 270 and 130, 3 x 5000 x 300 110
+            // and 46, 8 x 2048 x 64 67 and 28, in runs of two tiles 33; 1 x 1370 x 1152 48 and 27, of two tiles 33; but 3 x
+            // 515 x 321 fp32, whose states are formed too, 20 and 31).
+            const int64_t most = s.L > 6 * kTile ? ceil_div(s.L, kTile) : 1;
             want = blocks <= 64 ? 256 / blocks : 640 / blocks;
             want = want < most ? want : most;
             if (want < 4) want = 1;
@@ -1294,7 +1302,7 @@ hipError_t launch_gated_bwd(const GatedTensors& t, const GatedShape& s, const Ga
     a.dA_part = t.dA ? part : nullptr;
     run_bwd<kOut>(a, s, p.segments, stream);
     if (t.dA)
-        hipLaunchKernelGGL(join_kernel, dim3(unsigned(ceil_div(s.dim, 64))), dim3(64), 0, stream, part,
+        hipLaunchKernelGGL(join_kernel, dim3(unsigned(ceil_div(s.dim, 64))), dim3(1024), 0, stream, part,
                            s.batch * p.segments, s.dim, t.dA);
     return hipGetLastError();
 }

@@ -165,7 +165,7 @@ def test_gated_automatic_splits():
     assert runs(batch=8, seqlen=4096, dim=4096) == 0
     assert runs(batch=1, seqlen=512, dim=64) == 0
     assert runs(batch=1, seqlen=16384, dim=512) == 32
-    assert runs(batch=8, seqlen=2048, dim=64) == 8
+    assert runs(batch=8, seqlen=2048, dim=64) == 16
     assert gated_size(ga(batch=1 << 18, dim=8), False, segments=65536)[0] == S.OK      # 100 tokens: one tile
     assert gated_size(ga(batch=1 << 18, dim=8, seqlen=1 << 14), False, segments=64)[0] == S.ERR_DIMS
 
