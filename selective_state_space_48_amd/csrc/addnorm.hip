@@ -1,17 +1,18 @@
 // Norms around a block with the residual sum between them, and the gradients.
 //
 // Bound by memory: a row is held in registers, read once and written once. A
-// thread holds vectors of 8 values of a row, `lanes` threads a row: a power of two
-// of a wave's lanes for narrow rows (sums by shuffles, several rows a workgroup),
-// whole waves for wide ones (sums through LDS, one barrier each, as the entries
-// alternate). Workgroups go over their rows with the weights kept in registers and
-// the next row's loads in flight.
+// thread holds a vector of 8 values of a row (two above 8192), `lanes` threads a
+// row: a power of two of a wave's lanes for narrow rows (several a workgroup),
+// whole waves for wide ones (sums over the waves through LDS, one barrier each, as
+// the entries alternate). Sums over lanes are moves of the vector unit: through LDS
+// 8192 x 5120 bf16 took 131 us instead of 80. Workgroups go over their rows with the
+// weights kept in registers and the next row's loads in flight.
 //
 // Statistics in fp32: a mean, then the squares about it. Backward, a workgroup adds
 // what its rows give to the gradients of weights, biases and gate in registers and
 // writes them once; join_kernel adds the workgroups' parts in order.
 //
-// 16384 x 4096 bf16, both norms, residual fp32: 145 us (5.6 TB/s; a large copy has 4.9);
+// 16384 x 4096 bf16, both norms, residual fp32: 145 to 148 us (5.5 TB/s; a large copy has 4.9);
 // gradients with biases and 8 gate rows, residual bf16: 172 (4.8 with the parts).
 #include "../../include/selscan.h"
 #include "common.hpp"

@@ -3,7 +3,7 @@
 // Bound by memory where the vector units keep up: a bfloat16 value with a gate takes 47
 // vector instructions forward and 100 backward, which hold the units 60 and 66 % of the
 // time. 8 x 2048 x 4096 bf16, decay, gate: forward 175 to 186 us (3.6 to 3.8 TB/s), gradients
-// 320 to 335 (3.6 to 3.8), where a copy reaches 4.9; 1 x 32771 x 2560, chained: 213 to 219;
+// 286 to 335 (3.6 to 4.2), where a copy reaches 4.9; 1 x 32771 x 2560, chained: 213 to 219;
 // 256 x 5120 tokens: 6.1 (3.9).
 //
 // What a long memory settles to hangs on 1 - a, which a itself, near 1, does not
