@@ -1091,7 +1091,8 @@ def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, d
                 post: str = "none", post_weight: Optional[torch.Tensor] = None,
                 post_bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
                 res_scale: float = 1.0, want_dx: bool = True, want_dres: bool = True, want_dparams: bool = True,
-                dres: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+                dres: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                dtype: Optional[torch.dtype] = None, res_dtype: Optional[torch.dtype] = None) -> dict:
     """Gradients of ``addnorm`` (selscan_addnorm_bwd) for ``dy`` (None with pre
     "none") and ``dres_out`` (the gradient into res_out; None: zeros), from the
     ``res_out`` and ``stats`` that it returned.
@@ -1100,14 +1101,18 @@ def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, d
     ``want_dparams``, dpost_weight, dpost_bias, dpre_weight, dpre_bias [channels]
     and dgate (like gate), all fp32, of the parameters that are given. ``x`` may
     be None where there is neither a post norm nor a gate whose gradient is
-    wanted; with pre "none" ``res_out`` and ``dy`` must be None.
+    wanted; with pre "none" ``res_out`` and ``dy`` must be None. ``dtype`` is
+    x's type, for dx where neither x nor dy is given to say it (None: dres_out's,
+    so a bfloat16 block on a float32 stream has to name its own); ``res_dtype``
+    the residual stream's, for dres where no tensor of it is given (None: x's).
     """
     like = next((t for t in (dy, x, res_out, dres_out) if t is not None), None)
     if like is None or like.dim() < 1:
         raise ValueError("dy, x, res_out or dres_out must be given, as [..., channels]")
     shape, C, dev = like.shape, like.shape[-1], like.device
-    dt = dy.dtype if dy is not None else x.dtype if x is not None else like.dtype
-    rt = next((t.dtype for t in (res_out, dres_out, dres) if t is not None), dt)
+    # (a tensor of another type than the one that is named is turned down below)
+    dt = dtype or (dy.dtype if dy is not None else x.dtype if x is not None else like.dtype)
+    rt = res_dtype or next((t.dtype for t in (res_out, dres_out, dres) if t is not None), dt)
     rows = 1
     for n in shape[:-1]:
         rows *= n
