@@ -1158,7 +1158,8 @@ def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling: str = "none"
     fastest frequency and divides the slowest by ``factor``; "parts", those
     that turn more than ``fast`` times over ``original`` tokens left, those
     that turn less than ``slow`` times divided by ``factor``, and linear in the
-    index between these two (the magnitude is ``rotary``'s ``scale``).
+    index between these two, each rounded away from the other to a whole index
+    from 0 to rot - 1 (the magnitude is ``rotary``'s ``scale``).
     """
     if rot < 2 or rot % 2:
         raise ValueError("rot must be even and positive")
@@ -1177,8 +1178,9 @@ def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling: str = "none"
             raise ValueError('scaling "parts" needs original > 0 and fast > slow > 0')
         # the index whose frequency turns n times over the original context
         where = [rot * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow)]
-        lo, hi = max(math.floor(where[0]), 0), min(math.ceil(where[1]), rot - 1)
-        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        hi = min(math.ceil(where[1]), rot - 1)
+        lo = min(max(math.floor(where[0]), 0), hi - 1)  # (hi below 1: all are divided)
+        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / (hi - lo)).clamp(0, 1)
         freq = freq * (1 - ramp) + freq / factor * ramp
     elif scaling not in ("none", "base"):
         raise ValueError('scaling must be "none", "linear", "base" or "parts"')
