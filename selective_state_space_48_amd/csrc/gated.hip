@@ -598,7 +598,7 @@ __global__ __launch_bounds__(256) void start_chain_kernel(Chain ch, int64_t word
 
 // Eight waves compute; a ninth hands out the tiles and looks back. While it does that for a tile, the others
 // evaluate the next one and keep the tile's tokens in registers: one barrier a tile.
-template <typename T, bool DECAY, bool GATE, int V, int CL, int N, int MODE>
+template <typename T, bool DECAY, bool GATE, int V, int CL, int N>
 __global__ __launch_bounds__(kWaves * 64 + 64, 3) void fwd_chain_kernel(GaArgs a, Chain ch) {
     using W = Place<T, V, CL, N>;
     static_assert(W::kChan <= 64, "a lane of the ninth wave for each channel");
@@ -690,29 +690,27 @@ __global__ __launch_bounds__(kWaves * 64 + 64, 3) void fwd_chain_kernel(GaArgs a
                 if (a.ckpt && w.live && t % SELSCAN_GATED_CKPT == 0 && t < a.L)
 #pragma unroll
                     for (int v = 0; v < V; ++v) a.ckpt[t / SELSCAN_GATED_CKPT * lanes + lane + v] = hf[v];
-                if constexpr (MODE == kOut) {
-                    const int64_t at = w.base(a, t0);
+                const int64_t at = w.base(a, t0);
 #pragma unroll
-                    for (int q = 0; q < kQuads; ++q) {
-                        const f32x4 f = kept[side ^ 1][q][threadIdx.x];
+                for (int q = 0; q < kQuads; ++q) {
+                    const f32x4 f = kept[side ^ 1][q][threadIdx.x];
 #pragma unroll
-                        for (int u = 0; u < 2 / V; ++u) {
-                            const int i = q * (2 / V) + u;
-                            float o[V];
+                    for (int u = 0; u < 2 / V; ++u) {
+                        const int i = q * (2 / V) + u;
+                        float o[V];
 #pragma unroll
-                            for (int v = 0; v < V; ++v) {
-                                const int j = V == 1 ? u : v;
-                                hf[v] = fmaf(f[2 * j], hf[v], f[2 * j + 1]);
-                                o[v] = i < have ? hf[v] : 0.0f;
-                            }
-                            if constexpr (GATE) {
-                                float z[V];
-                                unpack<T, V>(prev_z[i], z);
-#pragma unroll
-                                for (int v = 0; v < V; ++v) o[v] *= i < have ? silu(z[v]) : 1.0f;
-                            }
-                            if (w.live && t + i < a.L) store_rows<T, V, N>(a.y, at, w.off, row, i, o);
+                        for (int v = 0; v < V; ++v) {
+                            const int j = V == 1 ? u : v;
+                            hf[v] = fmaf(f[2 * j], hf[v], f[2 * j + 1]);
+                            o[v] = i < have ? hf[v] : 0.0f;
                         }
+                        if constexpr (GATE) {
+                            float z[V];
+                            unpack<T, V>(prev_z[i], z);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) o[v] *= i < have ? silu(z[v]) : 1.0f;
+                        }
+                        if (w.live && t + i < a.L) store_rows<T, V, N>(a.y, at, w.off, row, i, o);
                     }
                 }
             }
@@ -1227,7 +1225,7 @@ size_t gated_bwd_workspace_bytes(const GatedShape& s, const GatedPlan& p, bool c
 }
 
 namespace {
-// The chain in `ws`, made ready: its words unset, and the states (gradients) that it starts from in a.h0 (a.dlast).
+// The chain in `ws`, made ready: its words unset, and the states that it starts from copied; `from` then is the copy.
 Chain start_chain(char* ws, const Layout& l, const GatedShape& s, const GatedPlan& p, const float** from,
                   hipStream_t st) {
     const int64_t rows = s.batch * s.dim, words = chain_words(s, p);
@@ -1244,11 +1242,11 @@ Chain start_chain(char* ws, const Layout& l, const GatedShape& s, const GatedPla
     *from = copy;
     return ch;
 }
-template <int MODE> void run_fwd_chain(const GaArgs& a, const Chain& ch, const GatedShape& s, hipStream_t st) {
-    dispatch(s, MODE == kOut && a.z, [&](auto T, auto decay, auto gate, auto V) {
+void run_fwd_chain(const GaArgs& a, const Chain& ch, const GatedShape& s, hipStream_t st) {
+    dispatch(s, a.z, [&](auto T, auto decay, auto gate, auto V) {
         const int64_t tiles = blocks_of(s, kWide) * int64_t(ch.tiles);
-        hipLaunchKernelGGL((fwd_chain_kernel<decltype(T), decltype(decay)::value, MODE == kOut && decltype(gate)::value,
-                                             decltype(V)::value, kWide, kNF, MODE>),
+        hipLaunchKernelGGL((fwd_chain_kernel<decltype(T), decltype(decay)::value, decltype(gate)::value,
+                                             decltype(V)::value, kWide, kNF>),
                            dim3(unsigned(tiles < kChainGroups ? tiles : kChainGroups)), dim3(kWaves * 64 + 64), 0, st, a, ch);
     });
 }
@@ -1267,7 +1265,7 @@ hipError_t launch_gated_fwd(const GatedTensors& t, const GatedShape& s, const Ga
     }
     if (p.chain) {
         const Chain ch = start_chain(static_cast<char*>(workspace), layout_of(s, p, false, false), s, p, &a.h0, stream);
-        run_fwd_chain<kOut>(a, ch, s, stream);
+        run_fwd_chain(a, ch, s, stream);
     } else {
         run_fwd<kOut>(a, s, p.segments, stream);
     }
