@@ -707,8 +707,10 @@ int selscan_groupnorm_workspace_size(const selscan_groupnorm_dims_t* dims, int32
  *                   the logarithm of the channel's smallest decay per token.
  *                   Above 0, where 1 - a^2 < 0, the state is a NaN
  *   last_state    : [B, D] fp32 output or NULL
- * dims: L < 2^27; D <= 2^20; B and B * ceil(D / 8) * segments <= 4194304 (else
- * SELSCAN_ERR_DIMS). Fully fp32 arithmetic on values that are rounded once;
+ * dims: L < 2^27; D <= 2^20; B and B * ceil(D / 8) <= 4194304, and so for the
+ * runs that are formed (segments) times B * ceil(D / 64) in bfloat16 of an even
+ * D, times B * ceil(D / 32) else (else SELSCAN_ERR_DIMS). Fully fp32 arithmetic
+ * on values that are rounded once;
  * 1 - a and sqrt(1 - a^2) are formed without cancellation, and the state that
  * passes from tile to tile of tokens is held in 64 bits. Tokens behind an
  * entry's length are not read. A NaN or an infinity reaches no token or
@@ -772,8 +774,8 @@ int selscan_gated_fwd_workspace_size(const selscan_gated_dims_t* dims,
 /*
  * selscan_gated_step — one token of the recurrence, the state updated in place:
  * state [B, D] fp32; x, g, r, z, y [B, D] of dtype; A [D] fp32, as
- * selscan_gated_fwd's. dims->seqlen is ignored. y and state must not overlap
- * any input or each other.
+ * selscan_gated_fwd's. dims->seqlen is ignored; the other bounds are
+ * selscan_gated_fwd's. y and state must not overlap any input or each other.
  */
 int selscan_gated_step(float* state, const void* x, const void* g, const void* r, const float* A,
                        const void* z, void* y, const selscan_gated_dims_t* dims, void* stream);
@@ -899,8 +901,8 @@ int selscan_addnorm(const void* x, const void* res, void* res_out, void* y, floa
  * Arguments: x [R, C] as the forward's (NULL if there is no post norm and no
  * dgate is wanted); sum [R, C] of res_dtype and dy [R, C] of dtype (NULL
  * without a pre norm); stats [R, 4]; dres_out [R, C] of res_dtype or NULL
- * (zeros); outputs dx [R, C] of dtype, dres [R, C] of res_dtype, either NULL if
- * not wanted; grads' fields fp32, each NULL if not wanted: the four of [C], and
+ * (zeros); outputs dx [R, C] of dtype, dres [R, C] of res_dtype, one of them NULL
+ * if not wanted; grads' fields fp32, each NULL if not wanted: the four of [C], and
  * dgate [gate_rows, C] (only with a gate). grads itself may be NULL. dres may be
  * dres_out itself; other outputs must not overlap inputs or each other. Sums
  * over rows in a fixed order: deterministic.

@@ -308,7 +308,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void fwd_kernel(AnArgs a) {
             statistics<K, EDGE>(a.pre, s, c, inv, a.eps, row, &m2, &r2);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                    float y[kV];
+                float y[kV];
                 float (&w)[kV] = w2[KEEP ? k : 0];
                 if constexpr (!KEEP) weights<EDGE>(t.pre_w, c[k], 1.0f, w);
 #pragma unroll

@@ -43,7 +43,8 @@ struct GaArgs {
     const double* enter;   // the states (gradients) entering the runs; null: h0 (dlast)
 };
 
-// sigmoid(v) to full relative accuracy, and sigmoid'(v).
+// sigmoid(v), and sigmoid'(v). The exponent's argument is rounded, so either is off by up to 2 |v| + 8 roundings of
+// 2^-24, relative; what fp32 has no normal number for is 0 or as fp32 has it.
 __device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw(-v * kLog2e)); }
 struct Sig { float s, slope; };
 __device__ __forceinline__ Sig sigmoid_slope(float v) {
@@ -54,7 +55,7 @@ __device__ __forceinline__ Sig sigmoid_slope(float v) {
 // A token of one channel: its decay a, e = a - 1 and its input's weight f: h = a h + f x.
 struct Token { float a, e, f; };
 
-// mix: a = 1 - sigmoid(g), f = sigmoid(g), each to full relative accuracy. (slope: sigmoid'(g))
+// mix: a = 1 - sigmoid(g), f = sigmoid(g), neither by a difference. (slope: sigmoid'(g))
 __device__ __forceinline__ Token mix_of(float g, float* slope) {
     const float t = exp2_hw(-fabsf(g) * kLog2e), w = rcp_hw(1.0f + t), m = t * w;
     const bool up = g >= 0.0f;
@@ -597,7 +598,7 @@ __global__ __launch_bounds__(256) void start_chain_kernel(Chain ch, int64_t word
 }
 
 // Eight waves compute; a ninth hands out the tiles and looks back. While it does that for a tile, the others
-// evaluate the next one and keep the tile's tokens in registers: one barrier a tile.
+// evaluate the next one; the tile's tokens wait in LDS: one barrier a tile.
 template <typename T, bool DECAY, bool GATE, int V, int CL, int N>
 __global__ __launch_bounds__(kWaves * 64 + 64, 3) void fwd_chain_kernel(GaArgs a, Chain ch) {
     using W = Place<T, V, CL, N>;
@@ -1007,8 +1008,8 @@ __global__ __launch_bounds__(kWaves * 64) void bwd_kernel(GaArgs a) {
     }
 }
 
-// The states entering the runs, from the first (against: the gradients, from the last) on, in 64 bits; in place of
-// the runs' own.
+// The states entering the runs, from the first (against: the gradients, from the last) on, in 64 bits: a thread goes
+// through a channel's runs one by one.
 __global__ __launch_bounds__(64) void carry_kernel(Stretch* runs, double* enter, const float* first, int64_t rows,
                                                    int segments, bool against) {
     const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
@@ -1196,7 +1197,10 @@ bool gated_plan(const GatedShape& s, int32_t requested, bool backward, GatedPlan
             // Chained tiles, which share out evenly what workgroups of whole sequences do not, at 1.3 of its cost (2.6 of
             // rows of 32 values of 2 bytes) and some 10 us (bf16, us, single and chained: 8 x 2048 x 64 31 and 17, 1 x
             // 2048 x 2560 33 and 24, 1 x 32771 x 2560 588 and 217, 2 x 4096 x 5120 135 and 113; but 2 x 1024 x 2560 20
-            // and 23, 2 x 4096 x 4096 66 and 85, 3 x 4096 x 5120 143 and 163, 8 x 2048 x 2049 84 and 159).
+            // and 23, 2 x 4096 x 4096 66 and 85, 3 x 4096 x 5120 143 and 163, 8 x 2048 x 2049 84 and 159). Runs, which
+            // a caller can ask for, are not weighed; a link waits for the one before, so very long sequences of one block
+            // of channels take less in runs (chained, 64 and 256 runs: 1 x 60000 x 64 100, 78, 87; 1 x 262144 x 64 401,
+            // 234, 135; but 4 x 16384 x 32 35, 40, 56).
             if (s.L > 12 * kTile && blocks * (thin(s) ? 104 : 52) < single * 256) p->chain = ceil_div(s.L, kTile);
         } else if (blocks > 0 && blocks < 96) {
             // Runs, which read what the decays hang on twice, where even narrow workgroups leave CUs idle: for one round of

@@ -1097,14 +1097,15 @@ def addnorm_bwd(x: Optional[torch.Tensor], res_out: Optional[torch.Tensor], *, d
     "none") and ``dres_out`` (the gradient into res_out; None: zeros), from the
     ``res_out`` and ``stats`` that it returned.
 
-    Returns a dict with dx, dres (``dres`` may be ``dres_out`` itself) and, with
-    ``want_dparams``, dpost_weight, dpost_bias, dpre_weight, dpre_bias [channels]
-    and dgate (like gate), all fp32, of the parameters that are given. ``x`` may
-    be None where there is neither a post norm nor a gate whose gradient is
-    wanted; with pre "none" ``res_out`` and ``dy`` must be None. ``dtype`` is
-    x's type, for dx where neither x nor dy is given to say it (None: dres_out's,
-    so a bfloat16 block on a float32 stream has to name its own); ``res_dtype``
-    the residual stream's, for dres where no tensor of it is given (None: x's).
+    Returns a dict with dx, dres (one of them at least; ``dres`` may be
+    ``dres_out`` itself) and, with ``want_dparams``, dpost_weight, dpost_bias,
+    dpre_weight, dpre_bias [channels] and dgate (like gate), all fp32, of the
+    parameters that are given. ``x`` may be None where there is neither a post
+    norm nor a gate whose gradient is wanted; with pre "none" ``res_out`` and
+    ``dy`` must be None. ``dtype`` is x's type, for dx where neither x nor dy is
+    given to say it (None: dres_out's, so a bfloat16 block on a float32 stream
+    has to name its own); ``res_dtype`` the residual stream's, for dres where no
+    tensor of it is given (None: x's).
     """
     like = next((t for t in (dy, x, res_out, dres_out) if t is not None), None)
     if like is None or like.dim() < 1:
